@@ -34,7 +34,8 @@
  *     caller word `status` (device int32, zeroed by the caller). Kernels never
  *     trap.
  *   - Index tensors are int32; T*k must be below 2^31.
- *   - dtype is MOE_F32 or MOE_BF16 for hidden, w13, w2, out (and the FFN's
+ *   - dtype is MOE_F32 or MOE_BF16 (the grouped products and the 4-bit calls
+ *     also take MOE_F16) for hidden, w13, w2, out (and the FFN's
  *     intermediate activation). Router logits, routing weights and probs are
  *     float32.
  *   - Logits must be finite. Rows of `indices` must name distinct experts.
@@ -65,6 +66,11 @@ extern "C" {
 /* dtypes */
 #define MOE_F32 0
 #define MOE_BF16 1
+#define MOE_F16 2               /* moe_grouped_gemm*, moe_mxfp4_* only */
+
+/* activations of moe_mxfp4_grouped_gemm */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU_AND_MUL 1
 
 /* device status bits */
 #define MOE_STATUS_BAD_INDEX 1  /* a routed expert index was outside [0, E); the slot was dropped */
@@ -274,6 +280,78 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
                               int norm_topk_prob, void* out, float* topk_weights_or_null,
                               int32_t* topk_indices_or_null, void* ws, size_t ws_bytes,
                               int32_t* status, void* stream);
+
+/*
+ * Product of rows grouped by expert with the expert's matrix.
+ *   y[p, n] = sum_k x[p, k] w[e, n, k]   for the rows p of expert e,
+ *             offsets[e] <= p < offsets[e + 1]
+ *   x [S, K], w [E, N, K], y [S, N], all of dtype (MOE_F32, MOE_BF16, MOE_F16;
+ *   sums in float32, one rounding to dtype).
+ *   offsets [E + 1] int32, ascending, in [0, S] (e.g. from moe_align_by_expert).
+ *   Rows of y before offsets[0] and from offsets[E] on are zero. An entry
+ *   outside [0, S] or below its predecessor sets MOE_STATUS_BAD_INDEX (groups
+ *   are cut to [0, S]; the rows concerned are then undefined).
+ *   ws / ws_bytes: at least moe_grouped_gemm_workspace_size(...) bytes (0 for
+ *   float32 and for 16-bit K % 8 == 0: then ws may be null).
+ * S, K, N may have any size >= 0 (K = 0 gives zeros). 16-bit types run on the
+ * tcgen05 tensor cores, float32 on the CUDA cores (full float32 products).
+ */
+MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E);
+MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
+                             const int32_t* offsets, void* y, void* ws, size_t ws_bytes, int32_t* status,
+                             void* stream);
+
+/*
+ * Gradients of moe_grouped_gemm for the gradient d_y [S, N] of y:
+ *   d_x[p, k]    = sum_n d_y[p, n] w[e, n, k]                 [S, K]
+ *   d_w[e, n, k] = sum over the rows p of e of d_y[p, n] x[p, k]   [E, N, K]
+ * Either output may be null (it is then not computed; w is read only for d_x,
+ * x only for d_w, and the one not read may be null). Rows that no expert owns
+ * have d_x = 0, experts without rows d_w = 0. Types, offsets and status as
+ * moe_grouped_gemm; sums in float32 in a fixed order, one rounding. No atomics
+ * on the outputs: equal calls give equal bits.
+ */
+MOE_API size_t moe_grouped_gemm_backward_workspace_size(int dtype, int S, int K, int N, int E);
+MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* d_y, int dtype, int S, int K,
+                                      int N, int E, const int32_t* offsets, void* d_x_or_null,
+                                      void* d_w_or_null, void* ws, size_t ws_bytes, int32_t* status,
+                                      void* stream);
+
+/*
+ * 4-bit microscaled values: blocks of 32 consecutive values of a row share a
+ * power-of-two scale.
+ *   s = max(floor(log2(largest magnitude of the block)) - 2, -127);
+ *   scales[r, b] = s + 127;  255 (NaN, codes 0) if the block holds inf or NaN;
+ *   code = sign << 3 | index of the nearest of {0, .5, 1, 1.5, 2, 3, 4, 6} to
+ *   |v| 2^-s (ties to the even index, above 6 to 6); element 2i of a row is the
+ *   low half of byte i of its codes, element 2i + 1 the high half.
+ *   x [T, K] of dtype, K % 32 == 0.
+ *   rows_or_null [R] int32: row r is quantised from x[rows[r]] (e.g. the
+ *   sorted_token_ids of moe_align_by_expert); an entry outside [0, T) gives a
+ *   zero row and sets MOE_STATUS_BAD_INDEX. Null: row r from x[r], R == T.
+ *   codes [R, K / 2], scales [R, K / 32] bytes out.
+ * moe_mxfp4_dequantize writes the values (code value * 2^s, rounded once to
+ * dtype: exact in float32 and bf16, and in float16 within its range).
+ */
+MOE_API int moe_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows_or_null, int R,
+                               uint8_t* codes, uint8_t* scales, int32_t* status, void* stream);
+MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype,
+                                 void* out, void* stream);
+
+/*
+ * moe_grouped_gemm on 4-bit microscaled operands (K % 32 == 0):
+ *   x_codes [S, K / 2], x_scales [S, K / 32]; w_codes [E, N, K / 2],
+ *   w_scales [E, N, K / 32]; products of the values they stand for, sums in
+ *   float32.
+ *   activation MOE_ACT_NONE: y [S, N]; MOE_ACT_SILU_AND_MUL (N even): y [S, N / 2]
+ *   = silu(columns 0 .. N/2 - 1) * (columns N/2 .. N - 1), as w13 is laid out in
+ *   moe_grouped_ffn. y is of out_dtype (any of the three), rounded once.
+ * offsets, rows without an expert and status as moe_grouped_gemm. A scale byte
+ * of 255 makes its row's (or column's) sums NaN.
+ */
+MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, int S, int K, int N, int E, const int32_t* offsets,
+                                   int activation, int out_dtype, void* y, int32_t* status, void* stream);
 
 /*
  * Expert-parallel exchange: G ranks, rank r owning the E_local = E / G

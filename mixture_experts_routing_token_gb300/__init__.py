@@ -8,12 +8,14 @@ the same entry-point names. Build the library with :func:`build`.
 process group (one GPU each).
 """
 from ._binding import (  # noqa: F401
-    MOE_BF16, MOE_F32, MOE_GROUP_TOPK_GREEDY, MOE_GROUP_TOPK_NOAUX_TC, MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT,
+    MOE_ACT_NONE, MOE_ACT_SILU_AND_MUL, MOE_BF16, MOE_F16, MOE_F32, MOE_GROUP_TOPK_GREEDY, MOE_GROUP_TOPK_NOAUX_TC, MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT,
     MoeError, SIGNATURES, LIB_PATH, MOE_ALIGN_NOALLOC_SCRATCH_INTS, lib, moe_align_by_expert,
     moe_align_by_expert_noalloc, moe_align_workspace_size,
     moe_gating_softmax_topk, moe_gating_softmax_topk_bf16, moe_group_limited_topk,
     moe_grouped_ffn_backward, moe_grouped_ffn_backward_workspace_size, moe_grouped_ffn, moe_grouped_ffn_workspace_size,
     moe_indices_to_multihot, moe_layer_forward, moe_layer_workspace_size, moe_multihot_to_indices,
+    moe_grouped_gemm, moe_grouped_gemm_backward, moe_grouped_gemm_backward_workspace_size,
+    moe_grouped_gemm_workspace_size, moe_mxfp4_dequantize, moe_mxfp4_grouped_gemm, moe_mxfp4_quantize,
     moe_gather_rows, moe_ep_receive_index, moe_ep_combine,
     profiler_enable, profiler_report, set_wait_limit_ns, version,
 )

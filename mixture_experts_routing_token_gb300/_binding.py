@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_WORKSPACE = 0, 1, 2, 3, 4
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SILU_AND_MUL = 0, 1
 MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT = 1, 2
 MOE_GROUP_TOPK_GREEDY, MOE_GROUP_TOPK_NOAUX_TC = 0, 1
 MOE_MAX_TOPK, MOE_MAX_EXPERTS = 32, 1024
@@ -43,6 +44,13 @@ SIGNATURES = {
                                       _p, _p, _sz, _p, _p]),
     "moe_layer_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "moe_layer_forward": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p, _p]),
+    "moe_grouped_gemm_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_grouped_gemm": (_i, [_p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _sz, _p, _p]),
+    "moe_grouped_gemm_backward_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_grouped_gemm_backward": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p, _p]),
+    "moe_mxfp4_quantize": (_i, [_p, _i, _i, _i, _p, _i, _p, _p, _p, _p]),
+    "moe_mxfp4_dequantize": (_i, [_p, _p, _i, _i, _i, _p, _p]),
+    "moe_mxfp4_grouped_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p]),
     "moe_gather_rows": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
     "moe_ep_receive_workspace_size": (_sz, [_i, _i]),
     "moe_ep_receive_index": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
@@ -364,6 +372,178 @@ def moe_layer_forward(hidden, router_logits, w13, w2, k, norm_topk_prob=True, ou
         int(bool(norm_topk_prob)), _ptr(out), _ptr(topk_weights), _ptr(topk_indices),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
         _stream(stream, d)))
+    return out
+
+
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+
+
+def _code(dtype):
+    try:
+        return _CODES[dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {dtype}") from None
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    _dev(status, "status", torch.int32)
+    if status.numel() < 1 or status.device != device:
+        raise ValueError("status must be an int32 word on the call's device")
+    return status.data_ptr()
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device} (got {t.device})")
+
+
+def _workspace(workspace, need, device):
+    """(address, bytes) of the caller's workspace or of a new one; nothing when none is needed. The tensor comes third."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _dev(workspace, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E) -> int:
+    return int(lib().moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E))
+
+
+def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, stream=None):
+    """Rows grouped by expert times the expert's matrix -> y [S, N].
+
+    ``x [S, K]``, ``w [E, N, K]`` (float32, bf16 or float16); ``offsets [E+1]`` int32: expert e owns the
+    rows ``offsets[e]`` to ``offsets[e+1] - 1``. Rows without an expert give zero rows."""
+    _dev(x, "x")
+    _dev(w, "w", x.dtype)
+    _dev(offsets, "offsets", torch.int32)
+    dt = _code(x.dtype)
+    if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1] or offsets.shape != (w.shape[0] + 1,):
+        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
+    S, K = x.shape
+    E, N, _ = w.shape
+    d = x.device
+    out = _out(out, (S, N), x.dtype, d, "out")
+    _on(d, w=w, offsets=offsets, out=out, workspace=workspace)
+    ws, ws_bytes, _keep = _workspace(workspace, moe_grouped_gemm_workspace_size(dt, S, K, N, E), d)
+    _check("moe_grouped_gemm", lib().moe_grouped_gemm(
+        x.data_ptr(), w.data_ptr(), dt, S, K, N, E, offsets.data_ptr(), out.data_ptr(), ws, ws_bytes,
+        _status_ptr(status, d), _stream(stream, d)))
+    return out
+
+
+def moe_grouped_gemm_backward_workspace_size(dtype_code, S, K, N, E) -> int:
+    return int(lib().moe_grouped_gemm_backward_workspace_size(dtype_code, S, K, N, E))
+
+
+def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=None, status=None, stream=None,
+                              want_d_x=True, want_d_w=True):
+    """Gradients of :func:`moe_grouped_gemm` for ``d_y [S, N]`` -> (d_x [S, K], d_w [E, N, K]) in x's dtype.
+
+    One that is not wanted is None. Experts without rows get a zero ``d_w``, rows without an expert a zero ``d_x``."""
+    _dev(x, "x")
+    _dev(w, "w", x.dtype)
+    _dev(d_y, "d_y", x.dtype)
+    _dev(offsets, "offsets", torch.int32)
+    dt = _code(x.dtype)
+    if (x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1] or offsets.shape != (w.shape[0] + 1,)
+            or d_y.shape != (x.shape[0], w.shape[1])):
+        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
+    S, K = x.shape
+    E, N, _ = w.shape
+    d = x.device
+    d_x = _out(d_x, (S, K), x.dtype, d, "d_x") if want_d_x else None
+    d_w = _out(d_w, (E, N, K), x.dtype, d, "d_w") if want_d_w else None
+    _on(d, w=w, offsets=offsets, d_y=d_y, d_x=d_x, d_w=d_w, workspace=workspace)
+    ws, ws_bytes, _keep = _workspace(workspace, moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d)
+    _check("moe_grouped_gemm_backward", lib().moe_grouped_gemm_backward(
+        x.data_ptr(), w.data_ptr(), d_y.data_ptr(), dt, S, K, N, E, offsets.data_ptr(), _ptr(d_x), _ptr(d_w),
+        ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
+    return d_x, d_w
+
+
+def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, status=None, stream=None):
+    """4-bit microscaled rows of ``x [T, K]`` (K % 32 == 0) -> (codes [R, K/2] uint8, scales [R, K/32] uint8).
+
+    Blocks of 32 values share the power of two ``2^(scale - 127)``; two codes to a byte, the first one low.
+    ``rows [R]`` int32 picks the rows (row r from ``x[rows[r]]``); without it R is T. ``x`` may have more
+    than two dimensions when no rows are given: they are kept."""
+    _dev(x, "x")
+    dt = _code(x.dtype)
+    if x.dim() < 2 or x.shape[-1] % 32:
+        raise ValueError("x must be [T, K] (or [..., K] without rows) with K a multiple of 32")
+    K = x.shape[-1]
+    T = x.numel() // K if K else 0
+    d = x.device
+    if rows is None:
+        lead = tuple(x.shape[:-1])
+        R = T
+    else:
+        _dev(rows, "rows", torch.int32)
+        if x.dim() != 2 or rows.dim() != 1:
+            raise ValueError("rows must be [R] and x [T, K]")
+        R = rows.shape[0]
+        lead = (R,)
+    codes = _out(codes, lead + (K // 2,), torch.uint8, d, "codes")
+    scales = _out(scales, lead + (K // 32,), torch.uint8, d, "scales")
+    _on(d, rows=rows, codes=codes, scales=scales)
+    _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(
+        x.data_ptr(), dt, T, K, _ptr(rows), R, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, d),
+        _stream(stream, d)))
+    return codes, scales
+
+
+def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that ``codes [..., K/2]`` and ``scales [..., K/32]`` stand for -> [..., K] of ``dtype``."""
+    _dev(codes, "codes", torch.uint8)
+    _dev(scales, "scales", torch.uint8)
+    dt = _code(dtype)
+    K = 2 * codes.shape[-1]
+    if K % 32 or tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // 32,):
+        raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32] with K a multiple of 32")
+    d = codes.device
+    out = _out(out, tuple(codes.shape[:-1]) + (K,), dtype, d, "out")
+    _on(d, scales=scales, out=out)
+    _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(
+        codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // K if K else 0, K, dt, out.data_ptr(),
+        _stream(stream, d)))
+    return out
+
+
+def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activation=None,
+                           out_dtype=torch.bfloat16, out=None, status=None, stream=None):
+    """:func:`moe_grouped_gemm` on 4-bit microscaled operands -> y [S, N] of ``out_dtype``.
+
+    ``x_codes [S, K/2]``, ``x_scales [S, K/32]``, ``w_codes [E, N, K/2]``, ``w_scales [E, N, K/32]`` from
+    :func:`moe_mxfp4_quantize`. ``activation="silu_and_mul"`` returns [S, N/2]: silu of the first half of
+    the columns times the second half."""
+    for t, name in ((x_codes, "x_codes"), (x_scales, "x_scales"), (w_codes, "w_codes"), (w_scales, "w_scales")):
+        _dev(t, name, torch.uint8)
+    _dev(offsets, "offsets", torch.int32)
+    dt = _code(out_dtype)
+    if activation not in (None, "silu_and_mul"):
+        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+    if x_codes.dim() != 2 or w_codes.dim() != 3 or w_codes.shape[2] != x_codes.shape[1]:
+        raise ValueError("shapes must be x_codes [S, K / 2], w_codes [E, N, K / 2]")
+    S, K = x_codes.shape[0], 2 * x_codes.shape[1]
+    E, N, _ = w_codes.shape
+    if (K % 32 or tuple(x_scales.shape) != (S, K // 32) or tuple(w_scales.shape) != (E, N, K // 32)
+            or offsets.shape != (E + 1,)):
+        raise ValueError("shapes must be x_scales [S, K / 32], w_scales [E, N, K / 32], offsets [E + 1], K a multiple of 32")
+    act = MOE_ACT_NONE if activation is None else MOE_ACT_SILU_AND_MUL
+    if act and N % 2:
+        raise ValueError("silu_and_mul needs an even N")
+    d = x_codes.device
+    out = _out(out, (S, N // 2 if act else N), out_dtype, d, "out")
+    _on(d, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, out=out)
+    _check("moe_mxfp4_grouped_gemm", lib().moe_mxfp4_grouped_gemm(
+        x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), S, K, N, E,
+        offsets.data_ptr(), act, dt, out.data_ptr(), _status_ptr(status, d), _stream(stream, d)))
     return out
 
 

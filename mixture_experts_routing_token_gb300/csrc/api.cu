@@ -600,6 +600,158 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
                  norm_topk_prob != 0, small ? fw.sync : nullptr);
 }
 
+namespace moe {
+namespace {
+
+int check_grouped_dims(int S, int K, int N, int E) {
+  REQUIRE(S >= 0 && K >= 0 && N >= 0, "S, K and N must be >= 0 (got S=%d, K=%d, N=%d)", S, K, N);
+  REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "E must be in [1, %d] (got %d)", MOE_MAX_EXPERTS, E);
+  // TMA coordinates and the tile numbering are 32-bit: the smallest tiles are 64 x 64
+  const long nt = ((long)N + 63) / 64, kt = ((long)K + 63) / 64, mt = ((long)S + 63) / 64 + E;
+  const long most = (1L << 31) - 1;
+  REQUIRE((long)E * N <= most && nt * mt <= most && kt * mt <= most && (long)E * nt * kt <= most,
+          "S=%d, K=%d, N=%d, E=%d are too large together", S, K, N, E);
+  REQUIRE(K <= most - 1024 && N <= most - 1024 && S <= most - 1024, "S, K and N must be below 2^31 - 1024");
+  return MOE_OK;
+}
+
+int check_any_dtype(int dtype) {
+  REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16, "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)",
+          dtype);
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E) {
+  if (S < 0 || K < 0 || N < 0 || E < 1) return 0;
+  return 0;
+}
+
+MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
+                             const int32_t* offsets, void* y, void* ws, size_t ws_bytes, int32_t* status,
+                             void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  if ((rc = check_grouped_dims(S, K, N, E))) return rc;
+  if ((rc = check_tensor(x, (long)S * K, "x"))) return rc;
+  if ((rc = check_tensor(w, (long)E * N * K, "w"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if ((rc = check_tensor(y, (long)S * N, "y"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_grouped_gemm_workspace_size(dtype, S, K, N, E)))) return rc;
+  if (S == 0 || N == 0) return MOE_OK;
+  GroupedArgs a{};
+  a.x = x;
+  a.w = w;
+  a.y = y;
+  a.dtype = dtype;
+  a.S = S;
+  a.K = K;
+  a.N = N;
+  a.E = E;
+  a.offsets = offsets;
+  a.ws = ws;
+  a.status = status;
+  return launch_grouped_simt(a, (cudaStream_t)stream);
+}
+
+MOE_API size_t moe_grouped_gemm_backward_workspace_size(int dtype, int S, int K, int N, int E) {
+  if (S < 0 || K < 0 || N < 0 || E < 1) return 0;
+  return 0;
+}
+
+MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* d_y, int dtype, int S, int K,
+                                      int N, int E, const int32_t* offsets, void* d_x_or_null,
+                                      void* d_w_or_null, void* ws, size_t ws_bytes, int32_t* status,
+                                      void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  if ((rc = check_grouped_dims(S, K, N, E))) return rc;
+  if (d_w_or_null && (rc = check_tensor(x, (long)S * K, "x"))) return rc;
+  if (d_x_or_null && (rc = check_tensor(w, (long)E * N * K, "w"))) return rc;
+  if ((rc = check_tensor(d_y, (long)S * N, "d_y"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if (d_x_or_null && (rc = check_tensor(d_x_or_null, (long)S * K, "d_x"))) return rc;
+  if (d_w_or_null && (rc = check_tensor(d_w_or_null, (long)E * N * K, "d_w"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_grouped_gemm_backward_workspace_size(dtype, S, K, N, E)))) return rc;
+  GroupedArgs a{};
+  a.x = x;
+  a.w = w;
+  a.d_y = d_y;
+  a.d_x = d_x_or_null;
+  a.d_w = d_w_or_null;
+  a.dtype = dtype;
+  a.S = S;
+  a.K = K;
+  a.N = N;
+  a.E = E;
+  a.offsets = offsets;
+  a.ws = ws;
+  a.status = status;
+  if (a.d_x && S > 0 && K > 0 && (rc = launch_grouped_simt_dx(a, (cudaStream_t)stream))) return rc;
+  if (a.d_w && N > 0 && K > 0 && (rc = launch_grouped_simt_dw(a, (cudaStream_t)stream))) return rc;
+  return MOE_OK;
+}
+
+MOE_API int moe_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows_or_null, int R,
+                               uint8_t* codes, uint8_t* scales, int32_t* status, void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  REQUIRE(T >= 0 && R >= 0, "T and R must be >= 0 (got T=%d, R=%d)", T, R);
+  REQUIRE(K >= 0 && K % 32 == 0, "K must be a multiple of 32 (got %d)", K);
+  REQUIRE(rows_or_null != nullptr || R == T, "R must equal T when no rows are given (got R=%d, T=%d)", R, T);
+  if ((rc = check_tensor(x, (long)T * K, "x"))) return rc;
+  if (rows_or_null && (rc = check_tensor(rows_or_null, R, "rows"))) return rc;
+  if ((rc = check_tensor(codes, (long)R * K, "codes"))) return rc;
+  if ((rc = check_tensor(scales, (long)R * K, "scales"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if (R == 0 || K == 0) return MOE_OK;
+  return launch_mxfp4_quantize(x, dtype, T, K, rows_or_null, R, codes, scales, status, (cudaStream_t)stream);
+}
+
+MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype,
+                                 void* out, void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  REQUIRE(R >= 0, "R must be >= 0 (got %d)", R);
+  REQUIRE(K >= 0 && K % 32 == 0, "K must be a multiple of 32 (got %d)", K);
+  if ((rc = check_tensor(codes, (long)R * K, "codes"))) return rc;
+  if ((rc = check_tensor(scales, (long)R * K, "scales"))) return rc;
+  if ((rc = check_tensor(out, (long)R * K, "out"))) return rc;
+  if (R == 0 || K == 0) return MOE_OK;
+  return launch_mxfp4_dequantize(codes, scales, R, K, dtype, out, (cudaStream_t)stream);
+}
+
+MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, int S, int K, int N, int E, const int32_t* offsets,
+                                   int activation, int out_dtype, void* y, int32_t* status, void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(out_dtype))) return rc;
+  if ((rc = check_grouped_dims(S, K, N, E))) return rc;
+  REQUIRE(K % 32 == 0, "K must be a multiple of 32 (got %d)", K);
+  REQUIRE(activation == MOE_ACT_NONE || activation == MOE_ACT_SILU_AND_MUL, "unknown activation %d", activation);
+  REQUIRE(activation == MOE_ACT_NONE || N % 2 == 0, "silu_and_mul needs an even N (got %d)", N);
+  if ((rc = check_tensor(x_codes, (long)S * K, "x_codes"))) return rc;
+  if ((rc = check_tensor(x_scales, (long)S * K, "x_scales"))) return rc;
+  if ((rc = check_tensor(w_codes, (long)E * N * K, "w_codes"))) return rc;
+  if ((rc = check_tensor(w_scales, (long)E * N * K, "w_scales"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if ((rc = check_tensor(y, (long)S * N, "y"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if (S == 0 || N == 0) return MOE_OK;
+  Mxfp4Args a{x_codes, x_scales, w_codes, w_scales, S, K, N, E, offsets, activation == MOE_ACT_SILU_AND_MUL,
+              out_dtype, y, status};
+  return launch_mxfp4_grouped(a, (cudaStream_t)stream);
+}
+
 MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids, const int32_t* offsets,
                             int dtype, int T, int H, int E, int k, void* x_sorted, void* stream) {
   g_err[0] = 0;

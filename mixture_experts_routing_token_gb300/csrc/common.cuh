@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 #include <stddef.h>
 
@@ -210,6 +211,42 @@ int launch_zero_dropped(const int32_t* offsets, int E, long S, int H, void* stag
 int launch_combine(const void* staging, int staging_bf16, int T, int k, int H, int dtype, void* out,
                    cudaStream_t s);
 
+// Products grouped by expert (grouped_*.cu): x [S, K], w [E, N, K], y and d_y [S, N], d_x as x, d_w as w.
+struct GroupedArgs {
+  const void* x;
+  const void* w;
+  const void* d_y;
+  void* y;
+  void* d_x;
+  void* d_w;
+  int dtype, S, K, N, E;
+  const int32_t* offsets;
+  void* ws;
+  int32_t* status;
+};
+int launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
+int launch_grouped_simt_dx(const GroupedArgs& a, cudaStream_t s);
+int launch_grouped_simt_dw(const GroupedArgs& a, cudaStream_t s);
+
+// 4-bit microscaled values (mxfp4.cu): codes [rows, K / 2], scales [rows, K / 32].
+int launch_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows, int R, uint8_t* codes,
+                          uint8_t* scales, int32_t* status, cudaStream_t s);
+int launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype, void* out,
+                            cudaStream_t s);
+struct Mxfp4Args {
+  const uint8_t* x;
+  const uint8_t* x_scales;
+  const uint8_t* w;
+  const uint8_t* w_scales;
+  int S, K, N, E;
+  const int32_t* offsets;
+  int silu;          // y = silu(gate half) * up half: [S, N / 2]
+  int out_dtype;
+  void* y;
+  int32_t* status;
+};
+int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s);
+
 // Launch with programmatic stream serialization (PDL): the kernel may start while
 // the previous kernel on the stream is still running; it must execute
 // pdl_wait() before touching anything that kernel writes, and every kernel
@@ -262,6 +299,7 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
 template <class T>
 __device__ __forceinline__ T from_float(float x);
@@ -270,6 +308,10 @@ __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) {
+  return __float2half_rn(x);
 }
 
 // silu(z) = z / (1 + e^-z); e^-z overflows to +inf for very negative z, giving -0.

@@ -615,6 +615,11 @@ int check_grouped_dims(int S, int K, int N, int E) {
   return MOE_OK;
 }
 
+int zero_out(void* p, size_t bytes, cudaStream_t s) {
+  const cudaError_t e = bytes ? cudaMemsetAsync(p, 0, bytes, s) : cudaSuccess;
+  return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "zeroing an output: %s", cudaGetErrorString(e));
+}
+
 int check_any_dtype(int dtype) {
   REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16, "dtype must be MOE_F32, MOE_BF16 or MOE_F16 (got %d)",
           dtype);
@@ -625,8 +630,8 @@ int check_any_dtype(int dtype) {
 }  // namespace moe
 
 MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E) {
-  if (S < 0 || K < 0 || N < 0 || E < 1) return 0;
-  return 0;
+  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
+  return grouped_tc_workspace(S, K, N, E, true);
 }
 
 MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
@@ -643,6 +648,7 @@ MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int
   if (status && (rc = check_tensor(status, 1, "status"))) return rc;
   if ((rc = check_ws(ws, ws_bytes, moe_grouped_gemm_workspace_size(dtype, S, K, N, E)))) return rc;
   if (S == 0 || N == 0) return MOE_OK;
+  if (K == 0) return zero_out(y, (size_t)S * N * dsize(dtype), (cudaStream_t)stream);
   GroupedArgs a{};
   a.x = x;
   a.w = w;
@@ -655,12 +661,12 @@ MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int
   a.offsets = offsets;
   a.ws = ws;
   a.status = status;
-  return launch_grouped_simt(a, (cudaStream_t)stream);
+  return dtype == MOE_F32 ? launch_grouped_simt(a, (cudaStream_t)stream) : launch_grouped_tc(a, (cudaStream_t)stream);
 }
 
 MOE_API size_t moe_grouped_gemm_backward_workspace_size(int dtype, int S, int K, int N, int E) {
-  if (S < 0 || K < 0 || N < 0 || E < 1) return 0;
-  return 0;
+  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
+  return grouped_tc_workspace(S, K, N, E, false);
 }
 
 MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* d_y, int dtype, int S, int K,
@@ -693,8 +699,13 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
   a.offsets = offsets;
   a.ws = ws;
   a.status = status;
-  if (a.d_x && S > 0 && K > 0 && (rc = launch_grouped_simt_dx(a, (cudaStream_t)stream))) return rc;
-  if (a.d_w && N > 0 && K > 0 && (rc = launch_grouped_simt_dw(a, (cudaStream_t)stream))) return rc;
+  if (K == 0) return MOE_OK;
+  if (N == 0) return d_x_or_null ? zero_out(d_x_or_null, (size_t)S * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
+  if (S == 0)
+    return d_w_or_null ? zero_out(d_w_or_null, (size_t)E * N * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
+  if (dtype != MOE_F32) return launch_grouped_tc_backward(a, (cudaStream_t)stream);
+  if (a.d_x && (rc = launch_grouped_simt_dx(a, (cudaStream_t)stream))) return rc;
+  if (a.d_w && (rc = launch_grouped_simt_dw(a, (cudaStream_t)stream))) return rc;
   return MOE_OK;
 }
 
@@ -747,6 +758,8 @@ MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scal
   if ((rc = check_tensor(y, (long)S * N, "y"))) return rc;
   if (status && (rc = check_tensor(status, 1, "status"))) return rc;
   if (S == 0 || N == 0) return MOE_OK;
+  if (K == 0)
+    return zero_out(y, (size_t)S * (activation == MOE_ACT_NONE ? N : N / 2) * dsize(out_dtype), (cudaStream_t)stream);
   Mxfp4Args a{x_codes, x_scales, w_codes, w_scales, S, K, N, E, offsets, activation == MOE_ACT_SILU_AND_MUL,
               out_dtype, y, status};
   return launch_mxfp4_grouped(a, (cudaStream_t)stream);

@@ -137,6 +137,10 @@ int make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
 // (cols * elem_bytes a multiple of 16, base 16-byte aligned).
 int make_tmap_rows128(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, int elem_bytes,
                       uint32_t box_rows);
+// Row-major [mats, rows, cols] of 1- or 2-byte elements; box = box_rows rows x box_cols columns (128
+// bytes) of one matrix, 128-byte swizzle. What lies past a matrix's rows or columns reads as zero.
+int make_tmap_3d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols, uint64_t rows, uint64_t mats,
+                 uint32_t box_cols, uint32_t box_rows);
 // x_sorted[p] = hidden[sorted_ids[p]] for p < offsets[E] (rows of row_bytes, a multiple of 16).
 int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int row_bytes,
                        void* xs, int32_t* status, cudaStream_t s);
@@ -227,6 +231,11 @@ struct GroupedArgs {
 int launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
 int launch_grouped_simt_dx(const GroupedArgs& a, cudaStream_t s);
 int launch_grouped_simt_dw(const GroupedArgs& a, cudaStream_t s);
+// bf16 / float16 (tensor cores); the workspace holds padded copies of operands whose rows are not a
+// multiple of 16 bytes.
+size_t grouped_tc_workspace(int S, int K, int N, int E, bool fwd);
+int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);
+int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s);
 
 // 4-bit microscaled values (mxfp4.cu): codes [rows, K / 2], scales [rows, K / 32].
 int launch_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows, int R, uint8_t* codes,

@@ -69,5 +69,59 @@ __device__ __forceinline__ void zero_unowned(T* out, const int32_t* offsets, int
   for (long j = (long)last * cols + i; j < (long)S * cols; j += n) out[j] = from_float<T>(0.0f);
 }
 
+// Two values of a 16-bit type in one word.
+template <class T>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// How rows of `cols` values are stored: 2 = 32-byte sectors, 1 = 16 bytes, 0 = single values.
+inline int store_width(const void* out, long cols, int bytes) {
+  if (cols * bytes % 32 == 0 && aligned(out, 32)) return 2;
+  return cols * bytes % 16 == 0 && aligned(out, 16) ? 1 : 0;
+}
+
+// 32 columns of one row from column c on (of `cols`): float32 sums (as bits), rounded once.
+template <class T>
+__device__ __forceinline__ void store32(T* row, int c, int cols, int vec, const uint32_t (&y)[32]) {
+  if (vec > 0 && c + 32 <= cols) {
+    constexpr int W = sizeof(T) == 4 ? 32 : 16;
+    uint32_t q[W];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) q[i] = y[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) q[i] = pack_pair<T>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+    }
+    uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
+    if (vec == 2) {
+#pragma unroll
+      for (int i = 0; i < W / 8; ++i) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = q[8 * i + j];
+        st_v8(p + 8 * i, v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < cols) row[c + i] = from_float<T>(__uint_as_float(y[i]));
+  }
+}
+
 }  // namespace grouped
 }  // namespace moe

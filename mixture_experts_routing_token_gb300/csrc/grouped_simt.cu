@@ -1,15 +1,13 @@
-// Products grouped by expert on the CUDA cores: every type, size and alignment.
+// Products grouped by expert in float32, on the CUDA cores: every size and alignment.
 //
 //   ROWS   y[p, n]    = sum_k x[p, k] w[e, n, k]     (rows p of expert e)
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
 //   GRADW  d_w[e, n, k] = sum over p of e of d_y[p, n] x[p, k]
 //
 // One CTA computes 64 x 64 outputs of one expert; 16 steps of the reduction at a time
-// go through shared memory (float32), each thread keeps 4 x 4 sums in registers.
+// go through shared memory, each thread keeps 4 x 4 sums in registers.
 // Products and sums are float32 fused multiply-adds in ascending order of the
 // reduction index, so results do not depend on the launch.
-#include <cuda_fp16.h>
-
 #include "grouped.cuh"
 
 namespace moe {
@@ -20,15 +18,15 @@ constexpr int TM = 64, TN = 64, TK = 16, TT = 256;
 enum { ROWS = 0, GRADX = 1, GRADW = 2 };
 
 struct SimtParams {
-  const void* a;        // x (ROWS), d_y (GRADX, GRADW)
-  const void* b;        // w (ROWS, GRADX), x (GRADW)
-  void* out;
+  const float* a;       // x (ROWS), d_y (GRADX, GRADW)
+  const float* b;       // w (ROWS, GRADX), x (GRADW)
+  float* out;
   const int32_t* offsets;
   int S, K, N, E;
   int32_t* status;
 };
 
-template <int MODE, class T>
+template <int MODE>
 __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   __shared__ float sa[TK][TM + 4], sb[TK][TN + 4];
   __shared__ int start[MOE_MAX_EXPERTS + 1], bad;
@@ -41,9 +39,8 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
                        [&](int rows) { return MODE == GRADW ? MT * NT : (rows + TM - 1) / TM * NT; }, start, &bad);
   __syncthreads();
   if (bad && blockIdx.x == 0 && tid == 0 && P.status) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
-  const T* A = static_cast<const T*>(P.a);
-  const T* B = static_cast<const T*>(P.b);
-  T* out = static_cast<T*>(P.out);
+  const float *A = P.a, *B = P.b;
+  float* out = P.out;
   const int tx = tid & 15, ty = tid >> 4;
   for (int t = blockIdx.x; t < start[P.E]; t += gridDim.x) {
     const int e = grouped::find(start, P.E, t);
@@ -59,7 +56,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
         float v = 0.0f;
         if (m0 + m < mcount && r0 + r < red) {
           const long row = MODE == GRADW ? g.lo + r0 + r : g.lo + m0 + m;
-          v = to_float(A[MODE == ROWS ? row * P.K + r0 + r : row * P.N + (MODE == GRADW ? m0 + m : r0 + r)]);
+          v = A[MODE == ROWS ? row * P.K + r0 + r : row * P.N + (MODE == GRADW ? m0 + m : r0 + r)];
         }
         sa[r][m] = v;
       }
@@ -68,7 +65,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
         float v = 0.0f;
         if (n0 + n < cols && r0 + r < red) {
           const long row = MODE == ROWS ? (long)e * P.N + n0 + n : MODE == GRADX ? (long)e * P.N + r0 + r : g.lo + r0 + r;
-          v = to_float(B[row * P.K + (MODE == ROWS ? r0 + r : n0 + n)]);
+          v = B[row * P.K + (MODE == ROWS ? r0 + r : n0 + n)];
         }
         sb[r][n] = v;
       }
@@ -93,7 +90,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = n0 + tx * 4 + j;
-        if (n < cols) out[row * cols + n] = from_float<T>(acc[i][j]);
+        if (n < cols) out[row * cols + n] = acc[i][j];
       }
     }
   }
@@ -101,37 +98,33 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
     grouped::zero_unowned(out, P.offsets, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
 }
 
-template <int MODE, class T>
+template <int MODE>
 int launch(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
   const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt : ((long)(p.S + TM - 1) / TM + p.E) * nt;
   const long most = (long)num_sms() * 8;
   ProfScope ps(name, s);
-  grouped_simt_kernel<MODE, T><<<(unsigned)(tiles < most ? tiles : most), TT, 0, s>>>(p);
+  grouped_simt_kernel<MODE><<<(unsigned)(tiles < most ? tiles : most), TT, 0, s>>>(p);
   return check_launch(name);
 }
 
-template <int MODE>
-int by_type(int dtype, const SimtParams& p, cudaStream_t s, const char* name) {
-  if (dtype == MOE_F32) return launch<MODE, float>(p, s, name);
-  if (dtype == MOE_BF16) return launch<MODE, __nv_bfloat16>(p, s, name);
-  return launch<MODE, __half>(p, s, name);
+SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out) {
+  return SimtParams{static_cast<const float*>(left), static_cast<const float*>(right), static_cast<float*>(out),
+                    a.offsets, a.S, a.K, a.N, a.E, a.status};
 }
 
 }  // namespace
 
 int launch_grouped_simt(const GroupedArgs& a, cudaStream_t s) {
-  return by_type<ROWS>(a.dtype, SimtParams{a.x, a.w, a.y, a.offsets, a.S, a.K, a.N, a.E, a.status}, s, "grouped_gemm");
+  return launch<ROWS>(params(a, a.x, a.w, a.y), s, "grouped_gemm");
 }
 
 int launch_grouped_simt_dx(const GroupedArgs& a, cudaStream_t s) {
-  return by_type<GRADX>(a.dtype, SimtParams{a.d_y, a.w, a.d_x, a.offsets, a.S, a.K, a.N, a.E, a.status}, s,
-                        "grouped_gemm_dx");
+  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x), s, "grouped_gemm_dx");
 }
 
 int launch_grouped_simt_dw(const GroupedArgs& a, cudaStream_t s) {
-  return by_type<GRADW>(a.dtype, SimtParams{a.d_y, a.x, a.d_w, a.offsets, a.S, a.K, a.N, a.E, a.status}, s,
-                        "grouped_gemm_dw");
+  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w), s, "grouped_gemm_dw");
 }
 
 }  // namespace moe

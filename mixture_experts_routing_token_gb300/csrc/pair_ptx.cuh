@@ -87,5 +87,31 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_major(int M, int N, int a_
   return ptx::idesc_bf16_f32(M, N) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
 }
 
+// 3-D form of tma_load_2d_pair (x = inner coordinate, y = row, z = matrix).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                                 uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(leader_bar)
+      : "memory");
+}
+
+// Arrive on an mbarrier of a CTA of the cluster after this thread's own shared-memory
+// writes, which the other CTA's threads may then rely on.
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Make this thread's shared-memory writes visible to TMA and tcgen05 (the async proxy).
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// After an mbarrier wait that arrivals of the other CTA completed.
+__device__ __forceinline__ void fence_acquire_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 }  // namespace pair
 }  // namespace moe

@@ -89,23 +89,23 @@ inline int store_width(const void* out, long cols, int bytes) {
   return cols * bytes % 16 == 0 && aligned(out, 16) ? 1 : 0;
 }
 
-// 32 columns of one row from column c on (of `cols`): float32 sums (as bits), rounded once.
-template <class T>
-__device__ __forceinline__ void store32(T* row, int c, int cols, int vec, const uint32_t (&y)[32]) {
-  if (vec > 0 && c + 32 <= cols) {
-    constexpr int W = sizeof(T) == 4 ? 32 : 16;
-    uint32_t q[W];
+// W (16 or 32) columns of one row from column c on (of `cols`): float32 sums (as bits), rounded once.
+template <class T, int W>
+__device__ __forceinline__ void store_cols(T* row, int c, int cols, int vec, const uint32_t (&y)[W]) {
+  if (vec > 0 && c + W <= cols) {
+    constexpr int Q = W * (int)sizeof(T) / 4;
+    uint32_t q[Q];
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) q[i] = y[i];
+      for (int i = 0; i < Q; ++i) q[i] = y[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) q[i] = pack_pair<T>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+      for (int i = 0; i < Q; ++i) q[i] = pack_pair<T>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
     }
     uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
     if (vec == 2) {
 #pragma unroll
-      for (int i = 0; i < W / 8; ++i) {
+      for (int i = 0; i < Q / 8; ++i) {
         uint32_t v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = q[8 * i + j];
@@ -113,12 +113,12 @@ __device__ __forceinline__ void store32(T* row, int c, int cols, int vec, const 
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i)
+      for (int i = 0; i < Q / 4; ++i)
         reinterpret_cast<uint4*>(p)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < W; ++i)
       if (c + i < cols) row[c + i] = from_float<T>(__uint_as_float(y[i]));
   }
 }

@@ -255,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       if (ti.steps == 0) {
         uint32_t z[32] = {};
         if (mine)
-          for (int c = ti.n * BN; c < min(P.C, (ti.n + 1) * BN); c += 32) grouped::store32(dst, c, P.C, P.vec, z);
+          for (int c = ti.n * BN; c < min(P.C, (ti.n + 1) * BN); c += 32) grouped::store_cols(dst, c, P.C, P.vec, z);
         continue;
       }
       if (!ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns)) break;
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c0 = ti.n * BN + (c + h) * 32;
-          if (mine && c0 < P.C) grouped::store32(dst, c0, P.C, P.vec, y[h]);
+          if (mine && c0 < P.C) grouped::store_cols(dst, c0, P.C, P.vec, y[h]);
         }
       }
       ptx::tc_fence_before();

@@ -1,0 +1,126 @@
+// Inline-PTX helpers of the block-scaled 4-bit products: the instruction descriptor and
+// MMA of kind::mxf4 (both operands e2m1, one power-of-two scale per 32 values) and the
+// copy of scales from shared memory to tensor memory. Written from the PTX ISA
+// descriptions of these instructions.
+//
+// Scales in tensor memory: 128 rows x 4 scales (K = 128) take 4 columns; lane l, column c
+// holds the four bytes of row 32 c + l, in every lane quarter alike. In shared memory that
+// is 512 bytes, 16 per lane: row r's four bytes at (r % 32) * 16 + (r / 32) * 4; one
+// tcgen05.cp (32 lanes x 128 bits, to all four quarters) moves them. An MMA covers K = 64,
+// two scales per row: the instruction descriptor says which two of the four bytes.
+#pragma once
+#include "common.cuh"
+#include "pair_ptx.cuh"
+
+namespace moe {
+namespace mx {
+
+constexpr uint32_t SF_ATOM = 512;    // bytes of 128 rows x 4 scales
+
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return (1u << 7)                         // A: e2m1
+         | (1u << 10)                      // B: e2m1
+         | ((uint32_t)(N >> 3) << 17)      // N / 8
+         | (1u << 23)                      // scales: powers of two (ue8m0)
+         | ((uint32_t)(M >> 4) << 24);     // M / 16
+}
+// Which of a row's four scale bytes: the pair starting at byte `sf` (0 or 2), for A and B.
+__host__ __device__ constexpr uint32_t idesc_scales(int sf) { return ((uint32_t)sf << 4) | ((uint32_t)sf << 29); }
+
+// Descriptor of a 512-byte scale atom: no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+template <int CTAS>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CTAS == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= (A * scales) (B * scales)^T over K = 64.
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                    uint32_t accumulate) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// The scales of 4 rows x CHUNK steps of K = 256 (8 bytes per row and step) on their way from
+// global to shared memory: lane l holds rows l, l + 32, l + 64, l + 96 of a 128-row block.
+constexpr int CHUNK = 4;
+
+struct ScaleRegs {
+  uint32_t w[4][2 * CHUNK];
+};
+
+// Scale bytes [8 step, 8 step + 32) of four rows; those at or past `count` read as 0.
+__device__ __forceinline__ void load_scales(ScaleRegs& v, const uint8_t* const (&row)[4], int step, int count, int vec) {
+  const int b0 = step * 8;
+  if (vec == 16) {              // rows a multiple of 16 bytes: two 16-byte loads
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (b0 + h * 16 < count) q = __ldg(reinterpret_cast<const uint4*>(row[i] + b0 + h * 16));
+        v.w[i][4 * h] = q.x;
+        v.w[i][4 * h + 1] = q.y;
+        v.w[i][4 * h + 2] = q.z;
+        v.w[i][4 * h + 3] = q.w;
+      }
+  } else if (vec == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * CHUNK; ++j)
+        v.w[i][j] = b0 + j * 4 < count ? __ldg(reinterpret_cast<const uint32_t*>(row[i] + b0 + j * 4)) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * CHUNK; ++j) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b0 + j * 4 + b < count) x |= (uint32_t)__ldg(row[i] + b0 + j * 4 + b) << (8 * b);
+        v.w[i][j] = x;
+      }
+  }
+}
+
+// Step d of the chunk: two atoms (K = 128 each) `atom_stride` bytes apart.
+__device__ __forceinline__ void store_scales(const ScaleRegs& v, int d, uint32_t dst, uint32_t atom_stride, int lane) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * atom_stride + lane * 16),
+                 "r"(v.w[0][2 * d + j]), "r"(v.w[1][2 * d + j]), "r"(v.w[2][2 * d + j]), "r"(v.w[3][2 * d + j])
+                 : "memory");
+}
+
+inline int scale_vec(const void* p, int count) {
+  return count % 16 == 0 && aligned(p, 16) ? 16 : count % 4 == 0 && aligned(p, 4) ? 4 : 1;
+}
+
+}  // namespace mx
+}  // namespace moe

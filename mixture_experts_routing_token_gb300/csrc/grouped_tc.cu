@@ -220,7 +220,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
             ok = false;
             break;
           }
-          if (MODE == GRADW && kb == ti.steps - 1) fence_acquire_cluster();
           ptx::tc_fence_after();
           const uint32_t a0 = sA(stage), b0 = sB(stage);
 #pragma unroll
@@ -302,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) arrive_remote_release(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
+      if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
     }
   }
 

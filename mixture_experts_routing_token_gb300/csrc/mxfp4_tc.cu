@@ -188,7 +188,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             ok = false;
             break;
           }
-          fence_acquire_cluster();    // the scales of both SMs were written by their own warps
           ptx::tc_fence_after();
           const uint32_t a0 = st(stage), b0 = a0 + A_BYTES, sa = a0 + SFA_OFF, sb = a0 + SFB_OFF;
           // copies and MMAs of one thread execute in the order of issue
@@ -309,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mx::store_scales(cur, d, st(stage) + off, mx::SF_ATOM, lane);
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) arrive_remote_release(map_to_rank(ptx::smem_u32(&full_bar[stage]), 0));
+            if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[stage]), 0));
             if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
           }
         }

@@ -97,20 +97,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Arrive on an mbarrier of a CTA of the cluster after this thread's own shared-memory
-// writes, which the other CTA's threads may then rely on.
-__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// Make this thread's shared-memory writes visible to TMA and tcgen05 (the async proxy).
+// Make this thread's shared-memory writes visible to TMA and tcgen05 (the async proxy). The
+// writes are complete when the fence is, so an arrive_remote after it (and a __syncwarp for the
+// warp's other lanes) may hand them to an MMA that the other CTA issues and that reads them on
+// this SM; a cluster-scope release, or an acquire fence in the issuer, would also wait for
+// unrelated global accesses.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// After an mbarrier wait that arrivals of the other CTA completed.
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 }  // namespace pair

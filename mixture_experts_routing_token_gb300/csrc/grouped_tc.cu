@@ -154,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       int stage = 0;
       uint32_t ph = 0;
       for (int t = cluster_id; t < total; t += nclusters) {
@@ -204,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader CTA)
-    if (leader && lane == 0) {
+    if (leader && ptx::elect_one()) {
       constexpr int A_MN = MODE == GRADW, B_MN = MODE != ROWS;
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;

@@ -348,10 +348,14 @@ MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, in
  *   moe_grouped_ffn. y is of out_dtype (any of the three), rounded once.
  * offsets, rows without an expert and status as moe_grouped_gemm. A scale byte
  * of 255 makes its row's (or column's) sums NaN.
+ * ws / ws_bytes: at least moe_mxfp4_grouped_gemm_workspace_size(...) bytes (the
+ * scales in the order the tensor cores read them).
  */
+MOE_API size_t moe_mxfp4_grouped_gemm_workspace_size(int S, int K, int N, int E, int activation);
 MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                                    const uint8_t* w_scales, int S, int K, int N, int E, const int32_t* offsets,
-                                   int activation, int out_dtype, void* y, int32_t* status, void* stream);
+                                   int activation, int out_dtype, void* y, void* ws, size_t ws_bytes,
+                                   int32_t* status, void* stream);
 
 /*
  * Expert-parallel exchange: G ranks, rank r owning the E_local = E / G

@@ -50,7 +50,8 @@ SIGNATURES = {
     "moe_grouped_gemm_backward": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p, _p]),
     "moe_mxfp4_quantize": (_i, [_p, _i, _i, _i, _p, _i, _p, _p, _p, _p]),
     "moe_mxfp4_dequantize": (_i, [_p, _p, _i, _i, _i, _p, _p]),
-    "moe_mxfp4_grouped_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p]),
+    "moe_mxfp4_grouped_gemm_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_mxfp4_grouped_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _sz, _p, _p]),
     "moe_gather_rows": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
     "moe_ep_receive_workspace_size": (_sz, [_i, _i]),
     "moe_ep_receive_index": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
@@ -515,8 +516,13 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     return out
 
 
+def moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation=None) -> int:
+    act = MOE_ACT_NONE if activation is None else MOE_ACT_SILU_AND_MUL
+    return int(lib().moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, act))
+
+
 def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activation=None,
-                           out_dtype=torch.bfloat16, out=None, status=None, stream=None):
+                           out_dtype=torch.bfloat16, out=None, workspace=None, status=None, stream=None):
     """:func:`moe_grouped_gemm` on 4-bit microscaled operands -> y [S, N] of ``out_dtype``.
 
     ``x_codes [S, K/2]``, ``x_scales [S, K/32]``, ``w_codes [E, N, K/2]``, ``w_scales [E, N, K/32]`` from
@@ -540,10 +546,11 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
         raise ValueError("silu_and_mul needs an even N")
     d = x_codes.device
     out = _out(out, (S, N // 2 if act else N), out_dtype, d, "out")
-    _on(d, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, out=out)
+    _on(d, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, out=out, workspace=workspace)
+    ws, ws_bytes, _keep = _workspace(workspace, moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation), d)
     _check("moe_mxfp4_grouped_gemm", lib().moe_mxfp4_grouped_gemm(
         x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), S, K, N, E,
-        offsets.data_ptr(), act, dt, out.data_ptr(), _status_ptr(status, d), _stream(stream, d)))
+        offsets.data_ptr(), act, dt, out.data_ptr(), ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
     return out
 
 

@@ -740,9 +740,15 @@ MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, in
   return launch_mxfp4_dequantize(codes, scales, R, K, dtype, out, (cudaStream_t)stream);
 }
 
+MOE_API size_t moe_mxfp4_grouped_gemm_workspace_size(int S, int K, int N, int E, int activation) {
+  if (S < 1 || K < 1 || N < 1 || E < 1) return 0;
+  return mxfp4_grouped_workspace(S, K, N, E, activation == MOE_ACT_SILU_AND_MUL);
+}
+
 MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                                    const uint8_t* w_scales, int S, int K, int N, int E, const int32_t* offsets,
-                                   int activation, int out_dtype, void* y, int32_t* status, void* stream) {
+                                   int activation, int out_dtype, void* y, void* ws, size_t ws_bytes,
+                                   int32_t* status, void* stream) {
   g_err[0] = 0;
   int rc;
   if ((rc = check_any_dtype(out_dtype))) return rc;
@@ -757,11 +763,12 @@ MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scal
   if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
   if ((rc = check_tensor(y, (long)S * N, "y"))) return rc;
   if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation)))) return rc;
   if (S == 0 || N == 0) return MOE_OK;
   if (K == 0)
     return zero_out(y, (size_t)S * (activation == MOE_ACT_NONE ? N : N / 2) * dsize(out_dtype), (cudaStream_t)stream);
   Mxfp4Args a{x_codes, x_scales, w_codes, w_scales, S, K, N, E, offsets, activation == MOE_ACT_SILU_AND_MUL,
-              out_dtype, y, status};
+              out_dtype, y, ws, status};
   return launch_mxfp4_grouped(a, (cudaStream_t)stream);
 }
 

@@ -141,6 +141,8 @@ int make_tmap_rows128(CUtensorMap* m, const void* base, uint64_t rows, uint64_t 
 // bytes) of one matrix, 128-byte swizzle. What lies past a matrix's rows or columns reads as zero.
 int make_tmap_3d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols, uint64_t rows, uint64_t mats,
                  uint32_t box_cols, uint32_t box_rows);
+// [atoms] pieces of 512 bytes (scales of 128 rows x 4); box = box_atoms of them, no swizzle.
+int make_tmap_atoms(CUtensorMap* m, const void* base, uint64_t atoms, uint32_t box_atoms);
 // x_sorted[p] = hidden[sorted_ids[p]] for p < offsets[E] (rows of row_bytes, a multiple of 16).
 int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int row_bytes,
                        void* xs, int32_t* status, cudaStream_t s);
@@ -252,8 +254,10 @@ struct Mxfp4Args {
   int silu;          // y = silu(gate half) * up half: [S, N / 2]
   int out_dtype;
   void* y;
+  void* ws;
   int32_t* status;
 };
+size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu);
 int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (PDL): the kernel may start while

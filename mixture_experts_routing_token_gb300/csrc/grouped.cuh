@@ -2,8 +2,9 @@
 //
 // offsets [E + 1] (device) says that expert e owns rows offsets[e] .. offsets[e + 1] - 1
 // of a matrix of S rows. The values come from the caller and are read on the device
-// only, so every kernel clamps them: a group is cut to [0, S) and one that ends before
-// it starts is empty. All indexing then stays in bounds whatever the words hold.
+// only, so every kernel first makes them an ascending list in [0, S] (each entry cut to
+// [0, S] and raised to the largest before it). Groups are then disjoint and all indexing
+// stays in bounds, whatever the words hold.
 #pragma once
 #include "common.cuh"
 
@@ -15,24 +16,41 @@ struct Span {
   __device__ __forceinline__ int rows() const { return hi - lo; }
 };
 
-__device__ __forceinline__ Span span(const int32_t* offsets, int e, int S) {
-  const int lo = min(max(__ldg(offsets + e), 0), S);
-  return Span{lo, max(lo, min(__ldg(offsets + e + 1), S))};
-}
+// In shared memory.
+struct Groups {
+  int off[MOE_MAX_EXPERTS + 1];     // the ascending offsets
+  int start[MOE_MAX_EXPERTS + 1];   // tiles of the experts before e; start[E]: all tiles
+  int bad;                          // the caller's offsets were not an ascending list in [0, S]
 
-// Whole warp: start[e] = sum over e' < e of tiles(rows of e'), start[E] = the total.
-// Also reports (bad != null) whether the offsets are not an ascending list in [0, S].
+  __device__ __forceinline__ Span span(int e) const { return Span{off[e], off[e + 1]}; }
+};
+
+// Whole warp: fills G; tiles(rows) is the tile count of a group.
 template <class Tiles>
-__device__ __forceinline__ void tile_list(const int32_t* offsets, int E, int S, Tiles tiles, int* start, int* bad) {
+__device__ __forceinline__ void group_list(const int32_t* offsets, int E, int S, Tiles tiles, Groups& G) {
   const int lane = threadIdx.x & 31;
-  const int per = (E + 31) / 32;
-  const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
-  int run = 0, wrong = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
-    wrong |= a < 0 || b < a || b > S;
-    run += tiles(span(offsets, e, S).rows());
+  const int per = (E + 32) / 32;          // entries per lane, E + 1 in all
+  const int i0 = min(E + 1, lane * per), i1 = min(E + 1, i0 + per);
+  int top = 0, wrong = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int v = __ldg(offsets + i);
+    wrong |= v < 0 || v > S || v < top;
+    top = max(top, min(max(v, 0), S));
+    G.off[i] = top;
   }
+  int before = top;                       // largest entry of the lanes before this one
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before = max(before, o);
+  }
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = 0;
+  if (i0 < i1) wrong |= __ldg(offsets + i0) < before;
+  for (int i = i0; i < i1; ++i) G.off[i] = max(G.off[i], before);
+  __syncwarp();
+  int run = 0;
+  for (int e = i0; e < min(i1, E); ++e) run += tiles(G.off[e + 1] - G.off[e]);
   int incl = run;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -40,13 +58,13 @@ __device__ __forceinline__ void tile_list(const int32_t* offsets, int E, int S, 
     if (lane >= d) incl += o;
   }
   int acc = incl - run;
-  for (int e = e0; e < e1; ++e) {
-    start[e] = acc;
-    acc += tiles(span(offsets, e, S).rows());
+  for (int e = i0; e < min(i1, E); ++e) {
+    G.start[e] = acc;
+    acc += tiles(G.off[e + 1] - G.off[e]);
   }
-  if (lane == 31) start[E] = incl;
+  if (lane == 31) G.start[E] = incl;
   wrong = __any_sync(0xffffffffu, wrong);
-  if (bad != nullptr && lane == 0) *bad = wrong;
+  if (lane == 0) G.bad = wrong;
 }
 
 // The expert whose tiles hold t: start[e] <= t < start[e + 1].
@@ -59,14 +77,12 @@ __device__ __forceinline__ int find(const int* start, int E, int t) {
   return lo;
 }
 
-// Rows that no group owns (before offsets[0], from offsets[E] on) are zero in row
+// Rows that no group owns (before the first offset, from the last one on) are zero in row
 // outputs. Thread `i` of `n` writes its share of them.
 template <class T>
-__device__ __forceinline__ void zero_unowned(T* out, const int32_t* offsets, int E, int S, long cols, long i, long n) {
-  const int first = min(max(__ldg(offsets), 0), S);
-  const int last = max(first, min(__ldg(offsets + E), S));
-  for (long j = i; j < (long)first * cols; j += n) out[j] = from_float<T>(0.0f);
-  for (long j = (long)last * cols + i; j < (long)S * cols; j += n) out[j] = from_float<T>(0.0f);
+__device__ __forceinline__ void zero_unowned(T* out, const Groups& G, int E, int S, long cols, long i, long n) {
+  for (long j = i; j < (long)G.off[0] * cols; j += n) out[j] = from_float<T>(0.0f);
+  for (long j = (long)G.off[E] * cols + i; j < (long)S * cols; j += n) out[j] = from_float<T>(0.0f);
 }
 
 // Two values of a 16-bit type in one word.

@@ -29,23 +29,23 @@ struct SimtParams {
 template <int MODE>
 __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   __shared__ float sa[TK][TM + 4], sb[TK][TN + 4];
-  __shared__ int start[MOE_MAX_EXPERTS + 1], bad;
+  __shared__ grouped::Groups G;
   const int tid = threadIdx.x;
   const int cols = MODE == ROWS ? P.N : P.K;           // columns of the output
   const int NT = (cols + TN - 1) / TN;
   const int MT = (P.N + TM - 1) / TM;                  // GRADW: row tiles of an expert's output
   if (tid < 32)
-    grouped::tile_list(P.offsets, P.E, P.S,
-                       [&](int rows) { return MODE == GRADW ? MT * NT : (rows + TM - 1) / TM * NT; }, start, &bad);
+    grouped::group_list(P.offsets, P.E, P.S,
+                       [&](int rows) { return MODE == GRADW ? MT * NT : (rows + TM - 1) / TM * NT; }, G);
   __syncthreads();
-  if (bad && blockIdx.x == 0 && tid == 0 && P.status) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
+  if (G.bad && blockIdx.x == 0 && tid == 0 && P.status) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
   const float *A = P.a, *B = P.b;
   float* out = P.out;
   const int tx = tid & 15, ty = tid >> 4;
-  for (int t = blockIdx.x; t < start[P.E]; t += gridDim.x) {
-    const int e = grouped::find(start, P.E, t);
-    const grouped::Span g = grouped::span(P.offsets, e, P.S);
-    const int local = t - start[e];
+  for (int t = blockIdx.x; t < G.start[P.E]; t += gridDim.x) {
+    const int e = grouped::find(G.start, P.E, t);
+    const grouped::Span g = G.span(e);
+    const int local = t - G.start[e];
     const int m0 = local / NT * TM, n0 = (local - local / NT * NT) * TN;
     const int red = MODE == ROWS ? P.K : MODE == GRADX ? P.N : g.rows();
     const int mcount = MODE == GRADW ? P.N : g.rows();
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
     }
   }
   if (MODE != GRADW)
-    grouped::zero_unowned(out, P.offsets, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
+    grouped::zero_unowned(out, G, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
 }
 
 template <int MODE>

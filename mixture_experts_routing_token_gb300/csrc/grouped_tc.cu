@@ -79,11 +79,11 @@ __device__ __forceinline__ int tiles_of(int rows, const Params& P) {
 // Tile t. Tiles of an expert that run together share the operand with fewer tiles, which
 // stays in L2, while the other one is walked once.
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(int t, const int* start, const Params& P) {
+__device__ __forceinline__ Tile tile_at(int t, const grouped::Groups& G, const Params& P) {
   Tile d;
-  d.e = grouped::find(start, P.E, t);
-  d.g = grouped::span(P.offsets, d.e, P.S);
-  const int local = t - start[d.e];
+  d.e = grouped::find(G.start, P.E, t);
+  d.g = G.span(d.e);
+  const int local = t - G.start[d.e];
   const int mt = MODE == GRADW ? P.MT : (d.g.rows() + 2 * BM - 1) / (2 * BM);
   if (mt > P.NT) {
     d.m = local / P.NT;
@@ -103,8 +103,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE], tail_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, bad_flag;
-  __shared__ int start[MOE_MAX_EXPERTS + 1];
+  __shared__ int abort_flag;
+  __shared__ grouped::Groups G;
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -144,13 +144,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2)
-    grouped::tile_list(P.offsets, P.E, P.S, [&](int rows) { return tiles_of<MODE>(rows, P); }, start, &bad_flag);
+    grouped::group_list(P.offsets, P.E, P.S, [&](int rows) { return tiles_of<MODE>(rows, P); }, G);
   ptx::tc_fence_before();
   __syncthreads();
   cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  const int total = start[P.E];
+  const int total = G.start[P.E];
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
@@ -158,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       int stage = 0;
       uint32_t ph = 0;
       for (int t = cluster_id; t < total; t += nclusters) {
-        const Tile ti = tile_at<MODE>(t, start, P);
+        const Tile ti = tile_at<MODE>(t, G, P);
         const bool cut = MODE == GRADW && ti.g.rows() % BK != 0;
         for (int kb = 0; kb < ti.steps; ++kb) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) goto producer_done;
@@ -209,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       for (int t = cluster_id; t < total; t += nclusters) {
-        const Tile ti = tile_at<MODE>(t, start, P);
+        const Tile ti = tile_at<MODE>(t, G, P);
         if (ti.steps == 0) continue;   // nothing to add up: the epilogue writes zeros
         if (!ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns)) break;
         ptx::tc_fence_after();
@@ -247,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
     int acc = 0;
     uint32_t aph = 0;
     for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at<MODE>(t, start, P);
+      const Tile ti = tile_at<MODE>(t, G, P);
       const int m = ti.m * (2 * BM) + (int)rank * BM + row;
       const bool mine = m < (MODE == GRADW ? P.M : ti.g.rows());
       T* dst = out + (MODE == GRADW ? (long)ti.e * P.M + m : (long)ti.g.lo + m) * P.C;
@@ -278,14 +278,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       if (++acc == 2) { acc = 0; aph ^= 1u; }
     }
     if (MODE != GRADW && !*abort_p)
-      grouped::zero_unowned(out, P.offsets, P.E, P.S, P.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
+      grouped::zero_unowned(out, G, P.E, P.S, P.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
   } else if (MODE == GRADW) {
     // ------------------------------------------------------------ tail (both CTAs): clears rows past a group's end
     int stage = 0;
     uint32_t tph = 0;                    // bit s: phase of tail_bar[s]
     for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at<MODE>(t, start, P);
+      const Tile ti = tile_at<MODE>(t, G, P);
       if (ti.steps == 0) continue;
       const int s = (stage + ti.steps - 1) % NSTAGE;
       stage = (stage + ti.steps) % NSTAGE;
@@ -320,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   }
   if (tid == 0 && P.status) {
     if (abort_flag) atomicOr(P.status, MOE_STATUS_TIMEOUT);
-    if (bad_flag && blockIdx.x == 0) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
+    if (G.bad && blockIdx.x == 0) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
   }
 }
 static_assert(A_BYTES == 2 * (int)MN_BLOCK && B_BYTES == 2 * (int)MN_BLOCK, "a stage is four boxes of 64 x 64");

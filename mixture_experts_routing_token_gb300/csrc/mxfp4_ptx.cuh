@@ -66,61 +66,5 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// The scales of 4 rows x CHUNK steps of K = 256 (8 bytes per row and step) on their way from
-// global to shared memory: lane l holds rows l, l + 32, l + 64, l + 96 of a 128-row block.
-constexpr int CHUNK = 4;
-
-struct ScaleRegs {
-  uint32_t w[4][2 * CHUNK];
-};
-
-// Scale bytes [8 step, 8 step + 32) of four rows; those at or past `count` read as 0.
-__device__ __forceinline__ void load_scales(ScaleRegs& v, const uint8_t* const (&row)[4], int step, int count, int vec) {
-  const int b0 = step * 8;
-  if (vec == 16) {              // rows a multiple of 16 bytes: two 16-byte loads
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (b0 + h * 16 < count) q = __ldg(reinterpret_cast<const uint4*>(row[i] + b0 + h * 16));
-        v.w[i][4 * h] = q.x;
-        v.w[i][4 * h + 1] = q.y;
-        v.w[i][4 * h + 2] = q.z;
-        v.w[i][4 * h + 3] = q.w;
-      }
-  } else if (vec == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2 * CHUNK; ++j)
-        v.w[i][j] = b0 + j * 4 < count ? __ldg(reinterpret_cast<const uint32_t*>(row[i] + b0 + j * 4)) : 0u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2 * CHUNK; ++j) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (b0 + j * 4 + b < count) x |= (uint32_t)__ldg(row[i] + b0 + j * 4 + b) << (8 * b);
-        v.w[i][j] = x;
-      }
-  }
-}
-
-// Step d of the chunk: two atoms (K = 128 each) `atom_stride` bytes apart.
-__device__ __forceinline__ void store_scales(const ScaleRegs& v, int d, uint32_t dst, uint32_t atom_stride, int lane) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * atom_stride + lane * 16),
-                 "r"(v.w[0][2 * d + j]), "r"(v.w[1][2 * d + j]), "r"(v.w[2][2 * d + j]), "r"(v.w[3][2 * d + j])
-                 : "memory");
-}
-
-inline int scale_vec(const void* p, int count) {
-  return count % 16 == 0 && aligned(p, 16) ? 16 : count % 4 == 0 && aligned(p, 4) ? 4 : 1;
-}
-
 }  // namespace mx
 }  // namespace moe

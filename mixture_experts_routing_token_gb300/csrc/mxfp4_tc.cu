@@ -12,11 +12,12 @@
 // scales (8 columns for A, 16 for B); two of 224 do, and keep the epilogue of one tile under
 // the products of the next.
 //
-// Scales stay as the user holds them, [rows, K / 32] bytes: three warps per SM (A's rows, B's
-// rows 0..127 and 128..223: both SMs need all of B's) read them four steps ahead into registers,
-// write them into the ring's stage in the order tcgen05.cp expects, and arrive on the stage's
-// full barrier beside the TMA bytes. Groups therefore start at any row, without a padded or
-// reordered copy of the scales.
+// The user holds scales as [rows, K / 32] bytes. tcgen05.cp wants them as atoms of 128 rows x 4
+// scales, by tile, so a first kernel (mxfp4_scales_kernel) writes them in that order into the
+// workspace: 1/17 of the operands' bytes, read and written once, after which a step's scales are
+// one TMA box each. Warps that read them from global memory inside the product's own pipeline
+// were slower (prompt 328 us with, 359 us with a deeper prefetch): with one row per lane their
+// loads touch 32 lines an instruction, beside the epilogue's stores.
 //
 // Bound: the tensor cores and L2 at prompt sizes (a step moves 30 KB per SM for 448 cycles of
 // products).
@@ -42,8 +43,7 @@ constexpr int SFB_OFF = SFA_OFF + 2 * (int)mx::SF_ATOM;
 constexpr int STAGE = SFB_OFF + 4 * (int)mx::SF_ATOM;
 constexpr int DSMEM = NSTAGE * STAGE + 1024;
 constexpr int EPI_WARPS = 4;
-constexpr int SF_WARPS = 3;
-constexpr int THREADS = (2 + EPI_WARPS + SF_WARPS) * 32;
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SFA_COL = 2 * BN, SFB_COL = SFA_COL + 8;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
@@ -52,13 +52,9 @@ constexpr uint32_t SF_COLS = 24;          // one step's scales; two sets, taken 
 static_assert(SFA_COL + 2 * SF_COLS <= TMEM_COLS, "tensor memory");
 
 struct Params {
-  const uint8_t* x_scales;
-  const uint8_t* w_scales;
   const int32_t* offsets;
-  int S, E, N;      // N: rows of w
+  int S, E;
   int steps;        // of 256 along K
-  int count;        // scale bytes of a row, K / 32
-  int vec_x, vec_w; // how they can be read (16, 4 or 1 bytes at a time)
   int cols;         // of y
   int NT;
   void* y;
@@ -74,11 +70,11 @@ struct Tile {
 
 __device__ __forceinline__ int mtiles(int rows) { return (rows + 2 * BM - 1) / (2 * BM); }
 
-__device__ __forceinline__ Tile tile_at(int t, const int* start, const Params& P) {
+__device__ __forceinline__ Tile tile_at(int t, const grouped::Groups& G, const Params& P) {
   Tile d;
-  d.e = grouped::find(start, P.E, t);
-  d.g = grouped::span(P.offsets, d.e, P.S);
-  const int local = t - start[d.e], mt = mtiles(d.g.rows());
+  d.e = grouped::find(G.start, P.E, t);
+  d.g = G.span(d.e);
+  const int local = t - G.start[d.e], mt = mtiles(d.g.rows());
   if (mt > P.NT) {
     d.m = local / P.NT;
     d.n = local - d.m * P.NT;
@@ -103,12 +99,13 @@ __device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f 
 template <bool SILU, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmXS, const __grid_constant__ CUtensorMap tmWS,
                       const Params P) {
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, bad_flag;
-  __shared__ int start[MOE_MAX_EXPERTS + 1];
+  __shared__ int abort_flag;
+  __shared__ grouped::Groups G;
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -121,7 +118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1 + 2 * SF_WARPS);
+      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -135,6 +132,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tmX);
     ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmXS);
+    ptx::prefetch_tmap(&tmWS);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -146,33 +145,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2)
-    grouped::tile_list(P.offsets, P.E, P.S, [&](int rows) { return mtiles(rows) * P.NT; }, start, &bad_flag);
+    grouped::group_list(P.offsets, P.E, P.S, [&](int rows) { return mtiles(rows) * P.NT; }, G);
   ptx::tc_fence_before();
   __syncthreads();
   cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  const int total = start[P.E];
+  const int total = G.start[P.E];
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer of codes (both CTAs)
+    // ------------------------------------------------------------ producer (both CTAs)
     if (ptx::elect_one()) {
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = cluster_id; t < total && ok; t += nclusters) {
-        const Tile ti = tile_at(t, start, P);
+        const Tile ti = tile_at(t, G, P);
         const int a_row = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, b_row = w_row<SILU>(ti.n, (int)rank, P);
+        const int a_atom = (G.start[ti.e] / P.NT * 2 + ti.m * 2 + (int)rank) * P.steps * 2;
+        const int b_atom = (ti.e * P.NT + ti.n) * P.steps * 4;
         for (int kb = 0; kb < P.steps; ++kb) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
             ok = false;
             break;
           }
           const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
-          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * (A_BYTES + B_BYTES));
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
           const uint32_t fb = map_to_rank(fb_local, 0);
           tma_load_3d_pair(st(stage), &tmX, kb * KB_BYTES, a_row, 0, fb);
           tma_load_3d_pair(st(stage) + A_BYTES, &tmW, kb * KB_BYTES, b_row, ti.e, fb);
+          tma_load_2d_pair(st(stage) + SFA_OFF, &tmXS, 0, a_atom + kb * 2, fb);
+          tma_load_2d_pair(st(stage) + SFB_OFF, &tmWS, 0, b_atom + kb * 4, fb);
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
         }
       }
@@ -219,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int dummy = 0;
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, &dummy, DRAIN_NS);
     }
-  } else if (warp < 2 + EPI_WARPS) {
+  } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int row = q * 32 + lane;
@@ -227,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int acc = 0;
     uint32_t aph = 0;
     for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at(t, start, P);
+      const Tile ti = tile_at(t, G, P);
       const int m = ti.m * (2 * BM) + (int)rank * BM + row;
       const bool mine = m < ti.g.rows();
       T* dst = y + ((long)ti.g.lo + m) * P.cols;
@@ -265,63 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (++acc == 2) { acc = 0; aph ^= 1u; }
     }
     if (!*abort_p)
-      grouped::zero_unowned(y, P.offsets, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
+      grouped::zero_unowned(y, G, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
-  } else {
-    // ------------------------------------------------------------ scales (both CTAs)
-    const int part = warp - 2 - EPI_WARPS;        // 0: A's rows; 1, 2: rows 0..127, 128..223 of the tile's B
-    const uint32_t off = part == 0 ? SFA_OFF : SFB_OFF + (uint32_t)(part - 1) * 2 * mx::SF_ATOM;
-    const int vec = part == 0 ? P.vec_x : P.vec_w;
-    const uint8_t* rows[4];
-    auto point = [&](int t) {                     // this lane's four rows of tile t (clamped: extra rows are not stored)
-      const Tile ti = tile_at(t, start, P);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane + 32 * i;
-        if (part == 0) {
-          rows[i] = P.x_scales + (long)min(ti.g.lo + ti.m * (2 * BM) + (int)rank * BM + r, P.S - 1) * P.count;
-        } else {
-          const int b = min((part - 1) * 128 + r, BN - 1), h = b >= HALF;
-          const int n = min(w_row<SILU>(ti.n, h, P) + b - h * HALF, P.N - 1);
-          rows[i] = P.w_scales + ((long)ti.e * P.N + n) * P.count;
-        }
-      }
-    };
-    mx::ScaleRegs cur, next;
-    int t = cluster_id, kb = 0, stage = 0;
-    uint32_t ph = 0;
-    if (t < total) {
-      point(t);
-      mx::load_scales(cur, rows, 0, P.count, vec);
-    }
-    bool ok = true;
-    while (t < total && ok) {
-      // request the next chunk, then hand over this one as stages come free
-      int nt = t, nkb = kb + mx::CHUNK;
-      if (nkb >= P.steps) {
-        nkb = 0;
-        nt = t + nclusters;
-        if (nt < total) point(nt);
-      }
-      if (nt < total) mx::load_scales(next, rows, nkb, P.count, vec);
-#pragma unroll
-      for (int d = 0; d < mx::CHUNK; ++d) {
-        if (kb + d < P.steps && ok) {
-          ok = ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            mx::store_scales(cur, d, st(stage) + off, mx::SF_ATOM, lane);
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[stage]), 0));
-            if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
-          }
-        }
-      }
-      cur = next;
-      t = nt;
-      kb = nkb;
-    }
   }
 
   if (*abort_p) {   // after a timeout, let copies in flight land before the shared memory is released
@@ -339,31 +287,132 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   if (tid == 0 && P.status) {
     if (abort_flag) atomicOr(P.status, MOE_STATUS_TIMEOUT);
-    if (bad_flag && blockIdx.x == 0) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
+    if (G.bad && blockIdx.x == 0) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
   }
 }
+
+// ---- scales in tile order ------------------------------------------------------------
+
+struct ScaleParams {
+  const uint8_t* x_scales;
+  const uint8_t* w_scales;
+  const int32_t* offsets;
+  int S, E, N, NT;
+  int steps, count;       // steps of 256 along K; scale bytes of a row (K / 32)
+  int vec;                // bytes at a time that both can be read in: 16, 4 or 1
+  int cols;               // of y (SILU: where the up rows start)
+  uint4* x_atoms;         // [128-row blocks of x, steps, 2][32 lanes]
+  uint4* w_atoms;         // [E, NT, steps, 2 blocks of 128 rows, 2][32 lanes]
+};
+
+// 16 scale bytes of a row from byte b on; those past its end are 0 (their codes are, too).
+__device__ __forceinline__ uint4 scale16(const uint8_t* row, int b, int count, int vec) {
+  if (vec == 16) return b < count ? __ldg(reinterpret_cast<const uint4*>(row + b)) : make_uint4(0, 0, 0, 0);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = b + 4 * j;
+    w[j] = 0;
+    if (vec == 4) {
+      if (at < count) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i < count) w[j] |= (uint32_t)__ldg(row + at + i) << (8 * i);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp writes four atoms (two steps) of one block of 128 rows: a lane reads 16 bytes of four
+// rows, 32 apart, and writes its 16 bytes of each atom, so the writes are whole lines. Rows past
+// a block's end (of the group, of the tile's 224) repeat a valid one; their results are not used.
+template <bool SILU>
+__global__ void __launch_bounds__(256) mxfp4_scales_kernel(const ScaleParams P) {
+  __shared__ grouped::Groups G;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 32)
+    grouped::group_list(P.offsets, P.E, P.S, [](int rows) { return mtiles(rows) * 2; }, G);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const int pairs = (P.steps + 1) / 2;
+  const int x_blocks = G.start[P.E], w_blocks = P.E * P.NT * 2;
+  const long units = (long)(x_blocks + w_blocks) * pairs, stride = (long)gridDim.x * (blockDim.x / 32);
+  for (long u = (long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; u < units; u += stride) {
+    const int block = (int)(u / pairs), step = (int)(u - (long)block * pairs) * 2;
+    const uint8_t* rows[4];
+    uint4* dst;
+    int step_stride;        // uint4 between the atoms of one step and the next
+    if (block < x_blocks) {
+      const int e = grouped::find(G.start, P.E, block);
+      const grouped::Span g = G.span(e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        rows[i] = P.x_scales + (long)min(g.lo + (block - G.start[e]) * 128 + lane + 32 * i, P.S - 1) * P.count;
+      dst = P.x_atoms + ((long)block * P.steps + step) * 2 * 32;
+      step_stride = 2 * 32;
+    } else {
+      const int b = block - x_blocks, tile = b >> 1, e = tile / P.NT, n = tile - e * P.NT;
+      if (G.start[e] == G.start[e + 1]) continue;     // no rows: no tile reads these
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = min((b & 1) * 128 + lane + 32 * i, BN - 1), h = r >= HALF;
+        const int row = SILU ? n * HALF + r + h * (P.cols - HALF) : n * BN + r;
+        rows[i] = P.w_scales + ((long)e * P.N + min(row, P.N - 1)) * P.count;
+      }
+      dst = P.w_atoms + (((long)tile * P.steps + step) * 4 + (b & 1) * 2) * 32;
+      step_stride = 4 * 32;
+    }
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = scale16(rows[i], step * 8, P.count, P.vec);
+    dst[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+    dst[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+    if (step + 1 < P.steps) {
+      dst[step_stride + lane] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+      dst[step_stride + 32 + lane] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+    }
+  }
+}
+
+int column_tiles(int N, bool silu) { return silu ? (N / 2 + HALF - 1) / HALF : (N + BN - 1) / BN; }
+int k_steps(int K) { return (K / 2 + KB_BYTES - 1) / KB_BYTES; }
+long x_atom_count(int S, int E, int steps) { return ((long)(S + 2 * BM - 1) / (2 * BM) + E) * 2 * steps * 2; }
 
 template <bool SILU, class T>
 int launch(const Mxfp4Args& a, cudaStream_t s) {
   const char* name = "mxfp4_grouped_gemm";
   if (int rc = ensure_smem_limit(mxfp4_pair_kernel<SILU, T>, DSMEM, name)) return rc;
-  CUtensorMap tx, tw;
+  const int steps = k_steps(a.K), NT = column_tiles(a.N, SILU);
+  const long xa = x_atom_count(a.S, a.E, steps), wa = (long)a.E * NT * steps * 4;
+  Carver c(a.ws);
+  uint4* x_atoms = c.take<uint4>((size_t)xa * 32);
+  uint4* w_atoms = c.take<uint4>((size_t)wa * 32);
+  {
+    ScaleParams q{a.x_scales, a.w_scales, a.offsets, a.S, a.E, a.N, NT, steps, a.K / 32, 16, SILU ? a.N / 2 : a.N,
+                  x_atoms, w_atoms};
+    if (q.count % 16 != 0) q.vec = q.count % 4 == 0 ? 4 : 1;
+    ProfScope ps("mxfp4_scales", s);
+    const long warps = (xa / (2 * steps) + wa / (2 * steps)) * ((steps + 1) / 2);
+    const int grid = (int)std::max(1L, std::min((warps + 7) / 8, (long)num_sms() * 8));
+    const cudaError_t e = launch_pdl(mxfp4_scales_kernel<SILU>, grid, 256, 0, s, q);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "mxfp4_scales: %s", cudaGetErrorString(e));
+    if (int rc = check_launch("mxfp4_scales")) return rc;
+  }
+  CUtensorMap tx, tw, txs, tws;
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K / 2, (uint64_t)a.S, 1, KB_BYTES, BM))) return rc;
   if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.E, KB_BYTES, HALF))) return rc;
+  if ((rc = make_tmap_atoms(&txs, x_atoms, (uint64_t)xa, 2))) return rc;
+  if ((rc = make_tmap_atoms(&tws, w_atoms, (uint64_t)wa, 4))) return rc;
   Params p{};
-  p.x_scales = a.x_scales;
-  p.w_scales = a.w_scales;
   p.offsets = a.offsets;
   p.S = a.S;
   p.E = a.E;
-  p.N = a.N;
-  p.steps = (a.K / 2 + KB_BYTES - 1) / KB_BYTES;
-  p.count = a.K / 32;
-  p.vec_x = mx::scale_vec(a.x_scales, p.count);
-  p.vec_w = mx::scale_vec(a.w_scales, p.count);
+  p.steps = steps;
   p.cols = SILU ? a.N / 2 : a.N;
-  p.NT = SILU ? (p.cols + HALF - 1) / HALF : (p.cols + BN - 1) / BN;
+  p.NT = NT;
   p.y = a.y;
   p.vec = grouped::store_width(a.y, p.cols, sizeof(T));
   p.status = a.status;
@@ -371,12 +420,20 @@ int launch(const Mxfp4Args& a, cudaStream_t s) {
   const long tiles = ((long)(a.S + 2 * BM - 1) / (2 * BM) + a.E) * p.NT;
   const int grid = 2 * (int)std::max(1L, std::min(tiles, (long)(num_sms() / 2)));
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(mxfp4_pair_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, p);
+  const cudaError_t e = launch_pdl(mxfp4_pair_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, txs, tws, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }
 
 }  // namespace
+
+size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu) {
+  const int steps = k_steps(K);
+  Carver c(nullptr);
+  c.take<uint4>((size_t)x_atom_count(S, E, steps) * 32);
+  c.take<uint4>((size_t)E * column_tiles(N, silu) * steps * 4 * 32);
+  return align_up(c.used, 256);
+}
 
 int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s) {
   if (a.out_dtype == MOE_F32) return a.silu ? launch<true, float>(a, s) : launch<false, float>(a, s);

@@ -63,7 +63,7 @@ def test_quantize_sizes_and_types(moe):
 def test_mxfp4_product_sizes_and_types(moe):
     f = moe.lib().moe_mxfp4_grouped_gemm
     one = ctypes.c_void_p(16)
-    call = lambda K=64, N=8, act=0, dt=1: f(one, one, one, one, 4, K, N, 2, None, act, dt, one, None, None)  # noqa: E731
+    call = lambda K=64, N=8, act=0, dt=1: f(one, one, one, one, 4, K, N, 2, None, act, dt, one, None, 0, None, None)  # noqa: E731
     assert call(K=40) == BAD and "multiple of 32" in err(moe)
     assert call(act=2) == BAD and "activation" in err(moe)
     assert call(act=1, N=7) == BAD and "even" in err(moe)

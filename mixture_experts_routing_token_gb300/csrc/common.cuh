@@ -239,6 +239,16 @@ size_t grouped_tc_workspace(int S, int K, int N, int E, bool fwd);
 int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);
 int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s);
 
+inline bool grouped_few_rows(int S, int E) {
+#ifdef FEWX
+  return S <= (long)E * FEWX;
+#else
+  return S <= (long)E * 16;
+#endif
+}
+// Few rows per expert (grouped_few.cu): x, w with rows of `cols` elements (a multiple of 8).
+int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s);
+
 // 4-bit microscaled values (mxfp4.cu): codes [rows, K / 2], scales [rows, K / 32].
 int launch_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows, int R, uint8_t* codes,
                           uint8_t* scales, int32_t* status, cudaStream_t s);
@@ -258,6 +268,7 @@ struct Mxfp4Args {
   int32_t* status;
 };
 size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu);
+int launch_mxfp4_few(const Mxfp4Args& a, cudaStream_t s);
 int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (PDL): the kernel may start while

@@ -422,6 +422,7 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   int rc;
   if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
   if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
+  if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
   CUtensorMap ta, tb;
   if ((rc = make_tmap_3d(&ta, x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
   if ((rc = make_tmap_3d(&tb, w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, BK, BN / 2))) return rc;

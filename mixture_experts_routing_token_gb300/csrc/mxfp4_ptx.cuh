@@ -66,5 +66,32 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// 16 scale bytes of a row from byte b on; those past its end are 0 (their codes are, too).
+__device__ __forceinline__ uint4 scale16(const uint8_t* row, int b, int count, int vec) {
+  if (vec == 16) return b < count ? __ldg(reinterpret_cast<const uint4*>(row + b)) : make_uint4(0, 0, 0, 0);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = b + 4 * j;
+    w[j] = 0;
+    if (vec == 4) {
+      if (at < count) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i < count) w[j] |= (uint32_t)__ldg(row + at + i) << (8 * i);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes at a time in which scale16 may read rows of `count` bytes (the base is 16-byte aligned).
+inline int scale_vec(int count) { return count % 16 == 0 ? 16 : count % 4 == 0 ? 4 : 1; }
+
+// silu(z) = z / (1 + e^-z) with the approximate division (2 ulp; results below 2^-119 in
+// magnitude, z < -87, become 0): with the IEEE division the epilogue took 12.9k cycles a tile,
+// three and a half times the products.
+__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
 }  // namespace mx
 }  // namespace moe

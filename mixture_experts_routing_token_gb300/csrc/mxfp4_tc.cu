@@ -91,11 +91,6 @@ __device__ __forceinline__ int w_row(int n, int b, const Params& P) {
   return SILU ? n * HALF + b * P.cols : n * BN + b * HALF;
 }
 
-// silu(z) = z / (1 + e^-z) with the approximate division (2 ulp; results below 2^-119 in
-// magnitude, z < -87, become 0): with the IEEE division the epilogue took 12.9k cycles a tile,
-// three and a half times the products.
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-
 template <bool SILU, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -248,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (mine && c0 < P.cols) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              g[i] = __float_as_uint(silu_fast(__uint_as_float(g[i])) * __uint_as_float(u[i]));
+              g[i] = __float_as_uint(mx::silu_fast(__uint_as_float(g[i])) * __uint_as_float(u[i]));
             grouped::store_cols(dst, c0, P.cols, P.vec, g);
           }
         }
@@ -305,25 +300,6 @@ struct ScaleParams {
   uint4* w_atoms;         // [E, NT, steps, 2 blocks of 128 rows, 2][32 lanes]
 };
 
-// 16 scale bytes of a row from byte b on; those past its end are 0 (their codes are, too).
-__device__ __forceinline__ uint4 scale16(const uint8_t* row, int b, int count, int vec) {
-  if (vec == 16) return b < count ? __ldg(reinterpret_cast<const uint4*>(row + b)) : make_uint4(0, 0, 0, 0);
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = b + 4 * j;
-    w[j] = 0;
-    if (vec == 4) {
-      if (at < count) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (at + i < count) w[j] |= (uint32_t)__ldg(row + at + i) << (8 * i);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // A warp writes four atoms (two steps) of one block of 128 rows: a lane reads 16 bytes of four
 // rows, 32 apart, and writes its 16 bytes of each atom, so the writes are whole lines. Rows past
 // a block's end (of the group, of the tile's 224) repeat a valid one; their results are not used.
@@ -366,7 +342,7 @@ __global__ void __launch_bounds__(256) mxfp4_scales_kernel(const ScaleParams P) 
     }
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = scale16(rows[i], step * 8, P.count, P.vec);
+    for (int i = 0; i < 4; ++i) v[i] = mx::scale16(rows[i], step * 8, P.count, P.vec);
     dst[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
     dst[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
     if (step + 1 < P.steps) {
@@ -390,10 +366,9 @@ int launch(const Mxfp4Args& a, cudaStream_t s) {
   uint4* x_atoms = c.take<uint4>((size_t)xa * 32);
   uint4* w_atoms = c.take<uint4>((size_t)wa * 32);
   {
-    ScaleParams q{a.x_scales, a.w_scales, a.offsets, a.S, a.E, a.N, NT, steps, a.K / 32, 16, SILU ? a.N / 2 : a.N,
+    ScaleParams q{a.x_scales, a.w_scales, a.offsets, a.S, a.E, a.N, NT, steps, a.K / 32, mx::scale_vec(a.K / 32), SILU ? a.N / 2 : a.N,
                   x_atoms, w_atoms};
-    if (q.count % 16 != 0) q.vec = q.count % 4 == 0 ? 4 : 1;
-    ProfScope ps("mxfp4_scales", s);
+      ProfScope ps("mxfp4_scales", s);
     const long warps = (xa / (2 * steps) + wa / (2 * steps)) * ((steps + 1) / 2);
     const int grid = (int)std::max(1L, std::min((warps + 7) / 8, (long)num_sms() * 8));
     const cudaError_t e = launch_pdl(mxfp4_scales_kernel<SILU>, grid, 256, 0, s, q);
@@ -428,6 +403,7 @@ int launch(const Mxfp4Args& a, cudaStream_t s) {
 }  // namespace
 
 size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu) {
+  if (grouped_few_rows(S, E)) return 0;
   const int steps = k_steps(K);
   Carver c(nullptr);
   c.take<uint4>((size_t)x_atom_count(S, E, steps) * 32);
@@ -436,6 +412,7 @@ size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu) {
 }
 
 int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s) {
+  if (grouped_few_rows(a.S, a.E)) return launch_mxfp4_few(a, s);
   if (a.out_dtype == MOE_F32) return a.silu ? launch<true, float>(a, s) : launch<false, float>(a, s);
   if (a.out_dtype == MOE_BF16) return a.silu ? launch<true, __nv_bfloat16>(a, s) : launch<false, __nv_bfloat16>(a, s);
   return a.silu ? launch<true, __half>(a, s) : launch<false, __half>(a, s);

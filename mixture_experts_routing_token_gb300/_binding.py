@@ -386,29 +386,46 @@ def _code(dtype):
         raise ValueError(f"unsupported dtype {dtype}") from None
 
 
+def _take(t, name, dtype, device=None):
+    """Address of an input tensor after its checks (one call per tensor: a decode step makes few)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    return t.data_ptr()
+
+
+def _give(t, name, shape, dtype, device):
+    """(tensor, address) of an output: the caller's after its checks, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    p = _take(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}")
+    return t, p
+
+
 def _status_ptr(status, device):
     if status is None:
         return None
-    _dev(status, "status", torch.int32)
-    if status.numel() < 1 or status.device != device:
-        raise ValueError("status must be an int32 word on the call's device")
-    return status.data_ptr()
-
-
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device} (got {t.device})")
+    p = _take(status, "status", torch.int32, device)
+    if status.numel() < 1:
+        raise ValueError("status must hold an int32 word")
+    return p
 
 
 def _workspace(workspace, need, device):
-    """(address, bytes) of the caller's workspace or of a new one; nothing when none is needed. The tensor comes third."""
+    """(address, bytes, tensor) of the caller's workspace or of a new one; nothing when none is needed."""
     if workspace is None:
         if not need:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _dev(workspace, "workspace")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return _take(workspace, "workspace", workspace.dtype, device), workspace.numel() * workspace.element_size(), workspace
 
 
 def moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E) -> int:
@@ -420,21 +437,22 @@ def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, strea
 
     ``x [S, K]``, ``w [E, N, K]`` (float32, bf16 or float16); ``offsets [E+1]`` int32: expert e owns the
     rows ``offsets[e]`` to ``offsets[e+1] - 1``. Rows without an expert give zero rows."""
-    _dev(x, "x")
-    _dev(w, "w", x.dtype)
-    _dev(offsets, "offsets", torch.int32)
-    dt = _code(x.dtype)
-    if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1] or offsets.shape != (w.shape[0] + 1,):
+    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
+    dtype, d = x.dtype, x.device
+    wp = _take(w, "w", dtype, d)
+    op = _take(offsets, "offsets", torch.int32, d)
+    dt = _code(dtype)
+    if x.dim() != 2 or w.dim() != 3:
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
     S, K = x.shape
-    E, N, _ = w.shape
-    d = x.device
-    out = _out(out, (S, N), x.dtype, d, "out")
-    _on(d, w=w, offsets=offsets, out=out, workspace=workspace)
-    ws, ws_bytes, _keep = _workspace(workspace, moe_grouped_gemm_workspace_size(dt, S, K, N, E), d)
-    _check("moe_grouped_gemm", lib().moe_grouped_gemm(
-        x.data_ptr(), w.data_ptr(), dt, S, K, N, E, offsets.data_ptr(), out.data_ptr(), ws, ws_bytes,
-        _status_ptr(status, d), _stream(stream, d)))
+    E, N, Kw = w.shape
+    if Kw != K or offsets.shape != (E + 1,):
+        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
+    out, yp = _give(out, "out", (S, N), dtype, d)
+    L = lib()
+    ws, ws_bytes, _keep = _workspace(workspace, L.moe_grouped_gemm_workspace_size(dt, S, K, N, E), d)
+    _check("moe_grouped_gemm", L.moe_grouped_gemm(xp, wp, dt, S, K, N, E, op, yp, ws, ws_bytes,
+                                                  _status_ptr(status, d), _stream(stream, d)))
     return out
 
 
@@ -447,24 +465,24 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
     """Gradients of :func:`moe_grouped_gemm` for ``d_y [S, N]`` -> (d_x [S, K], d_w [E, N, K]) in x's dtype.
 
     One that is not wanted is None. Experts without rows get a zero ``d_w``, rows without an expert a zero ``d_x``."""
-    _dev(x, "x")
-    _dev(w, "w", x.dtype)
-    _dev(d_y, "d_y", x.dtype)
-    _dev(offsets, "offsets", torch.int32)
-    dt = _code(x.dtype)
-    if (x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1] or offsets.shape != (w.shape[0] + 1,)
-            or d_y.shape != (x.shape[0], w.shape[1])):
+    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
+    dtype, d = x.dtype, x.device
+    wp = _take(w, "w", dtype, d)
+    gp = _take(d_y, "d_y", dtype, d)
+    op = _take(offsets, "offsets", torch.int32, d)
+    dt = _code(dtype)
+    if x.dim() != 2 or w.dim() != 3:
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
     S, K = x.shape
-    E, N, _ = w.shape
-    d = x.device
-    d_x = _out(d_x, (S, K), x.dtype, d, "d_x") if want_d_x else None
-    d_w = _out(d_w, (E, N, K), x.dtype, d, "d_w") if want_d_w else None
-    _on(d, w=w, offsets=offsets, d_y=d_y, d_x=d_x, d_w=d_w, workspace=workspace)
-    ws, ws_bytes, _keep = _workspace(workspace, moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d)
-    _check("moe_grouped_gemm_backward", lib().moe_grouped_gemm_backward(
-        x.data_ptr(), w.data_ptr(), d_y.data_ptr(), dt, S, K, N, E, offsets.data_ptr(), _ptr(d_x), _ptr(d_w),
-        ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
+    E, N, Kw = w.shape
+    if Kw != K or offsets.shape != (E + 1,) or d_y.shape != (S, N):
+        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
+    d_x, dxp = _give(d_x, "d_x", (S, K), dtype, d) if want_d_x else (None, None)
+    d_w, dwp = _give(d_w, "d_w", (E, N, K), dtype, d) if want_d_w else (None, None)
+    L = lib()
+    ws, ws_bytes, _keep = _workspace(workspace, L.moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d)
+    _check("moe_grouped_gemm_backward", L.moe_grouped_gemm_backward(
+        xp, wp, gp, dt, S, K, N, E, op, dxp, dwp, ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
     return d_x, d_w
 
 
@@ -474,45 +492,40 @@ def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, status=None, strea
     Blocks of 32 values share the power of two ``2^(scale - 127)``; two codes to a byte, the first one low.
     ``rows [R]`` int32 picks the rows (row r from ``x[rows[r]]``); without it R is T. ``x`` may have more
     than two dimensions when no rows are given: they are kept."""
-    _dev(x, "x")
-    dt = _code(x.dtype)
-    if x.dim() < 2 or x.shape[-1] % 32:
-        raise ValueError("x must be [T, K] (or [..., K] without rows) with K a multiple of 32")
-    K = x.shape[-1]
-    T = x.numel() // K if K else 0
+    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
     d = x.device
-    if rows is None:
-        lead = tuple(x.shape[:-1])
-        R = T
-    else:
-        _dev(rows, "rows", torch.int32)
+    dt = _code(x.dtype)
+    lead, K = x.shape[:-1], x.shape[-1] if x.dim() else 0
+    if x.dim() < 2 or K % 32:
+        raise ValueError("x must be [T, K] (or [..., K] without rows) with K a multiple of 32")
+    T = lead.numel()
+    rp, R = None, T
+    if rows is not None:
+        rp = _take(rows, "rows", torch.int32, d)
         if x.dim() != 2 or rows.dim() != 1:
             raise ValueError("rows must be [R] and x [T, K]")
-        R = rows.shape[0]
-        lead = (R,)
-    codes = _out(codes, lead + (K // 2,), torch.uint8, d, "codes")
-    scales = _out(scales, lead + (K // 32,), torch.uint8, d, "scales")
-    _on(d, rows=rows, codes=codes, scales=scales)
-    _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(
-        x.data_ptr(), dt, T, K, _ptr(rows), R, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, d),
-        _stream(stream, d)))
+        lead = rows.shape
+        R = lead[0]
+    codes, cp = _give(codes, "codes", (*lead, K // 2), torch.uint8, d)
+    scales, sp = _give(scales, "scales", (*lead, K // 32), torch.uint8, d)
+    _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(xp, dt, T, K, rp, R, cp, sp, _status_ptr(status, d),
+                                                          _stream(stream, d)))
     return codes, scales
 
 
 def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values that ``codes [..., K/2]`` and ``scales [..., K/32]`` stand for -> [..., K] of ``dtype``."""
-    _dev(codes, "codes", torch.uint8)
-    _dev(scales, "scales", torch.uint8)
-    dt = _code(dtype)
-    K = 2 * codes.shape[-1]
-    if K % 32 or tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // 32,):
-        raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32] with K a multiple of 32")
+    cp = _take(codes, "codes", torch.uint8)
     d = codes.device
-    out = _out(out, tuple(codes.shape[:-1]) + (K,), dtype, d, "out")
-    _on(d, scales=scales, out=out)
-    _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(
-        codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // K if K else 0, K, dt, out.data_ptr(),
-        _stream(stream, d)))
+    sp = _take(scales, "scales", torch.uint8, d)
+    dt = _code(dtype)
+    if codes.dim() < 1 or codes.shape[-1] % 16:
+        raise ValueError("codes must be [..., K / 2] with K a multiple of 32")
+    lead, K = codes.shape[:-1], 2 * codes.shape[-1]
+    if scales.shape != (*lead, K // 32):
+        raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32]")
+    out, op = _give(out, "out", (*lead, K), dtype, d)
+    _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(cp, sp, lead.numel(), K, dt, op, _stream(stream, d)))
     return out
 
 
@@ -528,29 +541,34 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
     ``x_codes [S, K/2]``, ``x_scales [S, K/32]``, ``w_codes [E, N, K/2]``, ``w_scales [E, N, K/32]`` from
     :func:`moe_mxfp4_quantize`. ``activation="silu_and_mul"`` returns [S, N/2]: silu of the first half of
     the columns times the second half."""
-    for t, name in ((x_codes, "x_codes"), (x_scales, "x_scales"), (w_codes, "w_codes"), (w_scales, "w_scales")):
-        _dev(t, name, torch.uint8)
-    _dev(offsets, "offsets", torch.int32)
-    dt = _code(out_dtype)
-    if activation not in (None, "silu_and_mul"):
-        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
-    if x_codes.dim() != 2 or w_codes.dim() != 3 or w_codes.shape[2] != x_codes.shape[1]:
-        raise ValueError("shapes must be x_codes [S, K / 2], w_codes [E, N, K / 2]")
-    S, K = x_codes.shape[0], 2 * x_codes.shape[1]
-    E, N, _ = w_codes.shape
-    if (K % 32 or tuple(x_scales.shape) != (S, K // 32) or tuple(w_scales.shape) != (E, N, K // 32)
-            or offsets.shape != (E + 1,)):
-        raise ValueError("shapes must be x_scales [S, K / 32], w_scales [E, N, K / 32], offsets [E + 1], K a multiple of 32")
-    act = MOE_ACT_NONE if activation is None else MOE_ACT_SILU_AND_MUL
-    if act and N % 2:
-        raise ValueError("silu_and_mul needs an even N")
+    u8 = torch.uint8
+    xp = _take(x_codes, "x_codes", u8)
     d = x_codes.device
-    out = _out(out, (S, N // 2 if act else N), out_dtype, d, "out")
-    _on(d, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, offsets=offsets, out=out, workspace=workspace)
-    ws, ws_bytes, _keep = _workspace(workspace, moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation), d)
-    _check("moe_mxfp4_grouped_gemm", lib().moe_mxfp4_grouped_gemm(
-        x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), S, K, N, E,
-        offsets.data_ptr(), act, dt, out.data_ptr(), ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
+    xsp = _take(x_scales, "x_scales", u8, d)
+    wp = _take(w_codes, "w_codes", u8, d)
+    wsp = _take(w_scales, "w_scales", u8, d)
+    op = _take(offsets, "offsets", torch.int32, d)
+    dt = _code(out_dtype)
+    if x_codes.dim() != 2 or w_codes.dim() != 3:
+        raise ValueError("shapes must be x_codes [S, K / 2], w_codes [E, N, K / 2]")
+    S, K = x_codes.shape
+    E, N, Kw = w_codes.shape
+    if Kw != K or K % 16 or x_scales.shape != (S, K // 16) or w_scales.shape != (E, N, K // 16) or offsets.shape != (E + 1,):
+        raise ValueError("shapes must be x_codes [S, K / 2], x_scales [S, K / 32], w_codes [E, N, K / 2], "
+                         "w_scales [E, N, K / 32], offsets [E + 1] with K a multiple of 32")
+    K *= 2
+    cols, act = N, MOE_ACT_NONE
+    if activation is not None:
+        if activation != "silu_and_mul":
+            raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+        if N % 2:
+            raise ValueError("silu_and_mul needs an even N")
+        cols, act = N // 2, MOE_ACT_SILU_AND_MUL
+    out, yp = _give(out, "out", (S, cols), out_dtype, d)
+    L = lib()
+    ws, ws_bytes, _keep = _workspace(workspace, L.moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, act), d)
+    _check("moe_mxfp4_grouped_gemm", L.moe_mxfp4_grouped_gemm(
+        xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
     return out
 
 

@@ -25,46 +25,51 @@ struct Groups {
   __device__ __forceinline__ Span span(int e) const { return Span{off[e], off[e + 1]}; }
 };
 
-// Whole warp: fills G; tiles(rows) is the tile count of a group.
+// Whole warp: fills G; tiles(rows) is the tile count of a group. Entries are taken 32 at a time,
+// the loads of four such turns under way together (one latency for up to 127 experts).
+// Returns (in every lane) the rows of the largest group.
 template <class Tiles>
-__device__ __forceinline__ void group_list(const int32_t* offsets, int E, int S, Tiles tiles, Groups& G) {
+__device__ __forceinline__ int group_list(const int32_t* offsets, int E, int S, Tiles tiles, Groups& G) {
   const int lane = threadIdx.x & 31;
-  const int per = (E + 32) / 32;          // entries per lane, E + 1 in all
-  const int i0 = min(E + 1, lane * per), i1 = min(E + 1, i0 + per);
-  int top = 0, wrong = 0;
-  for (int i = i0; i < i1; ++i) {
-    const int v = __ldg(offsets + i);
-    wrong |= v < 0 || v > S || v < top;
-    top = max(top, min(max(v, 0), S));
-    G.off[i] = top;
-  }
-  int before = top;                       // largest entry of the lanes before this one
+  int top = 0, last = 0, wrong = 0, sum = 0, most = 0;    // over all entries before this turn
+  for (int i0 = 0; i0 <= E; i0 += 128) {
+    int v[4];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, before, d);
-    if (lane >= d) before = max(before, o);
-  }
-  before = __shfl_up_sync(0xffffffffu, before, 1);
-  if (lane == 0) before = 0;
-  if (i0 < i1) wrong |= __ldg(offsets + i0) < before;
-  for (int i = i0; i < i1; ++i) G.off[i] = max(G.off[i], before);
-  __syncwarp();
-  int run = 0;
-  for (int e = i0; e < min(i1, E); ++e) run += tiles(G.off[e + 1] - G.off[e]);
-  int incl = run;
+    for (int u = 0; u < 4; ++u) v[u] = i0 + 32 * u + lane <= E ? __ldg(offsets + i0 + 32 * u + lane) : 0;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i - lane > E) break;
+      int prev = __shfl_up_sync(0xffffffffu, v[u], 1);
+      if (lane == 0) prev = last;
+      last = __shfl_sync(0xffffffffu, v[u], 31);
+      wrong |= i <= E && (v[u] < 0 || v[u] > S || (i > 0 && v[u] < prev));
+      int off = max(i <= E ? min(max(v[u], 0), S) : 0, top);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) off = max(off, __shfl_up_sync(0xffffffffu, off, d));
+      int before = __shfl_up_sync(0xffffffffu, off, 1);   // the entry before: group i - 1 ends at off
+      if (lane == 0) before = top;
+      top = __shfl_sync(0xffffffffu, off, 31);
+      const int rows = i > 0 && i <= E ? off - before : 0;
+      most = max(most, rows);
+      int incl = i > 0 && i <= E ? tiles(rows) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (i <= E) {
+        G.off[i] = off;
+        G.start[i] = sum + incl;       // the tiles of groups 0 .. i - 1
+      }
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
-  int acc = incl - run;
-  for (int e = i0; e < min(i1, E); ++e) {
-    G.start[e] = acc;
-    acc += tiles(G.off[e + 1] - G.off[e]);
-  }
-  if (lane == 31) G.start[E] = incl;
   wrong = __any_sync(0xffffffffu, wrong);
   if (lane == 0) G.bad = wrong;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+  return most;
 }
 
 // The expert whose tiles hold t: start[e] <= t < start[e + 1].

@@ -7,17 +7,20 @@
 // The operands change places: up to 128 rows of w are the MMA's M (A operand), the group's
 // rows of x, 16 to 64 of them, its N; a TMEM lane then holds one output column of every row.
 // One CTA per SM takes units of (expert, rows of x, f columns of y) by turns:
-//   warp 0     TMA producer: per step 128 bytes of each of the unit's rows, in boxes of 16
-//              rows, through a ring of 8 (4-bit: 7) stages, up to 128 KB of weights in flight
-//              per SM;
+//   warp 0     TMA producer: per step 128 bytes of each of the unit's rows (one box of f rows of
+//              w, boxes of 16 rows of x), through a ring whose stages are as large as the launch's units need (their
+//              columns, the rows of the largest group), so that there are up to 20 of them and
+//              about 160 KB of weights in flight per SM;
 //   warp 1     MMA issuer (M = 128, N = 16 .. 64);
 //   warps 2-5  epilogue: a warp stores 32 neighbouring columns of a row at a time;
 //   warps 6-9  4-bit only: scales, each warp every fourth chunk of four steps, through a buffer
 //              and a pair of barriers of its own, so that four chunks of loads are under way
 //              without registers for more than one.
-// f, the columns of a unit (a multiple of 16), is chosen in the kernel from the number of
-// active experts: M = 128 tiles of, say, 8 active experts with 2816 columns would be 176 units
-// for 152 SMs, two rounds of which the second is nearly empty; 80 columns make 288.
+// f, the columns of a unit (a multiple of 16), is chosen on the host from the number of experts
+// that can be active, min(S, E): M = 128 tiles of, say, 8 active experts with 2816 columns would
+// be 176 units for 152 SMs, two rounds of which the second is nearly empty; 80 columns make 288.
+// The box has f rows because TMA instructions are what limits a unit otherwise: with boxes of 16
+// rows a step took 600 cycles whatever its size (33 GB/s an SM at f = 80).
 // A group of more than 64 rows is several units that read the same weights next to each other.
 #include <algorithm>
 
@@ -37,12 +40,13 @@ constexpr uint64_t DRAIN_NS = 2000000000ull;
 
 template <bool MX>
 struct Cfg {
-  static constexpr int A_BYTES = MAXF * ROWB, B_BYTES = MAXR * ROWB;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NSTAGE = MX ? 7 : 8;
+  static constexpr int A_READ = MAXF * ROWB;         // what an MMA reads of its A operand, whatever was loaded
+  static constexpr int UP = A_READ / 2;              // with the gate: the up rows, after 64 rows of room for the gate's
+  static constexpr int MAXSTAGE = 20;
+  static constexpr int RING = (MX ? 176 : 208) * 1024;
   static constexpr int SF_WARPS = MX ? 4 : 0;
   static constexpr int SF_STEP = 4 * (int)mx::SF_ATOM;          // of one step: two atoms of A, two of B
-  static constexpr int SF_OFF = NSTAGE * STAGE, SF_BUF = CHUNK * SF_STEP;
+  static constexpr int SF_OFF = RING, SF_BUF = CHUNK * SF_STEP;
   static constexpr int DSMEM = SF_OFF + SF_WARPS * SF_BUF + 1024;
   static constexpr int THREADS = (6 + SF_WARPS) * 32;
   static constexpr uint32_t SF_COL = 2 * MAXR;       // scales: two sets of 16 columns
@@ -54,6 +58,7 @@ struct Params {
   const uint8_t* x_scales;
   const uint8_t* w_scales;
   int S, E, N, cols;    // rows of w; columns of y
+  int f;                // columns per unit
   int steps;            // of 128 bytes along K
   int count, vec;       // 4-bit: scale bytes of a row, bytes read at a time (16, 4, 1)
   void* y;
@@ -65,22 +70,6 @@ struct Params {
 struct Unit {
   int e, row, rows, n0, cols;    // group row of its first row of x; columns [n0, n0 + cols)
 };
-
-// Columns per unit: the largest number of rounds times (columns + the cost of a unit, about
-// that of 8 columns) is smallest. `heads` = units per column tile (expert, 64 rows of x).
-__device__ __forceinline__ int unit_columns(int heads, int cols, int most, int ctas) {
-  int best = most;
-  long cost = 1L << 62;
-  for (int f = most; f >= BOX; f -= BOX) {
-    const long units = (long)heads * ((cols + f - 1) / f);
-    const long c = (units + ctas - 1) / ctas * (f + 8);
-    if (c < cost) {
-      cost = c;
-      best = f;
-    }
-  }
-  return best;
-}
 
 __device__ __forceinline__ Unit unit_at(int t, const grouped::Groups& G, const Params& P, int f, int tiles) {
   // G.start counts heads; the heads of an expert that share a column tile follow each other
@@ -118,25 +107,23 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
     grouped_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const Params P) {
   using C = Cfg<MX>;
-  constexpr int NSTAGE = C::NSTAGE;
-  __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
+  __shared__ __align__(8) uint64_t full_bar[C::MAXSTAGE], empty_bar[C::MAXSTAGE];
   __shared__ __align__(8) uint64_t sf_full[4], sf_empty[4];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ int s_f;
+  __shared__ int s_most;
   __shared__ grouped::Groups G;
   __shared__ float up_part[SILU ? 64 : 1][17];      // up columns of 16 rows, on their way to the gate's warps
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t dsmem = (ptx::smem_u32(dsmem_raw) + 1023u) & ~1023u;
-  auto st = [&](int s) { return dsmem + (uint32_t)(s * C::STAGE); };
   auto sf = [&](int b, int step) { return dsmem + (uint32_t)(C::SF_OFF + b * C::SF_BUF + step * C::SF_STEP); };
   volatile int* abort_p = &abort_flag;
 
   if (tid == 0) {
-    for (int s = 0; s < NSTAGE; ++s) {
+    for (int s = 0; s < C::MAXSTAGE; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
     }
@@ -160,16 +147,22 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2) {
-    grouped::group_list(P.offsets, P.E, P.S, [](int rows) { return (rows + MAXR - 1) / MAXR; }, G);
-    __syncwarp();
-    if (lane == 0) s_f = unit_columns(G.start[P.E], P.cols, SILU ? MAXF / 2 : MAXF, gridDim.x);
+    const int most =
+        grouped::group_list(P.offsets, P.E, P.S, [](int rows) { return (rows + MAXR - 1) / MAXR; }, G);
+    if (lane == 0) s_most = min(most, MAXR);
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  const int f = s_f, tiles = (P.cols + f - 1) / f;
+  const int f = P.f, tiles = (P.cols + f - 1) / f;
   const int total = G.start[P.E] * tiles;
+  // the ring: A, then B; an MMA reads A_READ bytes from a stage on, so the last stage has to end
+  // that far inside the ring
+  const int a_bytes = (SILU ? C::UP : 0) + f * ROWB;
+  const int stage_bytes = a_bytes + (s_most + BOX - 1) / BOX * BOX_BYTES;
+  const int nstage = min(C::MAXSTAGE, (C::RING - max(0, C::A_READ - stage_bytes)) / stage_bytes);
+  auto st = [&](int s) { return dsmem + (uint32_t)(s * stage_bytes); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -179,23 +172,20 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
         const Unit u = unit_at(t, G, P, f, tiles);
-        const int na = (u.cols + BOX - 1) / BOX, nb = (u.rows + BOX - 1) / BOX;
+        const int nb = (u.rows + BOX - 1) / BOX;
         for (int k = 0; k < P.steps; ++k) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
             ok = false;
             break;
           }
           const uint32_t fb = ptx::smem_u32(&full_bar[stage]);
-          ptx::mbar_arrive_expect_tx(fb, (uint32_t)(((SILU ? 2 : 1) * na + nb) * BOX_BYTES));
+          ptx::mbar_arrive_expect_tx(fb, (uint32_t)((SILU ? 2 : 1) * f * ROWB + nb * BOX_BYTES));
           const int x = k * (MX ? ROWB : ROWB / 2);
-          for (int i = 0; i < na; ++i) {
-            ptx::tma_load_3d(st(stage) + i * BOX_BYTES, &tmW, x, u.n0 + i * BOX, u.e, fb);
-            if (SILU)
-              ptx::tma_load_3d(st(stage) + C::A_BYTES / 2 + i * BOX_BYTES, &tmW, x, P.cols + u.n0 + i * BOX, u.e, fb);
-          }
+          ptx::tma_load_3d(st(stage), &tmW, x, u.n0, u.e, fb);
+          if (SILU) ptx::tma_load_3d(st(stage) + C::UP, &tmW, x, P.cols + u.n0, u.e, fb);
           for (int i = 0; i < nb; ++i)
-            ptx::tma_load_3d(st(stage) + C::A_BYTES + i * BOX_BYTES, &tmX, x, u.row + i * BOX, 0, fb);
-          if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
+            ptx::tma_load_3d(st(stage) + a_bytes + i * BOX_BYTES, &tmX, x, u.row + i * BOX, 0, fb);
+          if (++stage == nstage) { stage = 0; ph ^= 1u; }
         }
       }
     }
@@ -223,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a0 = st(stage), b0 = a0 + C::A_BYTES;
+          const uint32_t a0 = st(stage), b0 = a0 + a_bytes;
           if constexpr (MX) {
             const uint32_t sfa = tmem_base + C::SF_COL + (set ? 16u : 0u), sfb = sfa + 8;
             const uint32_t s0 = sf(turn & 3, k % CHUNK);
@@ -247,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
             ptx::mma_commit(ptx::smem_u32(&sf_empty[turn & 3]));
             ++turn;
           }
-          if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
+          if (++stage == nstage) { stage = 0; ph ^= 1u; }
         }
         if (!ok) break;
         ptx::mma_commit(ptx::smem_u32(&tfull_bar[acc]));
@@ -370,6 +360,22 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
   }
 }
 
+// Columns per unit: the largest number of rounds times (columns + the cost of a unit, about that of
+// 8 columns) is smallest; of equals the larger.
+int unit_columns(long heads, int cols, int most) {
+  int best = most;
+  long cost = 1L << 62;
+  for (int f = most; f >= BOX; f -= BOX) {
+    const long units = heads * ((cols + f - 1) / f), ctas = num_sms();
+    const long c = (units + ctas - 1) / ctas * (f + 8);
+    if (c < cost) {
+      cost = c;
+      best = f;
+    }
+  }
+  return best;
+}
+
 template <bool MX, bool SILU, class T>
 int launch(const CUtensorMap& w, const CUtensorMap& x, const Params& p, cudaStream_t s, const char* name) {
   if (int rc = ensure_smem_limit(grouped_few_kernel<MX, SILU, T>, Cfg<MX>::DSMEM, name)) return rc;
@@ -392,9 +398,11 @@ int launch_mx(int dtype, const CUtensorMap& w, const CUtensorMap& x, const Param
 int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s) {
   CUtensorMap tw, tx;
   int rc;
-  if ((rc = make_tmap_3d(&tw, w, 2, (uint64_t)cols, (uint64_t)a.N, (uint64_t)a.E, ROWB / 2, BOX))) return rc;
+  const int f = unit_columns(std::min(a.S, a.E), a.N, MAXF);
+  if ((rc = make_tmap_3d(&tw, w, 2, (uint64_t)cols, (uint64_t)a.N, (uint64_t)a.E, ROWB / 2, f))) return rc;
   if ((rc = make_tmap_3d(&tx, x, 2, (uint64_t)cols, (uint64_t)a.S, 1, ROWB / 2, BOX))) return rc;
   Params p{};
+  p.f = f;
   p.offsets = a.offsets;
   p.S = a.S;
   p.E = a.E;
@@ -412,9 +420,11 @@ int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int c
 int launch_mxfp4_few(const Mxfp4Args& a, cudaStream_t s) {
   CUtensorMap tw, tx;
   int rc;
-  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.E, ROWB, BOX))) return rc;
+  const int f = unit_columns(std::min(a.S, a.E), a.silu ? a.N / 2 : a.N, a.silu ? MAXF / 2 : MAXF);
+  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.E, ROWB, f))) return rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K / 2, (uint64_t)a.S, 1, ROWB, BOX))) return rc;
   Params p{};
+  p.f = f;
   p.offsets = a.offsets;
   p.x_scales = a.x_scales;
   p.w_scales = a.w_scales;

@@ -330,11 +330,15 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
  *   sorted_token_ids of moe_align_by_expert); an entry outside [0, T) gives a
  *   zero row and sets MOE_STATUS_BAD_INDEX. Null: row r from x[r], R == T.
  *   codes [R, K / 2], scales [R, K / 32] bytes out.
+ *   ws / ws_bytes: at least moe_mxfp4_quantize_workspace_size(...) bytes (0
+ *   without rows; with many rows per source row, the quantised source rows).
  * moe_mxfp4_dequantize writes the values (code value * 2^s, rounded once to
  * dtype: exact in float32 and bf16, and in float16 within its range).
  */
+MOE_API size_t moe_mxfp4_quantize_workspace_size(int T, int K, int with_rows, int R);
 MOE_API int moe_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows_or_null, int R,
-                               uint8_t* codes, uint8_t* scales, int32_t* status, void* stream);
+                               uint8_t* codes, uint8_t* scales, void* ws, size_t ws_bytes, int32_t* status,
+                               void* stream);
 MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype,
                                  void* out, void* stream);
 

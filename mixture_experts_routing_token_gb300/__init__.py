@@ -17,6 +17,7 @@ from ._binding import (  # noqa: F401
     moe_grouped_gemm, moe_grouped_gemm_backward, moe_grouped_gemm_backward_workspace_size,
     moe_grouped_gemm_workspace_size, moe_mxfp4_dequantize, moe_mxfp4_grouped_gemm,
     moe_mxfp4_grouped_gemm_workspace_size, moe_mxfp4_quantize,
+    moe_mxfp4_quantize_workspace_size,
     moe_gather_rows, moe_ep_receive_index, moe_ep_combine,
     profiler_enable, profiler_report, set_wait_limit_ns, version,
 )

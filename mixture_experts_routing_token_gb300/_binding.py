@@ -48,7 +48,8 @@ SIGNATURES = {
     "moe_grouped_gemm": (_i, [_p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _sz, _p, _p]),
     "moe_grouped_gemm_backward_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "moe_grouped_gemm_backward": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _sz, _p, _p]),
-    "moe_mxfp4_quantize": (_i, [_p, _i, _i, _i, _p, _i, _p, _p, _p, _p]),
+    "moe_mxfp4_quantize_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_mxfp4_quantize": (_i, [_p, _i, _i, _i, _p, _i, _p, _p, _p, _sz, _p, _p]),
     "moe_mxfp4_dequantize": (_i, [_p, _p, _i, _i, _i, _p, _p]),
     "moe_mxfp4_grouped_gemm_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "moe_mxfp4_grouped_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _sz, _p, _p]),
@@ -486,7 +487,11 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
     return d_x, d_w
 
 
-def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, status=None, stream=None):
+def moe_mxfp4_quantize_workspace_size(T, K, with_rows, R) -> int:
+    return int(lib().moe_mxfp4_quantize_workspace_size(T, K, int(bool(with_rows)), R))
+
+
+def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, workspace=None, status=None, stream=None):
     """4-bit microscaled rows of ``x [T, K]`` (K % 32 == 0) -> (codes [R, K/2] uint8, scales [R, K/32] uint8).
 
     Blocks of 32 values share the power of two ``2^(scale - 127)``; two codes to a byte, the first one low.
@@ -508,8 +513,12 @@ def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, status=None, strea
         R = lead[0]
     codes, cp = _give(codes, "codes", (*lead, K // 2), torch.uint8, d)
     scales, sp = _give(scales, "scales", (*lead, K // 32), torch.uint8, d)
-    _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(xp, dt, T, K, rp, R, cp, sp, _status_ptr(status, d),
-                                                          _stream(stream, d)))
+    L = lib()
+    ws, ws_bytes, _keep = None, 0, None
+    if rows is not None:
+        ws, ws_bytes, _keep = _workspace(workspace, L.moe_mxfp4_quantize_workspace_size(T, K, 1, R), d)
+    _check("moe_mxfp4_quantize", L.moe_mxfp4_quantize(xp, dt, T, K, rp, R, cp, sp, ws, ws_bytes,
+                                                      _status_ptr(status, d), _stream(stream, d)))
     return codes, scales
 
 

@@ -709,8 +709,14 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
   return MOE_OK;
 }
 
+MOE_API size_t moe_mxfp4_quantize_workspace_size(int T, int K, int with_rows, int R) {
+  if (T < 1 || K < 32 || R < 1) return 0;
+  return mxfp4_quantize_workspace(T, K, with_rows != 0, R);
+}
+
 MOE_API int moe_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows_or_null, int R,
-                               uint8_t* codes, uint8_t* scales, int32_t* status, void* stream) {
+                               uint8_t* codes, uint8_t* scales, void* ws, size_t ws_bytes, int32_t* status,
+                               void* stream) {
   g_err[0] = 0;
   int rc;
   if ((rc = check_any_dtype(dtype))) return rc;
@@ -722,8 +728,9 @@ MOE_API int moe_mxfp4_quantize(const void* x, int dtype, int T, int K, const int
   if ((rc = check_tensor(codes, (long)R * K, "codes"))) return rc;
   if ((rc = check_tensor(scales, (long)R * K, "scales"))) return rc;
   if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_mxfp4_quantize_workspace_size(T, K, rows_or_null != nullptr, R)))) return rc;
   if (R == 0 || K == 0) return MOE_OK;
-  return launch_mxfp4_quantize(x, dtype, T, K, rows_or_null, R, codes, scales, status, (cudaStream_t)stream);
+  return launch_mxfp4_quantize(x, dtype, T, K, rows_or_null, R, codes, scales, ws, status, (cudaStream_t)stream);
 }
 
 MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype,

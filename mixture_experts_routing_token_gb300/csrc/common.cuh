@@ -248,8 +248,9 @@ inline bool grouped_few_rows(int S, int E) { return S <= 32L * E; }
 int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s);
 
 // 4-bit microscaled values (mxfp4.cu): codes [rows, K / 2], scales [rows, K / 32].
+size_t mxfp4_quantize_workspace(int T, int K, bool with_rows, int R);
 int launch_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows, int R, uint8_t* codes,
-                          uint8_t* scales, int32_t* status, cudaStream_t s);
+                          uint8_t* scales, void* ws, int32_t* status, cudaStream_t s);
 int launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int R, int K, int dtype, void* out,
                             cudaStream_t s);
 struct Mxfp4Args {

@@ -4,16 +4,18 @@
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
 //   GRADW  d_w[e, n, k] = sum over p of e of d_y[p, n] x[p, k]
 //
-// One CTA computes 64 x 64 outputs of one expert; 16 steps of the reduction at a time
-// go through shared memory, each thread keeps 4 x 4 sums in registers.
-// Products and sums are float32 fused multiply-adds in ascending order of the
-// reduction index, so results do not depend on the launch.
+// One CTA of 64 threads computes 64 x 64 outputs of one expert, 8 x 8 per thread: a step of the
+// reduction reads 16 values from shared memory for 64 fused multiply-adds. 16 steps at a time go
+// through one of two buffers; the next 16 are in registers on their way meanwhile, so a turn has
+// one barrier and no exposed load. Products and sums are float32 in ascending order of the
+// reduction index, so results do not depend on the launch. Bound by the FMA pipes.
 #include "grouped.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16, TT = 256;
+constexpr int TM = 64, TN = 64, TK = 16, TT = 64;
+constexpr int LOADS = TM * TK / TT;      // values of each operand a thread moves per turn
 
 enum { ROWS = 0, GRADX = 1, GRADW = 2 };
 
@@ -28,7 +30,7 @@ struct SimtParams {
 
 template <int MODE>
 __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
-  __shared__ float sa[TK][TM + 4], sb[TK][TN + 4];
+  __shared__ __align__(16) float sa[2][TK][TM + 4], sb[2][TK][TN + 4];
   __shared__ grouped::Groups G;
   const int tid = threadIdx.x;
   const int cols = MODE == ROWS ? P.N : P.K;           // columns of the output
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   if (G.bad && blockIdx.x == 0 && tid == 0 && P.status) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
   const float *A = P.a, *B = P.b;
   float* out = P.out;
-  const int tx = tid & 15, ty = tid >> 4;
+  const int tx = tid & 7, ty = tid >> 3;
   for (int t = blockIdx.x; t < G.start[P.E]; t += gridDim.x) {
     const int e = grouped::find(G.start, P.E, t);
     const grouped::Span g = G.span(e);
@@ -49,47 +51,68 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
     const int m0 = local / NT * TM, n0 = (local - local / NT * NT) * TN;
     const int red = MODE == ROWS ? P.K : MODE == GRADX ? P.N : g.rows();
     const int mcount = MODE == GRADW ? P.N : g.rows();
-    float acc[4][4] = {};
-    for (int r0 = 0; r0 < red; r0 += TK) {
-      for (int i = tid; i < TM * TK; i += TT) {
-        const int m = MODE == GRADW ? i % TM : i / TK, r = MODE == GRADW ? i / TM : i % TK;
-        float v = 0.0f;
-        if (m0 + m < mcount && r0 + r < red) {
-          const long row = MODE == GRADW ? g.lo + r0 + r : g.lo + m0 + m;
-          v = A[MODE == ROWS ? row * P.K + r0 + r : row * P.N + (MODE == GRADW ? m0 + m : r0 + r)];
-        }
-        sa[r][m] = v;
+    // Thread t moves values i = t, t + 64, ...: along the operand's contiguous index within a warp.
+    // Reduction-contiguous (x, w, d_y rows): r = t % 16, row t / 16 + 4 q; else column t, r = q.
+    constexpr bool A_RED = MODE != GRADW, B_RED = MODE == ROWS;
+    const int ra = A_RED ? tid % TK : 0, ma = A_RED ? tid / TK : tid;
+    const int rb = B_RED ? tid % TK : 0, nb = B_RED ? tid / TK : tid;
+    const long lda = MODE == ROWS ? P.K : P.N, ldb = P.K;
+    const float* at = A + (A_RED ? (long)(g.lo + m0 + ma) * lda + ra : (long)g.lo * lda + m0 + ma);
+    const float* bt = B + (MODE == ROWS    ? ((long)e * P.N + n0 + nb) * ldb + rb
+                           : MODE == GRADX ? (long)e * P.N * ldb + n0 + nb
+                                           : (long)g.lo * ldb + n0 + nb);
+    float pa[LOADS], pb[LOADS];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) {
+        const bool a_in = A_RED ? m0 + ma + 4 * q < mcount && r0 + ra < red : m0 + ma < mcount && r0 + q < red;
+        const bool b_in = B_RED ? n0 + nb + 4 * q < cols && r0 + rb < red : n0 + nb < cols && r0 + q < red;
+        pa[q] = a_in ? __ldg(at + (A_RED ? 4 * q * lda + r0 : (long)(r0 + q) * lda)) : 0.0f;
+        pb[q] = b_in ? __ldg(bt + (B_RED ? 4 * q * ldb + r0 : (long)(r0 + q) * ldb)) : 0.0f;
       }
-      for (int i = tid; i < TN * TK; i += TT) {
-        const int n = MODE == ROWS ? i / TK : i % TN, r = MODE == ROWS ? i % TK : i / TN;
-        float v = 0.0f;
-        if (n0 + n < cols && r0 + r < red) {
-          const long row = MODE == ROWS ? (long)e * P.N + n0 + n : MODE == GRADX ? (long)e * P.N + r0 + r : g.lo + r0 + r;
-          v = B[row * P.K + (MODE == ROWS ? r0 + r : n0 + n)];
-        }
-        sb[r][n] = v;
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) {
+        sa[buf][A_RED ? ra : q][A_RED ? ma + 4 * q : ma] = pa[q];
+        sb[buf][B_RED ? rb : q][B_RED ? nb + 4 * q : nb] = pb[q];
       }
-      __syncthreads();
+    };
+    float acc[8][8] = {};
+    fetch(0);
+    __syncthreads();       // the previous tile's last reads
+    put(0);
+    __syncthreads();
+    int buf = 0;
+    for (int r0 = 0; r0 < red; r0 += TK, buf ^= 1) {
+      const bool more = r0 + TK < red;
+      if (more) fetch(r0 + TK);
 #pragma unroll
       for (int r = 0; r < TK; ++r) {
-        const float4 a4 = *reinterpret_cast<const float4*>(&sa[r][ty * 4]);
-        const float4 b4 = *reinterpret_cast<const float4*>(&sb[r][tx * 4]);
-        const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
+        const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8]);
+        const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8 + 4]);
+        const float4 b0 = *reinterpret_cast<const float4*>(&sb[buf][r][tx * 4]);
+        const float4 b1 = *reinterpret_cast<const float4*>(&sb[buf][r][tx * 4 + 32]);
+        const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+          for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
       }
-      __syncthreads();
+      if (more) {
+        put(buf ^ 1);
+        __syncthreads();
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+      const int m = m0 + ty * 8 + i;
       if (m >= mcount) continue;
       const long row = MODE == GRADW ? (long)e * P.N + m : g.lo + m;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
+      for (int j = 0; j < 8; ++j) {
+        const int n = n0 + tx * 4 + (j & 3) + (j >> 2) * 32;
         if (n < cols) out[row * cols + n] = acc[i][j];
       }
     }
@@ -102,7 +125,7 @@ template <int MODE>
 int launch(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
   const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt : ((long)(p.S + TM - 1) / TM + p.E) * nt;
-  const long most = (long)num_sms() * 8;
+  const long most = (long)num_sms() * 6;
   ProfScope ps(name, s);
   grouped_simt_kernel<MODE><<<(unsigned)(tiles < most ? tiles : most), TT, 0, s>>>(p);
   return check_launch(name);

@@ -284,6 +284,24 @@ def test_quantize_rows(moe):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("K", [2048, 1056, 1120])
+def test_quantize_rows_many_times(moe, K):
+    """Each row wanted several times: quantised once, then copied."""
+    x, _ = draw((700, K), "bf16", 2)
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randint(0, 700, (6000,), dtype=torch.int32, generator=g)
+    rows[17], rows[5999] = -4, 700
+    assert moe.moe_mxfp4_quantize_workspace_size(700, K, True, 6000) > 0
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    codes, scales = moe.moe_mxfp4_quantize(x, rows=rows.to(DEV), status=status)
+    assert int(status.item()) == moe.MOE_STATUS_BAD_INDEX
+    all_c, all_s = moe.moe_mxfp4_quantize(x)
+    good = (rows >= 0) & (rows < 700)
+    at = torch.where(good, rows, 0).long().to(DEV)
+    keep = good.to(DEV)[:, None]
+    assert torch.equal(codes, all_c[at] * keep) and torch.equal(scales, all_s[at] * keep)
+
+
 SHAPES4 = [
     ([1], 0, 32, 16),
     ([0, 3, 0], 0, 64, 256),

@@ -50,11 +50,11 @@ def test_workspace_sizes(moe):
 def test_quantize_sizes_and_types(moe):
     f = moe.lib().moe_mxfp4_quantize
     one = ctypes.c_void_p(16)
-    assert f(one, 5, 4, 32, None, 4, one, one, None, None) == BAD
-    assert f(one, 0, 4, 33, None, 4, one, one, None, None) == BAD and "multiple of 32" in err(moe)
-    assert f(one, 0, 4, 32, None, 5, one, one, None, None) == BAD and "R must equal T" in err(moe)
-    assert f(one, 0, -4, 32, one, 5, one, one, None, None) == BAD
-    assert f(None, 0, 0, 32, None, 0, None, None, None, None) == 0
+    assert f(one, 5, 4, 32, None, 4, one, one, None, 0, None, None) == BAD
+    assert f(one, 0, 4, 33, None, 4, one, one, None, 0, None, None) == BAD and "multiple of 32" in err(moe)
+    assert f(one, 0, 4, 32, None, 5, one, one, None, 0, None, None) == BAD and "R must equal T" in err(moe)
+    assert f(one, 0, -4, 32, one, 5, one, one, None, 0, None, None) == BAD
+    assert f(None, 0, 0, 32, None, 0, None, None, None, 0, None, None) == 0
     g = moe.lib().moe_mxfp4_dequantize
     assert g(one, one, 4, 48, 1, one, None) == BAD and g(one, one, -1, 32, 1, one, None) == BAD
     assert g(None, None, 0, 32, 2, None, None) == 0

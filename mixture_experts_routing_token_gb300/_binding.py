@@ -420,13 +420,26 @@ def _status_ptr(status, device):
     return p
 
 
-def _workspace(workspace, need, device):
-    """(address, bytes, tensor) of the caller's workspace or of a new one; nothing when none is needed."""
+def _raw(stream, device):
+    """Handle of the caller's stream or of the current one, as an integer."""
+    if stream is None and _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return _stream(stream, device).value
+
+
+def _call(fn, name, size, device, workspace, before, after):
+    """fn(*before, ws, ws_bytes, *after), with a workspace of ``size()`` bytes made here when the call
+    needs one and the caller gave none (most calls need none: the library is asked first)."""
     if workspace is None:
-        if not need:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return _take(workspace, "workspace", workspace.dtype, device), workspace.numel() * workspace.element_size(), workspace
+        rc = fn(*before, None, 0, *after)
+        if rc == MOE_ERR_WORKSPACE:
+            workspace = torch.empty(size(), dtype=torch.uint8, device=device)
+            rc = fn(*before, workspace.data_ptr(), workspace.numel(), *after)
+    else:
+        p = _take(workspace, "workspace", workspace.dtype, device)
+        rc = fn(*before, p, workspace.numel() * workspace.element_size(), *after)
+    if rc:
+        _check(name, rc)
 
 
 def moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E) -> int:
@@ -450,10 +463,8 @@ def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, strea
     if Kw != K or offsets.shape != (E + 1,):
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
     out, yp = _give(out, "out", (S, N), dtype, d)
-    L = lib()
-    ws, ws_bytes, _keep = _workspace(workspace, L.moe_grouped_gemm_workspace_size(dt, S, K, N, E), d)
-    _check("moe_grouped_gemm", L.moe_grouped_gemm(xp, wp, dt, S, K, N, E, op, yp, ws, ws_bytes,
-                                                  _status_ptr(status, d), _stream(stream, d)))
+    _call(lib().moe_grouped_gemm, "moe_grouped_gemm", lambda: moe_grouped_gemm_workspace_size(dt, S, K, N, E), d, workspace,
+          (xp, wp, dt, S, K, N, E, op, yp), (_status_ptr(status, d), _raw(stream, d)))
     return out
 
 
@@ -480,10 +491,9 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
     d_x, dxp = _give(d_x, "d_x", (S, K), dtype, d) if want_d_x else (None, None)
     d_w, dwp = _give(d_w, "d_w", (E, N, K), dtype, d) if want_d_w else (None, None)
-    L = lib()
-    ws, ws_bytes, _keep = _workspace(workspace, L.moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d)
-    _check("moe_grouped_gemm_backward", L.moe_grouped_gemm_backward(
-        xp, wp, gp, dt, S, K, N, E, op, dxp, dwp, ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
+    _call(lib().moe_grouped_gemm_backward, "moe_grouped_gemm_backward",
+          lambda: moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d, workspace,
+          (xp, wp, gp, dt, S, K, N, E, op, dxp, dwp), (_status_ptr(status, d), _raw(stream, d)))
     return d_x, d_w
 
 
@@ -513,12 +523,8 @@ def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, workspace=None, st
         R = lead[0]
     codes, cp = _give(codes, "codes", (*lead, K // 2), torch.uint8, d)
     scales, sp = _give(scales, "scales", (*lead, K // 32), torch.uint8, d)
-    L = lib()
-    ws, ws_bytes, _keep = None, 0, None
-    if rows is not None:
-        ws, ws_bytes, _keep = _workspace(workspace, L.moe_mxfp4_quantize_workspace_size(T, K, 1, R), d)
-    _check("moe_mxfp4_quantize", L.moe_mxfp4_quantize(xp, dt, T, K, rp, R, cp, sp, ws, ws_bytes,
-                                                      _status_ptr(status, d), _stream(stream, d)))
+    _call(lib().moe_mxfp4_quantize, "moe_mxfp4_quantize", lambda: moe_mxfp4_quantize_workspace_size(T, K, rows is not None, R),
+          d, workspace, (xp, dt, T, K, rp, R, cp, sp), (_status_ptr(status, d), _raw(stream, d)))
     return codes, scales
 
 
@@ -534,7 +540,9 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     if scales.shape != (*lead, K // 32):
         raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32]")
     out, op = _give(out, "out", (*lead, K), dtype, d)
-    _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(cp, sp, lead.numel(), K, dt, op, _stream(stream, d)))
+    rc = lib().moe_mxfp4_dequantize(cp, sp, lead.numel(), K, dt, op, _raw(stream, d))
+    if rc:
+        _check("moe_mxfp4_dequantize", rc)
     return out
 
 
@@ -574,10 +582,9 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
             raise ValueError("silu_and_mul needs an even N")
         cols, act = N // 2, MOE_ACT_SILU_AND_MUL
     out, yp = _give(out, "out", (S, cols), out_dtype, d)
-    L = lib()
-    ws, ws_bytes, _keep = _workspace(workspace, L.moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, act), d)
-    _check("moe_mxfp4_grouped_gemm", L.moe_mxfp4_grouped_gemm(
-        xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, ws, ws_bytes, _status_ptr(status, d), _stream(stream, d)))
+    _call(lib().moe_mxfp4_grouped_gemm, "moe_mxfp4_grouped_gemm",
+          lambda: moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation), d, workspace,
+          (xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp), (_status_ptr(status, d), _raw(stream, d)))
     return out
 
 

@@ -699,7 +699,7 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
   a.offsets = offsets;
   a.ws = ws;
   a.status = status;
-  if (K == 0) return MOE_OK;
+  if (K == 0 || (!d_x_or_null && !d_w_or_null)) return MOE_OK;
   if (N == 0) return d_x_or_null ? zero_out(d_x_or_null, (size_t)S * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
   if (S == 0)
     return d_w_or_null ? zero_out(d_w_or_null, (size_t)E * N * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;

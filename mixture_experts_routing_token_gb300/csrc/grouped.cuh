@@ -82,6 +82,19 @@ __device__ __forceinline__ int find(const int* start, int E, int t) {
   return lo;
 }
 
+// The same for a t that grows from call to call; `e` is the last answer (0 at first).
+__device__ __forceinline__ int find_from(const int* start, int e, int t) {
+  while (start[e + 1] <= t) ++e;
+  return e;
+}
+
+// n / d for n >= 0, d > 0. The float32 quotient of (n + 1/2) is off by less than 2^-22 of itself, the
+// true one at least 1/(2 d) from the next integer, so below 2^21 its whole part is exact; a tenth of
+// the integer division's cycles, which the roles would wait for at every tile.
+__device__ __forceinline__ int quick_div(int n, int d) {
+  return n < (1 << 21) ? (int)__fdividef((float)n + 0.5f, (float)d) : n / d;
+}
+
 // Rows that no group owns (before the first offset, from the last one on) are zero in row
 // outputs. Thread `i` of `n` writes its share of them.
 template <class T>
@@ -141,6 +154,52 @@ __device__ __forceinline__ void store_cols(T* row, int c, int cols, int vec, con
 #pragma unroll
     for (int i = 0; i < W; ++i)
       if (c + i < cols) row[c + i] = from_float<T>(__uint_as_float(y[i]));
+  }
+}
+
+// Rows of an accumulator, one per lane, to the output through 4 KB of shared memory of the warp's
+// own: `q` holds 128 bytes of a row (packed values of columns c ..), and each store instruction
+// writes four whole 128-byte pieces of rows, where lanes that stored their own rows would touch 32
+// lines with every instruction (measured on the 4-bit product with a float16 output of 328 MB:
+// 156 us so, of which the stores were 32). The first `count` of the warp's 32 rows are stored; `row0`
+// is the output's row of lane 0, `ncols` columns from c on are meant. Needs rows that are a multiple
+// of 16 bytes, 16-byte aligned. The 16-byte pieces are kept in an order that depends
+// on the row, so neither side meets bank conflicts.
+template <class T>
+__device__ __forceinline__ void store_rows(uint32_t buf, const uint32_t (&q)[32], T* row0, int count, int c, int ncols,
+                                           int cols) {
+  constexpr int EP = 16 / (int)sizeof(T);      // values per piece
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                 "r"(q[4 * p]), "r"(q[4 * p + 1]), "r"(q[4 * p + 2]), "r"(q[4 * p + 3])
+                 : "memory");
+  __syncwarp();
+  const int p = lane & 7, col = c + p * EP;
+  const bool in = p * EP < ncols && col < cols;     // pieces are whole: cols is a multiple of EP
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(buf + r * 128 + ((p ^ (r & 7)) << 4))
+                 : "memory");
+    if (in && r < count) *reinterpret_cast<uint4*>(row0 + (long)r * cols + col) = v;
+  }
+  __syncwarp();
+}
+
+// W float32 sums (as bits) as words of T.
+template <class T, int W>
+__device__ __forceinline__ void pack_words(const uint32_t (&y)[W], uint32_t* q) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) q[i] = y[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) q[i] = pack_pair<T>(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
   }
 }
 

@@ -73,10 +73,10 @@ struct Unit {
 
 __device__ __forceinline__ Unit unit_at(int t, const grouped::Groups& G, const Params& P, int f, int tiles) {
   // G.start counts heads; the heads of an expert that share a column tile follow each other
-  const int e = grouped::find(G.start, P.E, t / tiles);
+  const int e = grouped::find(G.start, P.E, grouped::quick_div(t, tiles));
   const grouped::Span g = G.span(e);
   const int heads = G.start[e + 1] - G.start[e], local = t - G.start[e] * tiles;
-  const int tile = local / heads, head = local - tile * heads;
+  const int tile = grouped::quick_div(local, heads), head = local - tile * heads;
   Unit u;
   u.e = e;
   u.row = g.lo + head * MAXR;

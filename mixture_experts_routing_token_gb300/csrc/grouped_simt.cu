@@ -7,7 +7,8 @@
 // One CTA of 64 threads computes 64 x 64 outputs of one expert, 8 x 8 per thread: a step of the
 // reduction reads 16 values from shared memory for 64 fused multiply-adds. 16 steps at a time go
 // through one of two buffers; the next 16 are in registers on their way meanwhile, so a turn has
-// one barrier and no exposed load. Products and sums are float32 in ascending order of the
+// one barrier and no exposed load. The multiply-adds are issued in pairs (fma.f32x2, two columns),
+// which leaves issue slots for everything else beside a full FMA pipe. Products and sums are float32 in ascending order of the
 // reduction index, so results do not depend on the launch. Bound by the FMA pipes.
 #include "grouped.cuh"
 
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
         sb[buf][B_RED ? rb : q][B_RED ? nb + 4 * q : nb] = pb[q];
       }
     };
-    float acc[8][8] = {};
+    uint64_t acc[8][4] = {};       // pairs of columns
     fetch(0);
     __syncthreads();       // the previous tile's last reads
     put(0);
@@ -91,14 +92,17 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
       for (int r = 0; r < TK; ++r) {
         const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8]);
         const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8 + 4]);
-        const float4 b0 = *reinterpret_cast<const float4*>(&sb[buf][r][tx * 4]);
-        const float4 b1 = *reinterpret_cast<const float4*>(&sb[buf][r][tx * 4 + 32]);
+        const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[buf][r][tx * 4]);
+        const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&sb[buf][r][tx * 4 + 32]);
         const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        const uint64_t bv[4] = {b0.x, b0.y, b1.x, b1.y};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+          uint64_t aa;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(av[i]));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+          for (int j = 0; j < 4; ++j) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][j]) : "l"(aa), "l"(bv[j]));
+        }
       }
       if (more) {
         put(buf ^ 1);
@@ -113,7 +117,8 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int n = n0 + tx * 4 + (j & 3) + (j >> 2) * 32;
-        if (n < cols) out[row * cols + n] = acc[i][j];
+        const uint64_t pair = acc[i][j >> 1];
+        if (n < cols) out[row * cols + n] = __uint_as_float((uint32_t)(j & 1 ? pair >> 32 : pair));
       }
     }
   }

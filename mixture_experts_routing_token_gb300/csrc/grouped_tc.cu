@@ -1,14 +1,18 @@
 // Products grouped by expert on SM pairs, bf16 and float16 (tcgen05.mma.cta_group::2,
 // M = 256 x N = 256 x K = 16, float32 accumulators in both SMs' TMEM).
 //
-//   ROWS   y[p, n]      = sum_k x[p, k] w[e, n, k]        A = x rows, B = w rows (both K-major)
-//   GRADX  d_x[p, k]    = sum_n d_y[p, n] w[e, n, k]      A = d_y rows, B = w (MN-major)
-//   GRADW  d_w[e, n, k] = sum over p of e of d_y[p, n] x[p, k]   A = d_y, B = x (both MN-major)
+//   y[p, n]      = sum_k x[p, k] w[e, n, k]               A = x rows, B = w rows (both K-major)
+//   d_x[p, k]    = sum_n d_y[p, n] w[e, n, k]             A = d_y rows, B = w (MN-major)
+//   d_w[e, n, k] = sum over p of e of d_y[p, n] x[p, k]   A = d_y, B = x (both MN-major)
+//
+// The two gradients are the tiles of one launch, the ones with the longer reduction first: small
+// problems fill the SMs better and pay one start (1554 rows, 16 experts of [714, 1000]: two launches
+// took 28 us).
 //
 // Each SM of a 2-CTA cluster loads its own 128 of A's 256 rows and one half of B's 256
 // per step of 64 of the reduction (32 KB per SM and step, six steps in flight) and holds
 // its 128 rows x 256 columns of the result, twice, so the epilogue of a tile runs under
-// the next tile's products. A tile is 256 rows of one expert (GRADW: 256 x 256 of its
+// the next tile's products. A tile is 256 rows of one expert (d_w: 256 x 256 of its
 // matrix). Bound by the tensor cores at prompt sizes; where experts have few rows, by
 // the bytes of the weights.
 //
@@ -17,13 +21,13 @@
 //     or column is zero fill, not the next expert;
 //   - rows past a group's end inside a tile are the next expert's, but reach only their
 //     own rows of the result, which are not stored;
-//   - GRADW reduces over rows, so those rows have to count nothing even if they hold NaN.
+//   - d_w reduces over rows, so those rows have to count nothing even if they hold NaN.
 //     Its last step of a group arrives on a barrier of the CTA's own; a warp (tail) clears
 //     the rows past the end in shared memory (whole 128-byte lines, so the swizzle does
 //     not matter) and only then hands the step to the MMA issuer.
 //
 // Barriers as in the FFN's pair kernel: full[s] in the leader CTA (the pair's bytes, and in
-// GRADW one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
+// the gradients one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
 // accumulator. Every wait is bounded.
 #include <algorithm>
 
@@ -42,63 +46,88 @@ constexpr int NSTAGE = 6;
 constexpr int A_BYTES = BM * BK * 2;    // 16 KB
 constexpr int B_BYTES = (BN / 2) * BK * 2;
 constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int DSMEM = NSTAGE * STAGE + 1024;
 constexpr int EPI_WARPS = 4;
+constexpr int DSMEM = NSTAGE * STAGE + EPI_WARPS * 4096 + 1024;    // the ring, the epilogue's buffers
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint64_t DRAIN_NS = 2000000000ull;    // issued MMAs and copies
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;      // bytes between the two 64-column boxes of an MN-major operand
 
-enum { ROWS = 0, GRADX = 1, GRADW = 2 };
+template <bool GRAD>
+constexpr int threads() { return (2 + EPI_WARPS + (GRAD ? 1 : 0)) * 32; }
 
-template <int MODE>
-constexpr int threads() { return (2 + EPI_WARPS + (MODE == GRADW ? 1 : 0)) * 32; }
+// One product over the groups.
+struct Job {
+  int R;            // length of the reduction; d_w: the group's rows (0 here)
+  int C, NT;        // columns of the result, tiles of them
+  int M, MT;        // d_w: rows of an expert's result, tiles of them
+  void* out;        // null: not wanted
+  int vec;          // stores: > 0 = rows are a multiple of 16 bytes, 0 = single values
+  uint32_t idesc;
+};
 
 struct Params {
   const int32_t* offsets;
   int S, E;
-  int R;            // length of the reduction (K: ROWS, N: GRADX); GRADW: the group's rows
-  int M, C;         // GRADW: rows of an expert's result; columns of the result
-  int MT, NT;       // tiles: GRADW rows, columns
-  void* out;
-  int vec;          // stores: 2 = 32-byte sectors, 1 = 16 bytes, 0 = single values
-  uint32_t idesc;
+  Job rows;         // y or d_x
+  Job dw;           // d_w
+  int dw_first;
   int32_t* status;
   uint64_t wait_ns;
 };
 
 struct Tile {
+  bool dw;
   int e, m, n, steps;
   grouped::Span g;
 };
 
-template <int MODE>
-__device__ __forceinline__ int tiles_of(int rows, const Params& P) {
-  return MODE == GRADW ? P.MT * P.NT : (rows + 2 * BM - 1) / (2 * BM) * P.NT;
-}
+// Where a role is in the list of tiles: experts of its last tiles of either kind.
+struct At {
+  int e_rows = 0, e_dw = 0;
+};
 
 // Tile t. Tiles of an expert that run together share the operand with fewer tiles, which
 // stays in L2, while the other one is walked once.
-template <int MODE>
-__device__ __forceinline__ Tile tile_at(int t, const grouped::Groups& G, const Params& P) {
+template <bool GRAD>
+__device__ __forceinline__ Tile tile_at(int t, At& at, const grouped::Groups& G, int dw_tiles, const Params& P) {
   Tile d;
-  d.e = grouped::find(G.start, P.E, t);
-  d.g = G.span(d.e);
-  const int local = t - G.start[d.e];
-  const int mt = MODE == GRADW ? P.MT : (d.g.rows() + 2 * BM - 1) / (2 * BM);
-  if (mt > P.NT) {
-    d.m = local / P.NT;
-    d.n = local - d.m * P.NT;
+  const int row_tiles = G.start[P.E];
+  d.dw = GRAD && (P.dw_first ? t < dw_tiles : t >= row_tiles);
+  int mt, local;
+  if (d.dw) {
+    if (!P.dw_first) t -= row_tiles;
+    const int per = P.dw.MT * P.dw.NT;
+    while (t >= (at.e_dw + 1) * per) ++at.e_dw;
+    d.e = at.e_dw;
+    d.g = G.span(d.e);
+    local = t - d.e * per;
+    mt = P.dw.MT;
+    d.steps = (d.g.rows() + BK - 1) / BK;
   } else {
-    d.n = local / mt;
+    if (P.dw_first) t -= dw_tiles;
+    at.e_rows = grouped::find_from(G.start, at.e_rows, t);
+    d.e = at.e_rows;
+    d.g = G.span(d.e);
+    local = t - G.start[d.e];
+    mt = (d.g.rows() + 2 * BM - 1) / (2 * BM);
+    d.steps = (P.rows.R + BK - 1) / BK;
+  }
+  const int NT = d.dw ? P.dw.NT : P.rows.NT;
+  if (mt > NT) {
+    d.m = grouped::quick_div(local, NT);
+    d.n = local - d.m * NT;
+  } else {
+    d.n = grouped::quick_div(local, mt);
     d.m = local - d.n * mt;
   }
-  d.steps = ((MODE == GRADW ? d.g.rows() : P.R) + BK - 1) / BK;
   return d;
 }
 
-template <int MODE, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
+// GRAD = false: P.rows is y, tmA / tmB its operands. GRAD: P.rows is d_x (tmA, tmB), P.dw d_w (tmC, tmD).
+template <bool GRAD, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
     grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
                         const Params P) {
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE], tail_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
@@ -118,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
 
   if (tid == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), MODE == GRADW ? 2 : 1);
+      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), GRAD ? 2 : 1);
       ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&tail_bar[s]), 1);
     }
@@ -133,6 +162,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmB);
+    if (GRAD) {
+      ptx::prefetch_tmap(&tmC);
+      ptx::prefetch_tmap(&tmD);
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -144,57 +177,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2)
-    grouped::group_list(P.offsets, P.E, P.S, [&](int rows) { return tiles_of<MODE>(rows, P); }, G);
+    grouped::group_list(P.offsets, P.E, P.S,
+                        [&](int rows) { return P.rows.out ? (rows + 2 * BM - 1) / (2 * BM) * P.rows.NT : 0; }, G);
   ptx::tc_fence_before();
   __syncthreads();
   cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  const int total = G.start[P.E];
+  const int dw_tiles = GRAD && P.dw.out ? P.E * P.dw.MT * P.dw.NT : 0;
+  const int total = G.start[P.E] + dw_tiles;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     if (ptx::elect_one()) {
+      At at;
       int stage = 0;
       uint32_t ph = 0;
       for (int t = cluster_id; t < total; t += nclusters) {
-        const Tile ti = tile_at<MODE>(t, G, P);
-        const bool cut = MODE == GRADW && ti.g.rows() % BK != 0;
+        const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
+        const bool cut = ti.dw && ti.g.rows() % BK != 0;
+        const int xb = ti.n * BN + (int)rank * (BN / 2);
         for (int kb = 0; kb < ti.steps; ++kb) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) goto producer_done;
-          if (MODE == GRADW) {
-            const int xa = ti.m * (2 * BM) + (int)rank * BM, xb = ti.n * BN + (int)rank * (BN / 2);
-            const int y = ti.g.lo + kb * BK;
-            if (cut && kb == ti.steps - 1) {
-              const uint32_t tb = ptx::smem_u32(&tail_bar[stage]);
-              ptx::mbar_arrive_expect_tx(tb, STAGE);
-              ptx::tma_load_3d(sA(stage), &tmA, xa, y, 0, tb);
-              ptx::tma_load_3d(sA(stage) + MN_BLOCK, &tmA, xa + 64, y, 0, tb);
-              ptx::tma_load_3d(sB(stage), &tmB, xb, y, 0, tb);
-              ptx::tma_load_3d(sB(stage) + MN_BLOCK, &tmB, xb + 64, y, 0, tb);
-            } else {
-              const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
-              if (leader) {
-                ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
-                ptx::mbar_arrive(fb_local);
-              }
-              const uint32_t fb = map_to_rank(fb_local, 0);
-              tma_load_3d_pair(sA(stage), &tmA, xa, y, 0, fb);
-              tma_load_3d_pair(sA(stage) + MN_BLOCK, &tmA, xa + 64, y, 0, fb);
-              tma_load_3d_pair(sB(stage), &tmB, xb, y, 0, fb);
-              tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmB, xb + 64, y, 0, fb);
-            }
+          if (cut && kb == ti.steps - 1) {
+            const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + kb * BK;
+            const uint32_t tb = ptx::smem_u32(&tail_bar[stage]);
+            ptx::mbar_arrive_expect_tx(tb, STAGE);
+            ptx::tma_load_3d(sA(stage), &tmC, xa, y, 0, tb);
+            ptx::tma_load_3d(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, 0, tb);
+            ptx::tma_load_3d(sB(stage), &tmD, xb, y, 0, tb);
+            ptx::tma_load_3d(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, 0, tb);
           } else {
             const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
-            if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
+            if (leader) {
+              ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
+              if (GRAD) ptx::mbar_arrive(fb_local);
+            }
             const uint32_t fb = map_to_rank(fb_local, 0);
-            tma_load_3d_pair(sA(stage), &tmA, kb * BK, ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, 0, fb);
-            if (MODE == ROWS) {
-              tma_load_3d_pair(sB(stage), &tmB, kb * BK, ti.n * BN + (int)rank * (BN / 2), ti.e, fb);
+            if (GRAD && ti.dw) {
+              const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + kb * BK;
+              tma_load_3d_pair(sA(stage), &tmC, xa, y, 0, fb);
+              tma_load_3d_pair(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, 0, fb);
+              tma_load_3d_pair(sB(stage), &tmD, xb, y, 0, fb);
+              tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, 0, fb);
             } else {
-              const int x = ti.n * BN + (int)rank * (BN / 2);
-              tma_load_3d_pair(sB(stage), &tmB, x, kb * BK, ti.e, fb);
-              tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmB, x + 64, kb * BK, ti.e, fb);
+              tma_load_3d_pair(sA(stage), &tmA, kb * BK, ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, 0, fb);
+              if (GRAD) {
+                tma_load_3d_pair(sB(stage), &tmB, xb, kb * BK, ti.e, fb);
+                tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmB, xb + 64, kb * BK, ti.e, fb);
+              } else {
+                tma_load_3d_pair(sB(stage), &tmB, kb * BK, xb, ti.e, fb);
+              }
             }
           }
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
@@ -205,11 +238,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader CTA)
     if (leader && ptx::elect_one()) {
-      constexpr int A_MN = MODE == GRADW, B_MN = MODE != ROWS;
+      At at;
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       for (int t = cluster_id; t < total; t += nclusters) {
-        const Tile ti = tile_at<MODE>(t, G, P);
+        const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
+        const uint32_t idesc = ti.dw ? P.dw.idesc : P.rows.idesc;
         if (ti.steps == 0) continue;   // nothing to add up: the epilogue writes zeros
         if (!ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns)) break;
         ptx::tc_fence_after();
@@ -222,12 +256,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
           }
           ptx::tc_fence_after();
           const uint32_t a0 = sA(stage), b0 = sB(stage);
+          // descriptors of the step's first MMA; K-major operands advance 32 bytes a K = 16, MN-major 2 KB
+          const bool a_mn = GRAD && ti.dw;
+          const uint64_t ad = a_mn ? sdesc_mn128(a0, MN_BLOCK) : ptx::sdesc_k128(a0);
+          const uint64_t bd = GRAD ? sdesc_mn128(b0, MN_BLOCK) : ptx::sdesc_k128(b0);
+          const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (GRAD ? 2048u : 32u) >> 4;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = A_MN ? sdesc_mn128(a0 + kk * 2048, MN_BLOCK) : ptx::sdesc_k128(a0 + kk * 32);
-            const uint64_t bd = B_MN ? sdesc_mn128(b0 + kk * 2048, MN_BLOCK) : ptx::sdesc_k128(b0 + kk * 32);
-            mma_pair(d_tmem, ad, bd, P.idesc, (kb | kk) != 0);
-          }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
           commit_pair(ptx::smem_u32(&empty_bar[stage]), 0x3);
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
         }
@@ -243,33 +279,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int row = q * 32 + lane;
-    T* out = static_cast<T*>(P.out);
+    const uint32_t sbuf = dsmem + NSTAGE * STAGE + (uint32_t)q * 4096u;
+    At at;
     int acc = 0;
     uint32_t aph = 0;
     for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at<MODE>(t, G, P);
+      const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
+      const Job& J = ti.dw ? P.dw : P.rows;
       const int m = ti.m * (2 * BM) + (int)rank * BM + row;
-      const bool mine = m < (MODE == GRADW ? P.M : ti.g.rows());
-      T* dst = out + (MODE == GRADW ? (long)ti.e * P.M + m : (long)ti.g.lo + m) * P.C;
+      const int nrows = (ti.dw ? J.M : ti.g.rows()) - (m - lane);     // of this warp's 32 (from lane 0 on)
+      const bool mine = lane < nrows;
+      T* dst = static_cast<T*>(J.out) + (ti.dw ? (long)ti.e * J.M + m : (long)ti.g.lo + m) * J.C;
       if (ti.steps == 0) {
         uint32_t z[32] = {};
         if (mine)
-          for (int c = ti.n * BN; c < min(P.C, (ti.n + 1) * BN); c += 32) grouped::store_cols(dst, c, P.C, P.vec, z);
+          for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 32) grouped::store_cols(dst, c, J.C, J.vec, z);
         continue;
       }
       if (!ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns)) break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; c += 2) {   // two 32-column chunks per TMEM wait
+      for (int c = 0; c < BN; c += 64) {
         uint32_t y[2][32];
-        ptx::tmem_ld32(taddr + c * 32, y[0]);
-        ptx::tmem_ld32(taddr + c * 32 + 32, y[1]);
+        ptx::tmem_ld32(taddr + c, y[0]);
+        ptx::tmem_ld32(taddr + c + 32, y[1]);
         ptx::tmem_ld_wait();
+        const int c0 = ti.n * BN + c;
+        if (J.vec > 0) {
+          uint32_t words[32];
+          grouped::pack_words<T, 32>(y[0], words);
+          grouped::pack_words<T, 32>(y[1], words + 16);
+          if (nrows > 0 && c0 < J.C) grouped::store_rows(sbuf, words, dst - (long)lane * J.C, nrows, c0, 64, J.C);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c0 = ti.n * BN + (c + h) * 32;
-          if (mine && c0 < P.C) grouped::store_cols(dst, c0, P.C, P.vec, y[h]);
+          for (int h = 0; h < 2; ++h)
+            if (mine && c0 + h * 32 < J.C) grouped::store_cols(dst, c0 + h * 32, J.C, 0, y[h]);
         }
       }
       ptx::tc_fence_before();
@@ -277,20 +322,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
       if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
       if (++acc == 2) { acc = 0; aph ^= 1u; }
     }
-    if (MODE != GRADW && !*abort_p)
-      grouped::zero_unowned(out, G, P.E, P.S, P.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
+    if (P.rows.out != nullptr && !*abort_p)
+      grouped::zero_unowned(static_cast<T*>(P.rows.out), G, P.E, P.S, P.rows.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
-  } else if (MODE == GRADW) {
+  } else if (GRAD) {
     // ------------------------------------------------------------ tail (both CTAs): clears rows past a group's end
+    At at;
     int stage = 0;
     uint32_t tph = 0;                    // bit s: phase of tail_bar[s]
     for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at<MODE>(t, G, P);
+      const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
       if (ti.steps == 0) continue;
       const int s = (stage + ti.steps - 1) % NSTAGE;
       stage = (stage + ti.steps) % NSTAGE;
       const int keep = ti.g.rows() % BK;
-      if (keep == 0) continue;
+      if (!ti.dw || keep == 0) continue;
       if (!ptx::mbar_wait(ptx::smem_u32(&tail_bar[s]), (tph >> s) & 1u, abort_p, P.wait_ns)) break;
       tph ^= 1u << s;
       const int lines = (BK - keep) * 4, first = keep * 128;   // 128-byte lines to clear, in four boxes of 64
@@ -325,38 +371,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<MODE>(), 1)
 }
 static_assert(A_BYTES == 2 * (int)MN_BLOCK && B_BYTES == 2 * (int)MN_BLOCK, "a stage is four boxes of 64 x 64");
 
-template <int MODE, class T>
-int launch(const CUtensorMap& a, const CUtensorMap& b, Params p, long most_tiles, cudaStream_t s, const char* name) {
-  if (int rc = ensure_smem_limit(grouped_pair_kernel<MODE, T>, DSMEM, name)) return rc;
+template <bool GRAD, class T>
+int launch(const CUtensorMap (&m)[4], const Params& p, long most_tiles, cudaStream_t s, const char* name) {
+  if (int rc = ensure_smem_limit(grouped_pair_kernel<GRAD, T>, DSMEM, name)) return rc;
   const int grid = 2 * (int)std::max(1L, std::min(most_tiles, (long)(num_sms() / 2)));
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(grouped_pair_kernel<MODE, T>, grid, threads<MODE>(), DSMEM, s, a, b, p);
+  const cudaError_t e =
+      launch_pdl(grouped_pair_kernel<GRAD, T>, grid, threads<GRAD>(), DSMEM, s, m[0], m[1], m[2], m[3], p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }
 
-template <int MODE>
-int by_type(int dtype, const CUtensorMap& a, const CUtensorMap& b, Params& p, long most_tiles, cudaStream_t s,
-            const char* name) {
-  p.idesc = idesc_bf16_f32_major(2 * BM, BN, MODE == GRADW, MODE != ROWS);
-  if (dtype == MOE_BF16) return launch<MODE, __nv_bfloat16>(a, b, p, most_tiles, s, name);
-  p.idesc &= ~((1u << 7) | (1u << 10));   // A and B float16
-  return launch<MODE, __half>(a, b, p, most_tiles, s, name);
-}
-
-Params params(const GroupedArgs& a, int R, int C, void* out) {
-  Params p{};
-  p.offsets = a.offsets;
-  p.S = a.S;
-  p.E = a.E;
-  p.R = R;
-  p.C = C;
-  p.NT = (C + BN - 1) / BN;
-  p.out = out;
-  p.vec = grouped::store_width(out, C, 2);
-  p.status = a.status;
-  p.wait_ns = wait_limit_ns();
-  return p;
+Job job(int dtype, int R, int C, void* out, int a_mn, int b_mn) {
+  Job j{};
+  j.R = R;
+  j.C = C;
+  j.NT = (C + BN - 1) / BN;
+  j.out = out;
+  j.vec = grouped::store_width(out, C, 2);
+  j.idesc = idesc_bf16_f32_major(2 * BM, BN, a_mn, b_mn);
+  if (dtype == MOE_F16) j.idesc &= ~((1u << 7) | (1u << 10));   // A and B float16
+  return j;
 }
 
 long row_tiles(const GroupedArgs& a, int NT) { return ((long)(a.S + 2 * BM - 1) / (2 * BM) + a.E) * NT; }
@@ -423,36 +458,45 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
   if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
   if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
-  CUtensorMap ta, tb;
-  if ((rc = make_tmap_3d(&ta, x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
-  if ((rc = make_tmap_3d(&tb, w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, BK, BN / 2))) return rc;
-  Params p = params(a, a.K, a.N, a.y);
-  return by_type<ROWS>(a.dtype, ta, tb, p, row_tiles(a, p.NT), s, "grouped_gemm");
+  CUtensorMap m[4];
+  if ((rc = make_tmap_3d(&m[0], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
+  if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, BK, BN / 2))) return rc;
+  m[2] = m[3] = m[0];      // not read
+  Params p{a.offsets, a.S, a.E, job(a.dtype, a.K, a.N, a.y, 0, 0), Job{}, 0, a.status, wait_limit_ns()};
+  const long tiles = row_tiles(a, p.rows.NT);
+  return a.dtype == MOE_BF16 ? launch<false, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm")
+                             : launch<false, __half>(m, p, tiles, s, "grouped_gemm");
 }
 
 int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   Carver c(a.ws);
-  Mat dy, x, w;
-  CUtensorMap ta, tb;
+  Mat dy, x{}, w{};
+  CUtensorMap m[4] = {};
   int rc;
   if ((rc = padded(a.d_y, a.S, a.N, c, &dy, s))) return rc;
+  Params p{a.offsets, a.S, a.E, Job{}, Job{}, 0, a.status, wait_limit_ns()};
+  long tiles = 0;
   if (a.d_x) {
     if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
-    if ((rc = make_tmap_3d(&ta, dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
-    if ((rc = make_tmap_3d(&tb, w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, 64, BK))) return rc;
-    Params p = params(a, a.N, a.K, a.d_x);
-    if ((rc = by_type<GRADX>(a.dtype, ta, tb, p, row_tiles(a, p.NT), s, "grouped_gemm_dx"))) return rc;
+    if ((rc = make_tmap_3d(&m[0], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
+    if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, 64, BK))) return rc;
+    p.rows = job(a.dtype, a.N, a.K, a.d_x, 0, 1);
+    tiles += row_tiles(a, p.rows.NT);
   }
   if (a.d_w) {
     if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
-    if ((rc = make_tmap_3d(&ta, dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
-    if ((rc = make_tmap_3d(&tb, x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
-    Params p = params(a, 0, a.K, a.d_w);
-    p.M = a.N;
-    p.MT = (a.N + 2 * BM - 1) / (2 * BM);
-    if ((rc = by_type<GRADW>(a.dtype, ta, tb, p, (long)a.E * p.MT * p.NT, s, "grouped_gemm_dw"))) return rc;
+    if ((rc = make_tmap_3d(&m[2], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
+    if ((rc = make_tmap_3d(&m[3], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
+    p.dw = job(a.dtype, 0, a.K, a.d_w, 1, 1);
+    p.dw.M = a.N;
+    p.dw.MT = (a.N + 2 * BM - 1) / (2 * BM);
+    tiles += (long)a.E * p.dw.MT * p.dw.NT;
   }
-  return MOE_OK;
+  if (!a.d_x) m[0] = m[1] = m[2];      // not read
+  if (!a.d_w) m[2] = m[3] = m[0];
+  p.dw_first = a.S / a.E > a.N;
+  return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm_backward")
+                             : launch<true, __half>(m, p, tiles, s, "grouped_gemm_backward");
 }
 
 }  // namespace moe

@@ -19,8 +19,10 @@
 // were slower (prompt 328 us with, 359 us with a deeper prefetch): with one row per lane their
 // loads touch 32 lines an instruction, beside the epilogue's stores.
 //
-// Bound: the tensor cores and L2 at prompt sizes (a step moves 30 KB per SM for 448 cycles of
-// products).
+// Bound at prompt sizes: what an SM can take in. A step brings 33 KB (codes and scales) for about 490
+// cycles of products and takes 550, 60 bytes a cycle; with the copies left out the same code took
+// 224 us where it takes 252 (131072 rows, 64 experts of [2816, 2048] with the gate: 6.0 PFLOP/s).
+// Prefetches of the next steps' weights into L2 made it slower (282 us).
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -70,16 +72,17 @@ struct Tile {
 
 __device__ __forceinline__ int mtiles(int rows) { return (rows + 2 * BM - 1) / (2 * BM); }
 
-__device__ __forceinline__ Tile tile_at(int t, const grouped::Groups& G, const Params& P) {
+__device__ __forceinline__ Tile tile_at(int t, int& e, const grouped::Groups& G, const Params& P) {
   Tile d;
-  d.e = grouped::find(G.start, P.E, t);
+  e = grouped::find_from(G.start, e, t);
+  d.e = e;
   d.g = G.span(d.e);
   const int local = t - G.start[d.e], mt = mtiles(d.g.rows());
   if (mt > P.NT) {
-    d.m = local / P.NT;
+    d.m = grouped::quick_div(local, P.NT);
     d.n = local - d.m * P.NT;
   } else {
-    d.n = local / mt;
+    d.n = grouped::quick_div(local, mt);
     d.m = local - d.n * mt;
   }
   return d;
@@ -154,10 +157,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = cluster_id; t < total && ok; t += nclusters) {
-        const Tile ti = tile_at(t, G, P);
+      for (int t = cluster_id, e = 0; t < total && ok; t += nclusters) {
+        const Tile ti = tile_at(t, e, G, P);
         const int a_row = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, b_row = w_row<SILU>(ti.n, (int)rank, P);
-        const int a_atom = (G.start[ti.e] / P.NT * 2 + ti.m * 2 + (int)rank) * P.steps * 2;
+        const int a_atom = (grouped::quick_div(G.start[ti.e], P.NT) * 2 + ti.m * 2 + (int)rank) * P.steps * 2;
         const int b_atom = (ti.e * P.NT + ti.n) * P.steps * 4;
         for (int kb = 0; kb < P.steps; ++kb) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
@@ -181,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       constexpr uint32_t IDESC = mx::idesc(2 * BM, BN);
       int stage = 0, acc = 0, set = 0;
       uint32_t ph = 0, aph = 0;
-      for (int t = cluster_id; t < total; t += nclusters) {
+      for (int t = cluster_id, e = 0; t < total; t += nclusters) {
         if (!ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
@@ -224,8 +227,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     T* y = static_cast<T*>(P.y);
     int acc = 0;
     uint32_t aph = 0;
-    for (int t = cluster_id; t < total; t += nclusters) {
-      const Tile ti = tile_at(t, G, P);
+    for (int t = cluster_id, e = 0; t < total; t += nclusters) {
+      const Tile ti = tile_at(t, e, G, P);
       const int m = ti.m * (2 * BM) + (int)rank * BM + row;
       const bool mine = m < ti.g.rows();
       T* dst = y + ((long)ti.g.lo + m) * P.cols;

@@ -630,8 +630,8 @@ int check_any_dtype(int dtype) {
 }  // namespace moe
 
 MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E) {
-  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
-  return grouped_tc_workspace(S, K, N, E, true);
+  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
+  return grouped_tc_workspace(dtype, S, K, N, E, true);
 }
 
 MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
@@ -661,12 +661,14 @@ MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int
   a.offsets = offsets;
   a.ws = ws;
   a.status = status;
-  return dtype == MOE_F32 ? launch_grouped_simt(a, (cudaStream_t)stream) : launch_grouped_tc(a, (cudaStream_t)stream);
+  if (dtype == MOE_F32 && !grouped_f32_uses_tensor_cores(S, K, N, E))
+    return launch_grouped_simt(a, nullptr, 0, (cudaStream_t)stream);
+  return launch_grouped_tc(a, (cudaStream_t)stream);
 }
 
 MOE_API size_t moe_grouped_gemm_backward_workspace_size(int dtype, int S, int K, int N, int E) {
-  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
-  return grouped_tc_workspace(S, K, N, E, false);
+  if (S < 0 || K < 0 || N < 0 || E < 1 || (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16)) return 0;
+  return grouped_tc_workspace(dtype, S, K, N, E, false);
 }
 
 MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* d_y, int dtype, int S, int K,
@@ -703,9 +705,10 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
   if (N == 0) return d_x_or_null ? zero_out(d_x_or_null, (size_t)S * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
   if (S == 0)
     return d_w_or_null ? zero_out(d_w_or_null, (size_t)E * N * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
-  if (dtype != MOE_F32) return launch_grouped_tc_backward(a, (cudaStream_t)stream);
-  if (a.d_x && (rc = launch_grouped_simt_dx(a, (cudaStream_t)stream))) return rc;
-  if (a.d_w && (rc = launch_grouped_simt_dw(a, (cudaStream_t)stream))) return rc;
+  if (dtype != MOE_F32 || grouped_f32_uses_tensor_cores(S, K, N, E))
+    return launch_grouped_tc_backward(a, (cudaStream_t)stream);
+  if (a.d_x && (rc = launch_grouped_simt_dx(a, nullptr, 0, (cudaStream_t)stream))) return rc;
+  if (a.d_w && (rc = launch_grouped_simt_dw(a, nullptr, 0, (cudaStream_t)stream))) return rc;
   return MOE_OK;
 }
 

@@ -230,12 +230,19 @@ struct GroupedArgs {
   void* ws;
   int32_t* status;
 };
-int launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
-int launch_grouped_simt_dx(const GroupedArgs& a, cudaStream_t s);
-int launch_grouped_simt_dw(const GroupedArgs& a, cudaStream_t s);
-// bf16 / float16 (tensor cores); the workspace holds padded copies of operands whose rows are not a
-// multiple of 16 bytes.
-size_t grouped_tc_workspace(int S, int K, int N, int E, bool fwd);
+int launch_grouped_simt(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
+int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
+int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
+// The tensor cores; the workspace holds padded copies of 16-bit operands whose rows are not a multiple
+// of 16 bytes, and float32 operands in three parts.
+inline bool grouped_f32_uses_tensor_cores(int S, int K, int N, int E) {
+#ifdef F32T
+  return 2.0 * S * K * N >= F32T;
+#else
+  return 2.0 * S * K * N >= 2e8;
+#endif
+}
+size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd);
 int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);
 int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s);
 

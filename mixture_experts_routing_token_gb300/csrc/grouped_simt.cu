@@ -1,4 +1,5 @@
-// Products grouped by expert in float32, on the CUDA cores: every size and alignment.
+// Products grouped by expert in float32, on the CUDA cores: small sizes, and operands that hold
+// infinities or NaN (then launched behind the tensor-core kernel, with the flags that it gives way to).
 //
 //   ROWS   y[p, n]    = sum_k x[p, k] w[e, n, k]     (rows p of expert e)
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
@@ -10,6 +11,8 @@
 // one barrier and no exposed load. The multiply-adds are issued in pairs (fma.f32x2, two columns),
 // which leaves issue slots for everything else beside a full FMA pipe. Products and sums are float32 in ascending order of the
 // reduction index, so results do not depend on the launch. Bound by the FMA pipes.
+#include <algorithm>
+
 #include "grouped.cuh"
 
 namespace moe {
@@ -26,6 +29,8 @@ struct SimtParams {
   float* out;
   const int32_t* offsets;
   int S, K, N, E;
+  const int* flags;     // null, or words of which one must be set for the kernel to do anything
+  int nflags;
   int32_t* status;
 };
 
@@ -37,6 +42,11 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   const int cols = MODE == ROWS ? P.N : P.K;           // columns of the output
   const int NT = (cols + TN - 1) / TN;
   const int MT = (P.N + TM - 1) / TM;                  // GRADW: row tiles of an expert's output
+  if (P.flags != nullptr) {
+    int any = 0;
+    for (int i = tid; i < P.nflags; i += TT) any |= __ldg(P.flags + i);
+    if (!__syncthreads_or(any)) return;
+  }
   if (tid < 32)
     grouped::group_list(P.offsets, P.E, P.S,
                        [&](int rows) { return MODE == GRADW ? MT * NT : (rows + TM - 1) / TM * NT; }, G);
@@ -137,27 +147,27 @@ int launch(const SimtParams& p, cudaStream_t s, const char* name) {
   const long full = (long)num_sms() * 6;
   const size_t unused = tiles <= full ? 22000 : 0;
   ProfScope ps(name, s);
-  grouped_simt_kernel<MODE><<<(unsigned)(tiles < full * 16 ? tiles : full * 16), TT, unused, s>>>(p);
+  grouped_simt_kernel<MODE><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, unused, s>>>(p);
   return check_launch(name);
 }
 
-SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out) {
+SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out, const int* flags, int nflags) {
   return SimtParams{static_cast<const float*>(left), static_cast<const float*>(right), static_cast<float*>(out),
-                    a.offsets, a.S, a.K, a.N, a.E, a.status};
+                    a.offsets, a.S, a.K, a.N, a.E, flags, nflags, a.status};
 }
 
 }  // namespace
 
-int launch_grouped_simt(const GroupedArgs& a, cudaStream_t s) {
-  return launch<ROWS>(params(a, a.x, a.w, a.y), s, "grouped_gemm");
+int launch_grouped_simt(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
+  return launch<ROWS>(params(a, a.x, a.w, a.y, flags, nflags), s, "grouped_gemm");
 }
 
-int launch_grouped_simt_dx(const GroupedArgs& a, cudaStream_t s) {
-  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x), s, "grouped_gemm_dx");
+int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
+  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x, flags, nflags), s, "grouped_gemm_dx");
 }
 
-int launch_grouped_simt_dw(const GroupedArgs& a, cudaStream_t s) {
-  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w), s, "grouped_gemm_dw");
+int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
+  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w, flags, nflags), s, "grouped_gemm_dw");
 }
 
 }  // namespace moe

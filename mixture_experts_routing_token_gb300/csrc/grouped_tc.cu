@@ -1,5 +1,5 @@
-// Products grouped by expert on SM pairs, bf16 and float16 (tcgen05.mma.cta_group::2,
-// M = 256 x N = 256 x K = 16, float32 accumulators in both SMs' TMEM).
+// Products grouped by expert on SM pairs, bf16, float16 and float32 (tcgen05.mma.cta_group::2,
+// kind::f16, M = 256 x N = 256 x K = 16, float32 accumulators in both SMs' TMEM).
 //
 //   y[p, n]      = sum_k x[p, k] w[e, n, k]               A = x rows, B = w rows (both K-major)
 //   d_x[p, k]    = sum_n d_y[p, n] w[e, n, k]             A = d_y rows, B = w (MN-major)
@@ -26,6 +26,17 @@
 //     the rows past the end in shared memory (whole 128-byte lines, so the swizzle does
 //     not matter) and only then hands the step to the MMA issuer.
 //
+// float32. A value is h + m + l, three bf16 parts of 8 bits each (what is left is below 2^-26 of
+// it; a first kernel writes the parts into the workspace), and a product of two values the six
+// products of parts hl + lh + mm + hm + mh + hh, each exact in float32; the three left out are below
+// 2^-25 of it. The tensor cores add to an accumulator with truncation, 2^-24 of it on average and
+// always toward zero, which a float32 result must not collect over a long reduction (measured on
+// bf16 operands: 5e-7 at 512 terms, 9e-6 at 8192). So an accumulator holds two steps (K = 128, the
+// small products first) and is then added in registers, rounded to nearest, by eight epilogue warps
+// with 128 sums a thread, while the next two steps go into the other one. Parts make no sense of
+// infinities and NaN (nor of 2^127 and above, which may round to infinity): the first kernel flags
+// them, and then this one leaves everything to the kernel on the CUDA cores, which follows.
+//
 // Barriers as in the FFN's pair kernel: full[s] in the leader CTA (the pair's bytes, and in
 // the gradients one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
 // accumulator. Every wait is bounded.
@@ -46,14 +57,19 @@ constexpr int NSTAGE = 6;
 constexpr int A_BYTES = BM * BK * 2;    // 16 KB
 constexpr int B_BYTES = (BN / 2) * BK * 2;
 constexpr int STAGE = A_BYTES + B_BYTES;
-constexpr int EPI_WARPS = 4;
-constexpr int DSMEM = NSTAGE * STAGE + EPI_WARPS * 4096 + 1024;    // the ring, the epilogue's buffers
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint64_t DRAIN_NS = 2000000000ull;    // issued MMAs and copies
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;      // bytes between the two 64-column boxes of an MN-major operand
 
-template <bool GRAD>
-constexpr int threads() { return (2 + EPI_WARPS + (GRAD ? 1 : 0)) * 32; }
+template <class T>
+constexpr bool is_f32() { return sizeof(T) == 4; }
+template <class T>
+constexpr int epi_warps() { return is_f32<T>() ? 8 : 4; }
+template <bool GRAD, class T>
+constexpr int threads() { return (2 + epi_warps<T>() + (GRAD ? 1 : 0)) * 32; }
+// The ring and, for 16-bit results, the epilogue's buffers.
+template <class T>
+constexpr int dsmem_bytes() { return NSTAGE * STAGE + (is_f32<T>() ? 0 : 4 * 4096) + 1024; }
 
 // One product over the groups.
 struct Job {
@@ -71,15 +87,50 @@ struct Params {
   Job rows;         // y or d_x
   Job dw;           // d_w
   int dw_first;
+  const int* flags;   // float32: one word per block of the kernel that made the parts, set where it met a
+  int nflags;         // value that parts do not stand for
   int32_t* status;
   uint64_t wait_ns;
 };
 
 struct Tile {
   bool dw;
-  int e, m, n, steps;
+  int e, m, n, blocks;      // blocks: of 64 along the reduction
   grouped::Span g;
 };
+
+// Steps of a tile: its blocks, in order; in float32 two blocks (or the odd last one) at a time, with
+// six products of parts.
+template <class T>
+__device__ __forceinline__ int step_count(int blocks) { return is_f32<T>() ? 6 * blocks : blocks; }
+
+struct Step {
+  int block, pa, pb;        // parts of A and B
+  bool first, last;         // of an accumulator
+};
+
+template <class T>
+__device__ __forceinline__ Step step_at(int s, int blocks) {
+  if (!is_f32<T>()) return Step{s, 0, 0, s == 0, s == blocks - 1};
+  const int pairs = blocks >> 1;
+  Step d;
+  int p;
+  if (s < pairs * 12) {
+    const int c = s / 12, r = s - c * 12;
+    p = r >> 1;
+    d.block = 2 * c + (r & 1);
+    d.first = r == 0;
+    d.last = r == 11;
+  } else {
+    p = s - pairs * 12;
+    d.block = blocks - 1;
+    d.first = p == 0;
+    d.last = p == 5;
+  }
+  d.pa = (0x010120 >> (4 * p)) & 3;     // h m h m l h, with
+  d.pb = (0x001102 >> (4 * p)) & 3;     // h h m m h l, from the last to the first
+  return d;
+}
 
 // Where a role is in the list of tiles: experts of its last tiles of either kind.
 struct At {
@@ -102,7 +153,7 @@ __device__ __forceinline__ Tile tile_at(int t, At& at, const grouped::Groups& G,
     d.g = G.span(d.e);
     local = t - d.e * per;
     mt = P.dw.MT;
-    d.steps = (d.g.rows() + BK - 1) / BK;
+    d.blocks = (d.g.rows() + BK - 1) / BK;
   } else {
     if (P.dw_first) t -= dw_tiles;
     at.e_rows = grouped::find_from(G.start, at.e_rows, t);
@@ -110,7 +161,7 @@ __device__ __forceinline__ Tile tile_at(int t, At& at, const grouped::Groups& G,
     d.g = G.span(d.e);
     local = t - G.start[d.e];
     mt = (d.g.rows() + 2 * BM - 1) / (2 * BM);
-    d.steps = (P.rows.R + BK - 1) / BK;
+    d.blocks = (P.rows.R + BK - 1) / BK;
   }
   const int NT = d.dw ? P.dw.NT : P.rows.NT;
   if (mt > NT) {
@@ -125,7 +176,7 @@ __device__ __forceinline__ Tile tile_at(int t, At& at, const grouped::Groups& G,
 
 // GRAD = false: P.rows is y, tmA / tmB its operands. GRAD: P.rows is d_x (tmA, tmB), P.dw d_w (tmC, tmD).
 template <bool GRAD, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 1)
     grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
                         const Params P) {
@@ -134,7 +185,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ grouped::Groups G;
+  __shared__ int skip;
   extern __shared__ uint8_t dsmem_raw[];
+  constexpr bool F32 = is_f32<T>();
+  constexpr int EPI_WARPS = epi_warps<T>();
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -179,13 +233,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
   if (warp == 2)
     grouped::group_list(P.offsets, P.E, P.S,
                         [&](int rows) { return P.rows.out ? (rows + 2 * BM - 1) / (2 * BM) * P.rows.NT : 0; }, G);
+  if (F32 && warp == 3) {
+    int any = 0;
+    for (int i = lane; i < P.nflags; i += 32) any |= __ldg(P.flags + i);
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) skip = any;
+  }
   ptx::tc_fence_before();
   __syncthreads();
   cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const int dw_tiles = GRAD && P.dw.out ? P.E * P.dw.MT * P.dw.NT : 0;
-  const int total = G.start[P.E] + dw_tiles;
+  const int total = F32 && skip ? 0 : G.start[P.E] + dw_tiles;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
@@ -197,16 +257,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
         const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
         const bool cut = ti.dw && ti.g.rows() % BK != 0;
         const int xb = ti.n * BN + (int)rank * (BN / 2);
-        for (int kb = 0; kb < ti.steps; ++kb) {
+        const int steps = step_count<T>(ti.blocks);
+        for (int s = 0; s < steps; ++s) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) goto producer_done;
-          if (cut && kb == ti.steps - 1) {
-            const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + kb * BK;
+          const Step sp = step_at<T>(s, ti.blocks);
+          if (cut && sp.block == ti.blocks - 1) {
+            const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + sp.block * BK;
             const uint32_t tb = ptx::smem_u32(&tail_bar[stage]);
             ptx::mbar_arrive_expect_tx(tb, STAGE);
-            ptx::tma_load_3d(sA(stage), &tmC, xa, y, 0, tb);
-            ptx::tma_load_3d(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, 0, tb);
-            ptx::tma_load_3d(sB(stage), &tmD, xb, y, 0, tb);
-            ptx::tma_load_3d(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, 0, tb);
+            ptx::tma_load_3d(sA(stage), &tmC, xa, y, sp.pa, tb);
+            ptx::tma_load_3d(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, sp.pa, tb);
+            ptx::tma_load_3d(sB(stage), &tmD, xb, y, sp.pb, tb);
+            ptx::tma_load_3d(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, sp.pb, tb);
           } else {
             const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
             if (leader) {
@@ -215,18 +277,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
             }
             const uint32_t fb = map_to_rank(fb_local, 0);
             if (GRAD && ti.dw) {
-              const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + kb * BK;
-              tma_load_3d_pair(sA(stage), &tmC, xa, y, 0, fb);
-              tma_load_3d_pair(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, 0, fb);
-              tma_load_3d_pair(sB(stage), &tmD, xb, y, 0, fb);
-              tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, 0, fb);
+              const int xa = ti.m * (2 * BM) + (int)rank * BM, y = ti.g.lo + sp.block * BK;
+              tma_load_3d_pair(sA(stage), &tmC, xa, y, sp.pa, fb);
+              tma_load_3d_pair(sA(stage) + MN_BLOCK, &tmC, xa + 64, y, sp.pa, fb);
+              tma_load_3d_pair(sB(stage), &tmD, xb, y, sp.pb, fb);
+              tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmD, xb + 64, y, sp.pb, fb);
             } else {
-              tma_load_3d_pair(sA(stage), &tmA, kb * BK, ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, 0, fb);
+              const int k = sp.block * BK, mat = ti.e + sp.pb * P.E;
+              tma_load_3d_pair(sA(stage), &tmA, k, ti.g.lo + ti.m * (2 * BM) + (int)rank * BM, sp.pa, fb);
               if (GRAD) {
-                tma_load_3d_pair(sB(stage), &tmB, xb, kb * BK, ti.e, fb);
-                tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmB, xb + 64, kb * BK, ti.e, fb);
+                tma_load_3d_pair(sB(stage), &tmB, xb, k, mat, fb);
+                tma_load_3d_pair(sB(stage) + MN_BLOCK, &tmB, xb + 64, k, mat, fb);
               } else {
-                tma_load_3d_pair(sB(stage), &tmB, kb * BK, xb, ti.e, fb);
+                tma_load_3d_pair(sB(stage), &tmB, k, xb, mat, fb);
               }
             }
           }
@@ -244,16 +307,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
       for (int t = cluster_id; t < total; t += nclusters) {
         const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
         const uint32_t idesc = ti.dw ? P.dw.idesc : P.rows.idesc;
-        if (ti.steps == 0) continue;   // nothing to add up: the epilogue writes zeros
-        if (!ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns)) break;
-        ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        const int steps = step_count<T>(ti.blocks);   // 0: the epilogue writes zeros
         bool ok = true;
-        for (int kb = 0; kb < ti.steps; ++kb) {
-          if (!ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns)) {
-            ok = false;
-            break;
+        uint32_t d_tmem = 0;
+        for (int s = 0; s < steps; ++s) {
+          const Step sp = step_at<T>(s, ti.blocks);
+          if (sp.first) {
+            ok = ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            d_tmem = tmem_base + (uint32_t)(acc * BN);
           }
+          ok = ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
+          if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t a0 = sA(stage), b0 = sB(stage);
           // descriptors of the step's first MMA; K-major operands advance 32 bytes a K = 16, MN-major 2 KB
@@ -263,13 +329,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
           const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (GRAD ? 2048u : 32u) >> 4;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
+            mma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, !sp.first || kk != 0);
           commit_pair(ptx::smem_u32(&empty_bar[stage]), 0x3);
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
+          if (sp.last) {
+            commit_pair(ptx::smem_u32(&tfull_bar[acc]), 0x3);
+            if (++acc == 2) { acc = 0; aph ^= 1u; }
+          }
         }
         if (!ok) break;
-        commit_pair(ptx::smem_u32(&tfull_bar[acc]), 0x3);
-        if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       commit_pair(ptx::smem_u32(&drain_bar), 0x1);
       int dummy = 0;
@@ -290,10 +358,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
       const int nrows = (ti.dw ? J.M : ti.g.rows()) - (m - lane);     // of this warp's 32 (from lane 0 on)
       const bool mine = lane < nrows;
       T* dst = static_cast<T*>(J.out) + (ti.dw ? (long)ti.e * J.M + m : (long)ti.g.lo + m) * J.C;
-      if (ti.steps == 0) {
+      if (ti.blocks == 0) {
         uint32_t z[32] = {};
         if (mine)
           for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 32) grouped::store_cols(dst, c, J.C, J.vec, z);
+        continue;
+      }
+      if constexpr (F32) {
+        // this warp's 128 of the 256 columns, over the accumulators of the tile
+        const int half = (warp - 2) >> 2;
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        bool ok = true;
+        for (int left = (ti.blocks + 1) >> 1; left > 0; --left) {
+          ok = ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * 128);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            ptx::tmem_ld32(taddr + c * 32, y);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(y[j]);
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
+          if (++acc == 2) { acc = 0; aph ^= 1u; }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t y[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(sum[c * 32 + j]);
+          const int c0 = ti.n * BN + half * 128 + c * 32;
+          if (mine && c0 < J.C) grouped::store_cols(dst, c0, J.C, J.vec, y);
+        }
         continue;
       }
       if (!ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns)) break;
@@ -332,22 +436,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD>(), 1)
     uint32_t tph = 0;                    // bit s: phase of tail_bar[s]
     for (int t = cluster_id; t < total; t += nclusters) {
       const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
-      if (ti.steps == 0) continue;
-      const int s = (stage + ti.steps - 1) % NSTAGE;
-      stage = (stage + ti.steps) % NSTAGE;
-      const int keep = ti.g.rows() % BK;
+      const int first = stage, keep = ti.g.rows() % BK;
+      stage = (stage + step_count<T>(ti.blocks)) % NSTAGE;
       if (!ti.dw || keep == 0) continue;
-      if (!ptx::mbar_wait(ptx::smem_u32(&tail_bar[s]), (tph >> s) & 1u, abort_p, P.wait_ns)) break;
-      tph ^= 1u << s;
-      const int lines = (BK - keep) * 4, first = keep * 128;   // 128-byte lines to clear, in four boxes of 64
-      for (int i = lane; i < lines * 8; i += 32) {
-        const int line = i >> 3, box = line & 3;
-        const uint32_t a = sA(s) + (uint32_t)(box * (int)MN_BLOCK + first + (line >> 2) * 128 + (i & 7) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+      bool ok = true;
+      for (int p = 0; p < (F32 ? 6 : 1) && ok; ++p) {      // the last block's steps
+        const int at_step = !F32 ? ti.blocks - 1 : ti.blocks & 1 ? (ti.blocks - 1) * 6 + p : (ti.blocks - 2) * 6 + 2 * p + 1;
+        const int s = (first + at_step) % NSTAGE;
+        ok = ptx::mbar_wait(ptx::smem_u32(&tail_bar[s]), (tph >> s) & 1u, abort_p, P.wait_ns);
+        if (!ok) break;
+        tph ^= 1u << s;
+        const int lines = (BK - keep) * 4;               // 128-byte lines to clear, in four boxes of 64
+        for (int i = lane; i < lines * 8; i += 32) {
+          const int line = i >> 3, box = line & 3;
+          const uint32_t a = sA(s) + (uint32_t)(box * (int)MN_BLOCK + (keep + (line >> 2)) * 128 + (i & 7) * 16);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
       }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
+      if (!ok) break;
     }
   }
 
@@ -373,11 +482,11 @@ static_assert(A_BYTES == 2 * (int)MN_BLOCK && B_BYTES == 2 * (int)MN_BLOCK, "a s
 
 template <bool GRAD, class T>
 int launch(const CUtensorMap (&m)[4], const Params& p, long most_tiles, cudaStream_t s, const char* name) {
-  if (int rc = ensure_smem_limit(grouped_pair_kernel<GRAD, T>, DSMEM, name)) return rc;
+  if (int rc = ensure_smem_limit(grouped_pair_kernel<GRAD, T>, dsmem_bytes<T>(), name)) return rc;
   const int grid = 2 * (int)std::max(1L, std::min(most_tiles, (long)(num_sms() / 2)));
   ProfScope ps(name, s);
   const cudaError_t e =
-      launch_pdl(grouped_pair_kernel<GRAD, T>, grid, threads<GRAD>(), DSMEM, s, m[0], m[1], m[2], m[3], p);
+      launch_pdl(grouped_pair_kernel<GRAD, T>, grid, threads<GRAD, T>(), dsmem_bytes<T>(), s, m[0], m[1], m[2], m[3], p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }
@@ -388,7 +497,7 @@ Job job(int dtype, int R, int C, void* out, int a_mn, int b_mn) {
   j.C = C;
   j.NT = (C + BN - 1) / BN;
   j.out = out;
-  j.vec = grouped::store_width(out, C, 2);
+  j.vec = grouped::store_width(out, C, dtype == MOE_F32 ? 4 : 2);
   j.idesc = idesc_bf16_f32_major(2 * BM, BN, a_mn, b_mn);
   if (dtype == MOE_F16) j.idesc &= ~((1u << 7) | (1u << 10));   // A and B float16
   return j;
@@ -439,10 +548,105 @@ int padded(const void* src, long rows, int cols, Carver& c, Mat* m, cudaStream_t
   return check_launch("grouped_pad_rows");
 }
 
+// ---- float32 operands in parts ---------------------------------------------------------
+
+struct Split {
+  const float* src;
+  uint4* dst;           // [3 parts, rows, padded columns] bf16
+  long n;               // pieces of 8 columns of one part
+  int cols, pieces;     // columns; pieces of a row
+};
+
+struct SplitParams {
+  Split m[3];
+  int count;
+  int* flags;           // one word per block
+};
+
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+// x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out.
+__global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
+  pdl_wait();
+  pdl_trigger();
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (k >= P.count) break;
+    const Split M = P.m[k];
+    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < M.n; i += (long)gridDim.x * blockDim.x) {
+      const long r = M.n < (1L << 31) ? (long)((uint32_t)i / (uint32_t)M.pieces) : i / M.pieces;
+      const int c = (int)(i - r * M.pieces) * 8;
+      const float* p = M.src + r * M.cols + c;
+      float v[8];
+      if ((M.cols & 3) == 0 && c + 8 <= M.cols) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < M.cols ? __ldg(p + j) : 0.0f;
+      }
+      uint32_t q[3][4] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        bad |= (__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f000000u;     // 2^127 and above, infinity, NaN
+        float left = v[j];
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint32_t bits = bf16_bits(left);
+          q[part][j >> 1] |= bits << (16 * (j & 1));
+          left -= __uint_as_float(bits << 16);       // exact
+        }
+      }
+#pragma unroll
+      for (int part = 0; part < 3; ++part) M.dst[part * M.n + i] = make_uint4(q[part][0], q[part][1], q[part][2], q[part][3]);
+    }
+  }
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) P.flags[blockIdx.x] = any;
+}
+
+constexpr int kSplitBlocks = 1024;
+
+void add_split(SplitParams& p, const void* src, long rows, int cols, Carver& c, Mat* m) {
+  const int pc = pad8(cols);
+  uint16_t* dst = c.take<uint16_t>((size_t)3 * rows * pc);
+  *m = Mat{dst, pc};
+  p.m[p.count++] = Split{static_cast<const float*>(src), reinterpret_cast<uint4*>(dst), rows * (pc / 8), cols, pc / 8};
+}
+
+int launch_split(SplitParams& p, Params* out, cudaStream_t s) {
+  long n = 0;
+  for (int i = 0; i < p.count; ++i) n = std::max(n, p.m[i].n);
+  const int grid = (int)std::max(1L, std::min((n + 255) / 256, (long)kSplitBlocks));
+  out->flags = p.flags;
+  out->nflags = grid;
+  ProfScope ps("grouped_split", s);
+  const cudaError_t e = launch_pdl(split_kernel, grid, 256, 0, s, p);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped_split: %s", cudaGetErrorString(e));
+  return check_launch("grouped_split");
+}
+
+size_t split_bytes(Carver& c, long rows, int cols) {
+  c.take<uint16_t>((size_t)3 * rows * pad8(cols));
+  return c.used;
+}
+
 }  // namespace
 
-size_t grouped_tc_workspace(int S, int K, int N, int E, bool fwd) {
+size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd) {
   Carver c(nullptr);
+  if (dtype == MOE_F32) {
+    if (!grouped_f32_uses_tensor_cores(S, K, N, E)) return 0;
+    c.take<int>(kSplitBlocks);
+    split_bytes(c, S, K);
+    split_bytes(c, (long)E * N, K);
+    if (!fwd) split_bytes(c, S, N);
+    return align_up(c.used, 256);
+  }
   if (K % 8 != 0) {
     c.take<uint16_t>((size_t)S * pad8(K));
     c.take<uint16_t>((size_t)E * N * pad8(K));
@@ -455,38 +659,63 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   Carver c(a.ws);
   Mat x, w;
   int rc;
-  if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
-  if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
-  if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
+  Params p{a.offsets, a.S, a.E, job(a.dtype, a.K, a.N, a.y, 0, 0), Job{}, 0, nullptr, 0, a.status, wait_limit_ns()};
+  const bool f32 = a.dtype == MOE_F32;
+  if (f32) {
+    SplitParams q{};
+    q.flags = c.take<int>(kSplitBlocks);
+    add_split(q, a.x, a.S, a.K, c, &x);
+    add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    if ((rc = launch_split(q, &p, s))) return rc;
+  } else {
+    if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
+    if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
+    if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
+  }
+  const uint64_t parts = f32 ? 3 : 1;
   CUtensorMap m[4];
-  if ((rc = make_tmap_3d(&m[0], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
-  if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, BK, BN / 2))) return rc;
+  if ((rc = make_tmap_3d(&m[0], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, parts, BK, BM))) return rc;
+  if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, parts * (uint64_t)a.E, BK, BN / 2))) return rc;
   m[2] = m[3] = m[0];      // not read
-  Params p{a.offsets, a.S, a.E, job(a.dtype, a.K, a.N, a.y, 0, 0), Job{}, 0, a.status, wait_limit_ns()};
   const long tiles = row_tiles(a, p.rows.NT);
+  if (f32) {
+    if ((rc = launch<false, float>(m, p, tiles, s, "grouped_gemm"))) return rc;
+    return launch_grouped_simt(a, p.flags, p.nflags, s);
+  }
   return a.dtype == MOE_BF16 ? launch<false, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm")
                              : launch<false, __half>(m, p, tiles, s, "grouped_gemm");
 }
 
 int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   Carver c(a.ws);
-  Mat dy, x{}, w{};
+  Mat dy{}, x{}, w{};
   CUtensorMap m[4] = {};
   int rc;
-  if ((rc = padded(a.d_y, a.S, a.N, c, &dy, s))) return rc;
-  Params p{a.offsets, a.S, a.E, Job{}, Job{}, 0, a.status, wait_limit_ns()};
+  Params p{a.offsets, a.S, a.E, Job{}, Job{}, 0, nullptr, 0, a.status, wait_limit_ns()};
+  const bool f32 = a.dtype == MOE_F32;
+  const uint64_t parts = f32 ? 3 : 1;
+  if (f32) {
+    SplitParams q{};
+    q.flags = c.take<int>(kSplitBlocks);
+    add_split(q, a.d_y, a.S, a.N, c, &dy);
+    if (a.d_w) add_split(q, a.x, a.S, a.K, c, &x);
+    if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    if ((rc = launch_split(q, &p, s))) return rc;
+  } else {
+    if ((rc = padded(a.d_y, a.S, a.N, c, &dy, s))) return rc;
+    if (a.d_x && (rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
+    if (a.d_w && (rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
+  }
   long tiles = 0;
   if (a.d_x) {
-    if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
-    if ((rc = make_tmap_3d(&m[0], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, BK, BM))) return rc;
-    if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, (uint64_t)a.E, 64, BK))) return rc;
+    if ((rc = make_tmap_3d(&m[0], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, parts, BK, BM))) return rc;
+    if ((rc = make_tmap_3d(&m[1], w.p, 2, (uint64_t)w.cols, (uint64_t)a.N, parts * (uint64_t)a.E, 64, BK))) return rc;
     p.rows = job(a.dtype, a.N, a.K, a.d_x, 0, 1);
     tiles += row_tiles(a, p.rows.NT);
   }
   if (a.d_w) {
-    if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
-    if ((rc = make_tmap_3d(&m[2], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
-    if ((rc = make_tmap_3d(&m[3], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, 1, 64, BK))) return rc;
+    if ((rc = make_tmap_3d(&m[2], dy.p, 2, (uint64_t)dy.cols, (uint64_t)a.S, parts, 64, BK))) return rc;
+    if ((rc = make_tmap_3d(&m[3], x.p, 2, (uint64_t)x.cols, (uint64_t)a.S, parts, 64, BK))) return rc;
     p.dw = job(a.dtype, 0, a.K, a.d_w, 1, 1);
     p.dw.M = a.N;
     p.dw.MT = (a.N + 2 * BM - 1) / (2 * BM);
@@ -495,8 +724,14 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   if (!a.d_x) m[0] = m[1] = m[2];      // not read
   if (!a.d_w) m[2] = m[3] = m[0];
   p.dw_first = a.S / a.E > a.N;
-  return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm_backward")
-                             : launch<true, __half>(m, p, tiles, s, "grouped_gemm_backward");
+  const char* name = "grouped_gemm_backward";
+  if (f32) {
+    if ((rc = launch<true, float>(m, p, tiles, s, name))) return rc;
+    if (a.d_x && (rc = launch_grouped_simt_dx(a, p.flags, p.nflags, s))) return rc;
+    return a.d_w ? launch_grouped_simt_dw(a, p.flags, p.nflags, s) : MOE_OK;
+  }
+  return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, p, tiles, s, name)
+                             : launch<true, __half>(m, p, tiles, s, name);
 }
 
 }  // namespace moe

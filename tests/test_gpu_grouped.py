@@ -65,12 +65,25 @@ SHAPES = [
 ]
 
 
+# float32 products this large go to the tensor cores in parts
+SHAPES_F32 = [
+    ([257, 255, 0, 256, 1], 3, 520, 523),
+    ([63, 65, 1, 0, 500], 0, 777, 333),
+    ([700], 1, 129, 1100),
+    ([128, 64, 0, 192, 320], 0, 512, 640),
+    ([5, 900, 0, 33], 2, 64, 1700),
+]
+
+
 def shape_id(s):
     return f"{len(s[0])}x{sum(s[0])}+{s[1]}_K{s[2]}_N{s[3]}"
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("shape", SHAPES, ids=shape_id)
+CASES = [(s, d) for s in SHAPES for d in ("f32", "bf16", "f16")] + [(s, "f32") for s in SHAPES_F32]
+IDS = [f"{shape_id(s)}-{d}" for s, d in CASES]
+
+
+@pytest.mark.parametrize("shape,dtype", CASES, ids=IDS)
 def test_grouped_gemm(moe, shape, dtype):
     counts, beyond, K, N = shape
     off = offsets_of(counts)
@@ -84,8 +97,7 @@ def test_grouped_gemm(moe, shape, dtype):
     assert int(status.item()) == 0
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("shape", SHAPES, ids=shape_id)
+@pytest.mark.parametrize("shape,dtype", CASES, ids=IDS)
 def test_grouped_gemm_backward(moe, shape, dtype):
     counts, beyond, K, N = shape
     off = offsets_of(counts)
@@ -153,6 +165,42 @@ def test_values_do_not_leak_between_groups(moe, dtype):
     ax, aw = grouped.grouped_gemm_backward(abs(x64), abs(w64), off, abs(g64))
     check(d_x[keep], rx[keep], ax[keep], N, dtype, "d_x")
     check(d_w[[0, 2, 3]], rw[[0, 2, 3]], aw[[0, 2, 3]], 70, dtype, "d_w")
+
+
+def test_f32_in_parts_is_float32(moe):
+    """Large float32 products: close to float64 as float32 sums are (2-norm), in both directions, also
+    where all products have one sign, so that a bias of the sums would add up."""
+    off = offsets_of([300, 0, 212])
+    o = torch.from_numpy(off).to(DEV)
+    for positive in (False, True):
+        x, x64 = draw((512, 2048), "f32", 1)
+        w, w64 = draw((3, 384, 2048), "f32", 2)
+        g, g64 = draw((512, 384), "f32", 3)
+        if positive:
+            x, w, g, x64, w64, g64 = abs(x), abs(w), abs(g), abs(x64), abs(w64), abs(g64)
+        y = moe.moe_grouped_gemm(x, w, o)
+        d_x, d_w = moe.moe_grouped_gemm_backward(x, w, o, g)
+        for got, want in zip((y, d_x, d_w), (grouped.grouped_gemm(x64, w64, off), *grouped.grouped_gemm_backward(x64, w64, off, g64))):
+            # sums of n rounded additions: at most n 2^-24 of the magnitudes, and their square root in the mean;
+            # 16 of them between two roundings to nearest, 6e-8 each, are 1e-6
+            assert np.linalg.norm(to64(got) - want) <= 1e-6 * np.linalg.norm(want)
+
+
+def test_f32_infinities_follow_float32(moe):
+    """Infinities, NaN and values next to the largest float32 give what float32 arithmetic gives."""
+    off = offsets_of([257, 255, 0, 256, 1])
+    o = torch.from_numpy(off).to(DEV)
+    x, _ = draw((769, 520), "f32", 1)
+    w, _ = draw((5, 523, 520), "f32", 2)
+    x[3, 5], x[300, 0], x[600, 519], x[601, 2] = float("inf"), float("nan"), -float("inf"), 3.0e38
+    y = moe.moe_grouped_gemm(x, w, o).cpu()
+    e = grouped.expert_of_rows(off, 769)
+    for p in (3, 300, 600, 601, 0, 768):
+        want = (x[p].double() * w[e[p]].double()).sum(1).float().cpu()
+        assert torch.equal(torch.isnan(y[p]), torch.isnan(want)) and torch.equal(torch.isinf(y[p]), torch.isinf(want))
+        fin = torch.isfinite(want)
+        assert torch.equal(torch.sign(y[p][~torch.isnan(want)]), torch.sign(want[~torch.isnan(want)]))
+        assert (y[p][fin] - want[fin]).abs().max() <= 1e-5 * max(1e-30, float(want[fin].abs().max())) if fin.any() else True
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -43,7 +43,7 @@ def test_backward_sizes_and_types(moe):
 def test_workspace_sizes(moe):
     for f in (moe.moe_grouped_gemm_workspace_size, moe.moe_grouped_gemm_backward_workspace_size):
         assert f(moe.MOE_BF16, 100, 64, 128, 4) == 0 and f(moe.MOE_F16, 100, 63, 128, 4) >= (100 + 4 * 128) * 64 * 2
-        assert f(moe.MOE_F32, 100, 63, 127, 4) == 0
+        assert f(moe.MOE_F32, 100, 63, 127, 4) == 0 and f(moe.MOE_F32, 2000, 517, 1030, 8) >= 6 * (2000 + 8 * 1030) * 517
         assert f(moe.MOE_BF16, -1, 64, 64, 4) == 0
 
 

@@ -661,7 +661,7 @@ MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int
   a.offsets = offsets;
   a.ws = ws;
   a.status = status;
-  if (dtype == MOE_F32 && !grouped_f32_uses_tensor_cores(S, K, N, E))
+  if (dtype == MOE_F32 && !grouped_f32_uses_tensor_cores(S, K, N, E, false))
     return launch_grouped_simt(a, nullptr, 0, (cudaStream_t)stream);
   return launch_grouped_tc(a, (cudaStream_t)stream);
 }
@@ -705,7 +705,7 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
   if (N == 0) return d_x_or_null ? zero_out(d_x_or_null, (size_t)S * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
   if (S == 0)
     return d_w_or_null ? zero_out(d_w_or_null, (size_t)E * N * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
-  if (dtype != MOE_F32 || grouped_f32_uses_tensor_cores(S, K, N, E))
+  if (dtype != MOE_F32 || grouped_f32_uses_tensor_cores(S, K, N, E, true))
     return launch_grouped_tc_backward(a, (cudaStream_t)stream);
   if (a.d_x && (rc = launch_grouped_simt_dx(a, nullptr, 0, (cudaStream_t)stream))) return rc;
   if (a.d_w && (rc = launch_grouped_simt_dw(a, nullptr, 0, (cudaStream_t)stream))) return rc;

@@ -235,12 +235,12 @@ int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, int nflags, c
 int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
 // The tensor cores; the workspace holds padded copies of 16-bit operands whose rows are not a multiple
 // of 16 bytes, and float32 operands in three parts.
-inline bool grouped_f32_uses_tensor_cores(int S, int K, int N, int E) {
-#ifdef F32T
-  return 2.0 * S * K * N >= F32T;
-#else
-  return 2.0 * S * K * N >= 2e8;
-#endif
+// float32 takes the tensor cores where there is enough to multiply for what making the parts costs
+// (ten bytes moved per value of x and w). Measured, us, tensor cores / CUDA cores: 64 rows per expert,
+// 64 experts of [1200, 800] 256 / 266, at 32 rows 248 / 200; 8 experts of [512, 512] 31 / 48 at 2000 rows,
+// [512, 256] 22 / 23 at 512; gradients, 16 rows per expert, 32 of [1024, 512] 107 / 116, 8 of [256, 256] 27 / 21.
+inline bool grouped_f32_uses_tensor_cores(int S, int K, int N, int E, bool grad) {
+  return 2.0 * S * K * N >= 1.5e8 && S >= (grad ? 16L : 64L) * E;
 }
 size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd);
 int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);

@@ -157,6 +157,31 @@ __device__ __forceinline__ void store_cols(T* row, int c, int cols, int vec, con
   }
 }
 
+// 32 columns of a warp's 32 rows (row l's in lane l's y) where rows are not a multiple of 16 bytes:
+// the lanes exchange the block's transpose (five rounds of shuffles), then each store instruction
+// writes neighbouring columns of one row. Lanes storing their own rows value by value touched 32
+// lines with every instruction.
+template <class T>
+__device__ __forceinline__ void store_turned(uint32_t (&y)[32], T* row0, int count, int c, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 16; s; s >>= 1) {
+    const bool hi = lane & s;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j & s) continue;
+      const uint32_t give = hi ? y[j] : y[j + s];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
+      if (hi) y[j] = got; else y[j + s] = got;
+    }
+  }
+  if (c + lane < cols) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < count) row0[(long)j * cols + c + lane] = from_float<T>(__uint_as_float(y[j]));
+  }
+}
+
 // Rows of an accumulator, one per lane, to the output through 4 KB of shared memory of the warp's
 // own: `q` holds 128 bytes of a row (packed values of columns c ..), and each store instruction
 // writes four whole 128-byte pieces of rows, where lanes that stored their own rows would touch 32

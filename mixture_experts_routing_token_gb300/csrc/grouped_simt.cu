@@ -5,12 +5,14 @@
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
 //   GRADW  d_w[e, n, k] = sum over p of e of d_y[p, n] x[p, k]
 //
-// One CTA of 64 threads computes 64 x 64 outputs of one expert, 8 x 8 per thread: a step of the
-// reduction reads 16 values from shared memory for 64 fused multiply-adds. 16 steps at a time go
-// through one of two buffers; the next 16 are in registers on their way meanwhile, so a turn has
-// one barrier and no exposed load. The multiply-adds are issued in pairs (fma.f32x2, two columns),
-// which leaves issue slots for everything else beside a full FMA pipe. Products and sums are float32 in ascending order of the
-// reduction index, so results do not depend on the launch. Bound by the FMA pipes.
+// One CTA of 64 threads computes 64 x 64 outputs of one expert, 8 x 8 per thread (where experts
+// have few rows 16 x 64, 2 x 8): a step of the reduction reads 16 values from shared memory for 64
+// fused multiply-adds. 16 steps at a time go through one of two buffers; the next 16 are in
+// registers on their way meanwhile, so a turn has one barrier and no exposed load. The multiply-adds
+// are issued in pairs (fma.f32x2, two columns), which leaves issue slots for everything else. Products
+// and sums are float32 in ascending order of the reduction index, so results do not depend on the
+// launch. Bound by shared memory and the FMA pipes (45 TFLOP/s at 8000 rows of [2048, 1024]), with
+// few rows by the weights.
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -18,8 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16, TT = 64;
-constexpr int LOADS = TM * TK / TT;      // values of each operand a thread moves per turn
+constexpr int TN = 64, TK = 16, TT = 64;
 
 enum { ROWS = 0, GRADX = 1, GRADW = 2 };
 
@@ -34,8 +35,10 @@ struct SimtParams {
   int32_t* status;
 };
 
-template <int MODE>
+template <int MODE, int TM>
 __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
+  constexpr int LA = TM * TK / TT, LB = TN * TK / TT;      // values of the operands a thread moves per turn
+  constexpr int MR = TM / 8;                               // rows of a thread's sums
   __shared__ __align__(16) float sa[2][TK][TM + 4], sb[2][TK][TN + 4];
   __shared__ grouped::Groups G;
   const int tid = threadIdx.x;
@@ -63,33 +66,39 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
     const int red = MODE == ROWS ? P.K : MODE == GRADX ? P.N : g.rows();
     const int mcount = MODE == GRADW ? P.N : g.rows();
     // Thread t moves values i = t, t + 64, ...: along the operand's contiguous index within a warp.
-    // Reduction-contiguous (x, w, d_y rows): r = t % 16, row t / 16 + 4 q; else column t, r = q.
+    // Reduction-contiguous (x, w, d_y rows): r = t % 16, row t / 16 + 4 q; else column t % width,
+    // r = t / width + q 64 / width.
     constexpr bool A_RED = MODE != GRADW, B_RED = MODE == ROWS;
-    const int ra = A_RED ? tid % TK : 0, ma = A_RED ? tid / TK : tid;
-    const int rb = B_RED ? tid % TK : 0, nb = B_RED ? tid / TK : tid;
+    constexpr int A_TURN = A_RED ? TT / TK : TT / TM, B_TURN = B_RED ? TT / TK : TT / TN;
+    const int ra = A_RED ? tid % TK : tid / TM, ma = A_RED ? tid / TK : tid % TM;
+    const int rb = B_RED ? tid % TK : tid / TN, nb = B_RED ? tid / TK : tid % TN;
     const long lda = MODE == ROWS ? P.K : P.N, ldb = P.K;
-    const float* at = A + (A_RED ? (long)(g.lo + m0 + ma) * lda + ra : (long)g.lo * lda + m0 + ma);
+    const float* at = A + (A_RED ? (long)(g.lo + m0 + ma) * lda + ra : (long)(g.lo + ra) * lda + m0 + ma);
     const float* bt = B + (MODE == ROWS    ? ((long)e * P.N + n0 + nb) * ldb + rb
-                           : MODE == GRADX ? (long)e * P.N * ldb + n0 + nb
-                                           : (long)g.lo * ldb + n0 + nb);
-    float pa[LOADS], pb[LOADS];
+                           : MODE == GRADX ? ((long)e * P.N + rb) * ldb + n0 + nb
+                                           : (long)(g.lo + rb) * ldb + n0 + nb);
+    float pa[LA], pb[LB];
     auto fetch = [&](int r0) {
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q) {
-        const bool a_in = A_RED ? m0 + ma + 4 * q < mcount && r0 + ra < red : m0 + ma < mcount && r0 + q < red;
-        const bool b_in = B_RED ? n0 + nb + 4 * q < cols && r0 + rb < red : n0 + nb < cols && r0 + q < red;
-        pa[q] = a_in ? __ldg(at + (A_RED ? 4 * q * lda + r0 : (long)(r0 + q) * lda)) : 0.0f;
-        pb[q] = b_in ? __ldg(bt + (B_RED ? 4 * q * ldb + r0 : (long)(r0 + q) * ldb)) : 0.0f;
+      for (int q = 0; q < LA; ++q) {
+        const bool in = A_RED ? m0 + ma + A_TURN * q < mcount && r0 + ra < red
+                              : m0 + ma < mcount && r0 + ra + A_TURN * q < red;
+        pa[q] = in ? __ldg(at + (A_RED ? A_TURN * q * lda + r0 : (long)(r0 + A_TURN * q) * lda)) : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < LB; ++q) {
+        const bool in = B_RED ? n0 + nb + B_TURN * q < cols && r0 + rb < red
+                              : n0 + nb < cols && r0 + rb + B_TURN * q < red;
+        pb[q] = in ? __ldg(bt + (B_RED ? B_TURN * q * ldb + r0 : (long)(r0 + B_TURN * q) * ldb)) : 0.0f;
       }
     };
     auto put = [&](int buf) {
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q) {
-        sa[buf][A_RED ? ra : q][A_RED ? ma + 4 * q : ma] = pa[q];
-        sb[buf][B_RED ? rb : q][B_RED ? nb + 4 * q : nb] = pb[q];
-      }
+      for (int q = 0; q < LA; ++q) sa[buf][A_RED ? ra : ra + A_TURN * q][A_RED ? ma + A_TURN * q : ma] = pa[q];
+#pragma unroll
+      for (int q = 0; q < LB; ++q) sb[buf][B_RED ? rb : rb + B_TURN * q][B_RED ? nb + B_TURN * q : nb] = pb[q];
     };
-    uint64_t acc[8][4] = {};       // pairs of columns
+    uint64_t acc[MR][4] = {};       // pairs of columns
     fetch(0);
     __syncthreads();       // the previous tile's last reads
     put(0);
@@ -100,14 +109,21 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
       if (more) fetch(r0 + TK);
 #pragma unroll
       for (int r = 0; r < TK; ++r) {
-        const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8 + 4]);
+        float av[MR];
+        if constexpr (MR == 8) {
+          const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8]);
+          const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][r][ty * 8 + 4]);
+          av[0] = a0.x; av[1] = a0.y; av[2] = a0.z; av[3] = a0.w;
+          av[4] = a1.x; av[5] = a1.y; av[6] = a1.z; av[7] = a1.w;
+        } else {
+          const float2 a0 = *reinterpret_cast<const float2*>(&sa[buf][r][ty * 2]);
+          av[0] = a0.x; av[1] = a0.y;
+        }
         const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&sb[buf][r][tx * 4]);
         const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&sb[buf][r][tx * 4 + 32]);
-        const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
         const uint64_t bv[4] = {b0.x, b0.y, b1.x, b1.y};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < MR; ++i) {
           uint64_t aa;
           asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(av[i]));
 #pragma unroll
@@ -120,8 +136,8 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int m = m0 + ty * 8 + i;
+    for (int i = 0; i < MR; ++i) {
+      const int m = m0 + ty * MR + i;
       if (m >= mcount) continue;
       const long row = MODE == GRADW ? (long)e * P.N + m : g.lo + m;
 #pragma unroll
@@ -136,19 +152,27 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
     grouped::zero_unowned(out, G, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
 }
 
-template <int MODE>
-int launch(const SimtParams& p, cudaStream_t s, const char* name) {
+template <int MODE, int TM>
+int launch_tiles(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
   const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt : ((long)(p.S + TM - 1) / TM + p.E) * nt;
-  // Six CTAs fit an SM. When all tiles are resident at once some SMs get six and others four, and the
-  // six set the time; with room for four (the unused shared memory says so) the rest go where one ends:
-  // 2000 rows, 8 experts of [1030, 517], 680 tiles: 69 us instead of 88. With more tiles than that six
-  // are the faster: 8000 rows, [2048, 1024]: 740 us instead of 798.
-  const long full = (long)num_sms() * 6;
-  const size_t unused = tiles <= full ? 22000 : 0;
+  // Six CTAs of 64 x 64 fit an SM. When all tiles are resident at once some SMs get six and others
+  // four, and the six set the time; with room for four (the unused shared memory says so) the rest go
+  // where one ends: 2000 rows, 8 experts of [1030, 517], 680 tiles: 69 us instead of 88. With more
+  // tiles than that six are the faster: 8000 rows, [2048, 1024]: 740 us instead of 798.
+  const long full = (long)num_sms() * (TM == 64 ? 6 : 11);
+  const size_t unused = TM == 64 && tiles <= full ? 22000 : 0;
   ProfScope ps(name, s);
-  grouped_simt_kernel<MODE><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, unused, s>>>(p);
+  grouped_simt_kernel<MODE, TM><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, unused, s>>>(p);
   return check_launch(name);
+}
+
+template <int MODE>
+int launch(const SimtParams& p, cudaStream_t s, const char* name) {
+  // few rows per expert: tiles of 16 rows, so that CTAs mostly stream weights (128 rows, 32 experts of
+  // [2048, 1024]: 128 us instead of 234; 19 rows per expert 176 / 187, 32 rows 244 / 200)
+  if (MODE != GRADW && p.flags == nullptr && p.S <= 16L * p.E) return launch_tiles<MODE, 16>(p, s, name);
+  return launch_tiles<MODE, 64>(p, s, name);
 }
 
 SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out, const int* flags, int nflags) {

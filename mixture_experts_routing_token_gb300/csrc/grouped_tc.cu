@@ -396,7 +396,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
 #pragma unroll
           for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(sum[c * 32 + j]);
           const int c0 = ti.n * BN + half * 128 + c * 32;
-          if (mine && c0 < J.C) grouped::store_cols(dst, c0, J.C, J.vec, y);
+          if (J.vec > 0) {
+            if (mine && c0 < J.C) grouped::store_cols(dst, c0, J.C, J.vec, y);
+          } else if (nrows > 0 && c0 < J.C) {
+            grouped::store_turned(y, dst - (long)lane * J.C, nrows, c0, J.C);
+          }
         }
         continue;
       }
@@ -418,7 +422,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (mine && c0 + h * 32 < J.C) grouped::store_cols(dst, c0 + h * 32, J.C, 0, y[h]);
+            if (nrows > 0 && c0 + h * 32 < J.C)
+              grouped::store_turned(y[h], dst - (long)lane * J.C, nrows, c0 + h * 32, J.C);
         }
       }
       ptx::tc_fence_before();
@@ -640,7 +645,7 @@ size_t split_bytes(Carver& c, long rows, int cols) {
 size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd) {
   Carver c(nullptr);
   if (dtype == MOE_F32) {
-    if (!grouped_f32_uses_tensor_cores(S, K, N, E)) return 0;
+    if (!grouped_f32_uses_tensor_cores(S, K, N, E, !fwd)) return 0;
     c.take<int>(kSplitBlocks);
     split_bytes(c, S, K);
     split_bytes(c, (long)E * N, K);

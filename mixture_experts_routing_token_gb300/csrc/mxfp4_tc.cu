@@ -257,7 +257,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ptx::tmem_ld32(taddr + c, v);
           ptx::tmem_ld_wait();
           const int c0 = ti.n * BN + c;
-          if (mine && c0 < P.cols) grouped::store_cols(dst, c0, P.cols, P.vec, v);
+          if (P.vec > 0) {
+            if (mine && c0 < P.cols) grouped::store_cols(dst, c0, P.cols, P.vec, v);
+          } else if (m - lane < ti.g.rows() && c0 < P.cols) {
+            grouped::store_turned(v, dst - (long)lane * P.cols, ti.g.rows() - (m - lane), c0, P.cols);
+          }
         }
       }
       ptx::tc_fence_before();

@@ -662,7 +662,7 @@ MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int
   a.ws = ws;
   a.status = status;
   if (dtype == MOE_F32 && !grouped_f32_uses_tensor_cores(S, K, N, E, false))
-    return launch_grouped_simt(a, nullptr, 0, (cudaStream_t)stream);
+    return launch_grouped_simt(a, nullptr, (cudaStream_t)stream);
   return launch_grouped_tc(a, (cudaStream_t)stream);
 }
 
@@ -707,8 +707,8 @@ MOE_API int moe_grouped_gemm_backward(const void* x, const void* w, const void* 
     return d_w_or_null ? zero_out(d_w_or_null, (size_t)E * N * K * dsize(dtype), (cudaStream_t)stream) : MOE_OK;
   if (dtype != MOE_F32 || grouped_f32_uses_tensor_cores(S, K, N, E, true))
     return launch_grouped_tc_backward(a, (cudaStream_t)stream);
-  if (a.d_x && (rc = launch_grouped_simt_dx(a, nullptr, 0, (cudaStream_t)stream))) return rc;
-  if (a.d_w && (rc = launch_grouped_simt_dw(a, nullptr, 0, (cudaStream_t)stream))) return rc;
+  if (a.d_x && (rc = launch_grouped_simt_dx(a, nullptr, (cudaStream_t)stream))) return rc;
+  if (a.d_w && (rc = launch_grouped_simt_dw(a, nullptr, (cudaStream_t)stream))) return rc;
   return MOE_OK;
 }
 

@@ -230,9 +230,9 @@ struct GroupedArgs {
   void* ws;
   int32_t* status;
 };
-int launch_grouped_simt(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
-int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
-int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s);
+int launch_grouped_simt(const GroupedArgs& a, const int* flags, cudaStream_t s);
+int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, cudaStream_t s);
+int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t s);
 // The tensor cores; the workspace holds padded copies of 16-bit operands whose rows are not a multiple
 // of 16 bytes, and float32 operands in three parts.
 // float32 takes the tensor cores where there is enough to multiply for what making the parts costs

@@ -103,6 +103,21 @@ __device__ __forceinline__ void zero_unowned(T* out, const Groups& G, int E, int
   for (long j = (long)G.off[E] * cols + i; j < (long)S * cols; j += n) out[j] = from_float<T>(0.0f);
 }
 
+// float32 products in parts: one word per block of the kernel that makes the parts, not 0 where it
+// met a value that parts do not stand for (kFlagWords in all). Thread `i` of `n` looks at its share,
+// all loads under way together.
+constexpr int kFlagWords = 1024;
+template <int N>
+__device__ __forceinline__ int any_flag(const int* flags, int i) {
+  int any = 0;
+#pragma unroll
+  for (int j = 0; j < kFlagWords / 4 / N; ++j) {
+    const int4 q = __ldg(reinterpret_cast<const int4*>(flags) + i + j * N);
+    any |= q.x | q.y | q.z | q.w;
+  }
+  return any;
+}
+
 // Two values of a 16-bit type in one word.
 template <class T>
 __device__ __forceinline__ uint32_t pack_pair(float a, float b);

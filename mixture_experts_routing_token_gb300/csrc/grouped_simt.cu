@@ -30,8 +30,7 @@ struct SimtParams {
   float* out;
   const int32_t* offsets;
   int S, K, N, E;
-  const int* flags;     // null, or words of which one must be set for the kernel to do anything
-  int nflags;
+  const int* flags;     // null, or grouped::any_flag must hold for the kernel to do anything
   int32_t* status;
 };
 
@@ -45,11 +44,7 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   const int cols = MODE == ROWS ? P.N : P.K;           // columns of the output
   const int NT = (cols + TN - 1) / TN;
   const int MT = (P.N + TM - 1) / TM;                  // GRADW: row tiles of an expert's output
-  if (P.flags != nullptr) {
-    int any = 0;
-    for (int i = tid; i < P.nflags; i += TT) any |= __ldg(P.flags + i);
-    if (!__syncthreads_or(any)) return;
-  }
+  if (P.flags != nullptr && !__syncthreads_or(grouped::any_flag<TT>(P.flags, tid))) return;
   if (tid < 32)
     grouped::group_list(P.offsets, P.E, P.S,
                        [&](int rows) { return MODE == GRADW ? MT * NT : (rows + TM - 1) / TM * NT; }, G);
@@ -175,23 +170,23 @@ int launch(const SimtParams& p, cudaStream_t s, const char* name) {
   return launch_tiles<MODE, 64>(p, s, name);
 }
 
-SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out, const int* flags, int nflags) {
+SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out, const int* flags) {
   return SimtParams{static_cast<const float*>(left), static_cast<const float*>(right), static_cast<float*>(out),
-                    a.offsets, a.S, a.K, a.N, a.E, flags, nflags, a.status};
+                    a.offsets, a.S, a.K, a.N, a.E, flags, a.status};
 }
 
 }  // namespace
 
-int launch_grouped_simt(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
-  return launch<ROWS>(params(a, a.x, a.w, a.y, flags, nflags), s, "grouped_gemm");
+int launch_grouped_simt(const GroupedArgs& a, const int* flags, cudaStream_t s) {
+  return launch<ROWS>(params(a, a.x, a.w, a.y, flags), s, "grouped_gemm");
 }
 
-int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
-  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x, flags, nflags), s, "grouped_gemm_dx");
+int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, cudaStream_t s) {
+  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x, flags), s, "grouped_gemm_dx");
 }
 
-int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, int nflags, cudaStream_t s) {
-  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w, flags, nflags), s, "grouped_gemm_dw");
+int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t s) {
+  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w, flags), s, "grouped_gemm_dw");
 }
 
 }  // namespace moe

@@ -87,8 +87,7 @@ struct Params {
   Job rows;         // y or d_x
   Job dw;           // d_w
   int dw_first;
-  const int* flags;   // float32: one word per block of the kernel that made the parts, set where it met a
-  int nflags;         // value that parts do not stand for
+  const int* flags;   // float32: grouped::any_flag
   int32_t* status;
   uint64_t wait_ns;
 };
@@ -234,9 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
     grouped::group_list(P.offsets, P.E, P.S,
                         [&](int rows) { return P.rows.out ? (rows + 2 * BM - 1) / (2 * BM) * P.rows.NT : 0; }, G);
   if (F32 && warp == 3) {
-    int any = 0;
-    for (int i = lane; i < P.nflags; i += 32) any |= __ldg(P.flags + i);
-    any = __any_sync(0xffffffffu, any);
+    const int any = __any_sync(0xffffffffu, grouped::any_flag<32>(P.flags, lane));
     if (lane == 0) skip = any;
   }
   ptx::tc_fence_before();
@@ -565,7 +562,7 @@ struct Split {
 struct SplitParams {
   Split m[3];
   int count;
-  int* flags;           // one word per block
+  int* flags;           // grouped::kFlagWords, one per block and zeros
 };
 
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
@@ -612,9 +609,9 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
   }
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) P.flags[blockIdx.x] = any;
+  if (blockIdx.x == 0)
+    for (int i = gridDim.x + threadIdx.x; i < grouped::kFlagWords; i += blockDim.x) P.flags[i] = 0;
 }
-
-constexpr int kSplitBlocks = 1024;
 
 void add_split(SplitParams& p, const void* src, long rows, int cols, Carver& c, Mat* m) {
   const int pc = pad8(cols);
@@ -626,9 +623,8 @@ void add_split(SplitParams& p, const void* src, long rows, int cols, Carver& c, 
 int launch_split(SplitParams& p, Params* out, cudaStream_t s) {
   long n = 0;
   for (int i = 0; i < p.count; ++i) n = std::max(n, p.m[i].n);
-  const int grid = (int)std::max(1L, std::min((n + 255) / 256, (long)kSplitBlocks));
+  const int grid = (int)std::max(1L, std::min((n + 255) / 256, (long)grouped::kFlagWords));
   out->flags = p.flags;
-  out->nflags = grid;
   ProfScope ps("grouped_split", s);
   const cudaError_t e = launch_pdl(split_kernel, grid, 256, 0, s, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped_split: %s", cudaGetErrorString(e));
@@ -646,7 +642,7 @@ size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd) {
   Carver c(nullptr);
   if (dtype == MOE_F32) {
     if (!grouped_f32_uses_tensor_cores(S, K, N, E, !fwd)) return 0;
-    c.take<int>(kSplitBlocks);
+    c.take<int>(grouped::kFlagWords);
     split_bytes(c, S, K);
     split_bytes(c, (long)E * N, K);
     if (!fwd) split_bytes(c, S, N);
@@ -664,11 +660,11 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   Carver c(a.ws);
   Mat x, w;
   int rc;
-  Params p{a.offsets, a.S, a.E, job(a.dtype, a.K, a.N, a.y, 0, 0), Job{}, 0, nullptr, 0, a.status, wait_limit_ns()};
+  Params p{a.offsets, a.S, a.E, job(a.dtype, a.K, a.N, a.y, 0, 0), Job{}, 0, nullptr, a.status, wait_limit_ns()};
   const bool f32 = a.dtype == MOE_F32;
   if (f32) {
     SplitParams q{};
-    q.flags = c.take<int>(kSplitBlocks);
+    q.flags = c.take<int>(grouped::kFlagWords);
     add_split(q, a.x, a.S, a.K, c, &x);
     add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
@@ -685,7 +681,7 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   const long tiles = row_tiles(a, p.rows.NT);
   if (f32) {
     if ((rc = launch<false, float>(m, p, tiles, s, "grouped_gemm"))) return rc;
-    return launch_grouped_simt(a, p.flags, p.nflags, s);
+    return launch_grouped_simt(a, p.flags, s);
   }
   return a.dtype == MOE_BF16 ? launch<false, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm")
                              : launch<false, __half>(m, p, tiles, s, "grouped_gemm");
@@ -696,12 +692,12 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   Mat dy{}, x{}, w{};
   CUtensorMap m[4] = {};
   int rc;
-  Params p{a.offsets, a.S, a.E, Job{}, Job{}, 0, nullptr, 0, a.status, wait_limit_ns()};
+  Params p{a.offsets, a.S, a.E, Job{}, Job{}, 0, nullptr, a.status, wait_limit_ns()};
   const bool f32 = a.dtype == MOE_F32;
   const uint64_t parts = f32 ? 3 : 1;
   if (f32) {
     SplitParams q{};
-    q.flags = c.take<int>(kSplitBlocks);
+    q.flags = c.take<int>(grouped::kFlagWords);
     add_split(q, a.d_y, a.S, a.N, c, &dy);
     if (a.d_w) add_split(q, a.x, a.S, a.K, c, &x);
     if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
@@ -732,8 +728,8 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   const char* name = "grouped_gemm_backward";
   if (f32) {
     if ((rc = launch<true, float>(m, p, tiles, s, name))) return rc;
-    if (a.d_x && (rc = launch_grouped_simt_dx(a, p.flags, p.nflags, s))) return rc;
-    return a.d_w ? launch_grouped_simt_dw(a, p.flags, p.nflags, s) : MOE_OK;
+    if (a.d_x && (rc = launch_grouped_simt_dx(a, p.flags, s))) return rc;
+    return a.d_w ? launch_grouped_simt_dw(a, p.flags, s) : MOE_OK;
   }
   return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, p, tiles, s, name)
                              : launch<true, __half>(m, p, tiles, s, name);

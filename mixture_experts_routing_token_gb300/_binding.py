@@ -378,6 +378,7 @@ def moe_layer_forward(hidden, router_logits, w13, w2, k, norm_topk_prob=True, ou
 
 
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_U8, _I32 = torch.uint8, torch.int32
 
 
 def _code(dtype):
@@ -387,59 +388,79 @@ def _code(dtype):
         raise ValueError(f"unsupported dtype {dtype}") from None
 
 
-def _take(t, name, dtype, device=None):
-    """Address of an input tensor after its checks (one call per tensor: a decode step makes few)."""
+# The calls below are made per layer and token, so their checks are few and cheap: one condition per
+# tensor, and what was wrong with it is found out afterwards.
+
+def _refuse(t, name, dtype, index):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+
+
+def _first(t, name):
+    """(address, dtype, device index) of the tensor that the others go by."""
+    if not isinstance(t, torch.Tensor):
+        _refuse(t, name, None, -1)
+    index = t.get_device()
+    if index < 0 or not t.is_contiguous():
+        _refuse(t, name, None, index)
+    return t.data_ptr(), t.dtype, index
+
+
+def _take(t, name, dtype, index):
+    """Address of an input after its checks."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, dtype, index)
     return t.data_ptr()
 
 
-def _give(t, name, shape, dtype, device):
+def _give(t, name, shape, dtype, index):
     """(tensor, address) of an output: the caller's after its checks, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
         return t, t.data_ptr()
-    p = _take(t, name, dtype, device)
+    p = _take(t, name, dtype, index)
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t, p
 
 
-def _status_ptr(status, device):
+def _status_ptr(status, index):
     if status is None:
         return None
-    p = _take(status, "status", torch.int32, device)
+    p = _take(status, "status", _I32, index)
     if status.numel() < 1:
         raise ValueError("status must hold an int32 word")
     return p
 
 
-def _raw(stream, device):
+def _raw(stream, index):
     """Handle of the caller's stream or of the current one, as an integer."""
-    if stream is None and _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return _stream(stream, device).value
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return _stream(stream, torch.device("cuda", index)).value
 
 
-def _call(fn, name, size, device, workspace, before, after):
-    """fn(*before, ws, ws_bytes, *after), with a workspace of ``size()`` bytes made here when the call
-    needs one and the caller gave none (most calls need none: the library is asked first)."""
+def _space(workspace, index):
+    """(address, bytes) of the caller's workspace, nothing without one: a call that needs one then says so."""
     if workspace is None:
-        rc = fn(*before, None, 0, *after)
-        if rc == MOE_ERR_WORKSPACE:
-            workspace = torch.empty(size(), dtype=torch.uint8, device=device)
-            rc = fn(*before, workspace.data_ptr(), workspace.numel(), *after)
-    else:
-        p = _take(workspace, "workspace", workspace.dtype, device)
-        rc = fn(*before, p, workspace.numel() * workspace.element_size(), *after)
-    if rc:
-        _check(name, rc)
+        return None, 0
+    return _take(workspace, "workspace", workspace.dtype, index), workspace.numel() * workspace.element_size()
+
+
+def _again(name, rc, size, workspace, index, stream, call):
+    """A call came back with an error: without a workspace where one is needed, one is made. It goes back to
+    the current stream's pool when this returns, so a call on another stream is noted with it."""
+    if rc == MOE_ERR_WORKSPACE and workspace is None:
+        buf = torch.empty(size(), dtype=_U8, device=f"cuda:{index}")
+        rc = call(buf.data_ptr(), buf.numel())
+        if stream is not None:
+            buf.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    _check(name, rc)
 
 
 def moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E) -> int:
@@ -451,20 +472,23 @@ def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, strea
 
     ``x [S, K]``, ``w [E, N, K]`` (float32, bf16 or float16); ``offsets [E+1]`` int32: expert e owns the
     rows ``offsets[e]`` to ``offsets[e+1] - 1``. Rows without an expert give zero rows."""
-    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
-    dtype, d = x.dtype, x.device
+    xp, dtype, d = _first(x, "x")
     wp = _take(w, "w", dtype, d)
-    op = _take(offsets, "offsets", torch.int32, d)
+    op = _take(offsets, "offsets", _I32, d)
     dt = _code(dtype)
-    if x.dim() != 2 or w.dim() != 3:
+    xs, wsh = x.shape, w.shape
+    if len(xs) != 2 or len(wsh) != 3 or wsh[2] != xs[1] or offsets.shape != (wsh[0] + 1,):
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
-    S, K = x.shape
-    E, N, Kw = w.shape
-    if Kw != K or offsets.shape != (E + 1,):
-        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
+    S, K = xs
+    E, N, _ = wsh
     out, yp = _give(out, "out", (S, N), dtype, d)
-    _call(lib().moe_grouped_gemm, "moe_grouped_gemm", lambda: moe_grouped_gemm_workspace_size(dt, S, K, N, E), d, workspace,
-          (xp, wp, dt, S, K, N, E, op, yp), (_status_ptr(status, d), _raw(stream, d)))
+    ws, nb = _space(workspace, d)
+    st, sm = _status_ptr(status, d), _raw(stream, d)
+    f = lib().moe_grouped_gemm
+    rc = f(xp, wp, dt, S, K, N, E, op, yp, ws, nb, st, sm)
+    if rc:
+        _again("moe_grouped_gemm", rc, lambda: moe_grouped_gemm_workspace_size(dt, S, K, N, E), workspace, d, stream,
+               lambda p, n: f(xp, wp, dt, S, K, N, E, op, yp, p, n, st, sm))
     return out
 
 
@@ -477,23 +501,26 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
     """Gradients of :func:`moe_grouped_gemm` for ``d_y [S, N]`` -> (d_x [S, K], d_w [E, N, K]) in x's dtype.
 
     One that is not wanted is None. Experts without rows get a zero ``d_w``, rows without an expert a zero ``d_x``."""
-    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
-    dtype, d = x.dtype, x.device
+    xp, dtype, d = _first(x, "x")
     wp = _take(w, "w", dtype, d)
     gp = _take(d_y, "d_y", dtype, d)
-    op = _take(offsets, "offsets", torch.int32, d)
+    op = _take(offsets, "offsets", _I32, d)
     dt = _code(dtype)
-    if x.dim() != 2 or w.dim() != 3:
+    xs, wsh = x.shape, w.shape
+    if (len(xs) != 2 or len(wsh) != 3 or wsh[2] != xs[1] or offsets.shape != (wsh[0] + 1,)
+            or d_y.shape != (xs[0], wsh[1])):
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
-    S, K = x.shape
-    E, N, Kw = w.shape
-    if Kw != K or offsets.shape != (E + 1,) or d_y.shape != (S, N):
-        raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
-    d_x, dxp = _give(d_x, "d_x", (S, K), dtype, d) if want_d_x else (None, None)
-    d_w, dwp = _give(d_w, "d_w", (E, N, K), dtype, d) if want_d_w else (None, None)
-    _call(lib().moe_grouped_gemm_backward, "moe_grouped_gemm_backward",
-          lambda: moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E), d, workspace,
-          (xp, wp, gp, dt, S, K, N, E, op, dxp, dwp), (_status_ptr(status, d), _raw(stream, d)))
+    S, K = xs
+    E, N, _ = wsh
+    d_x, dxp = _give(d_x, "d_x", xs, dtype, d) if want_d_x else (None, None)
+    d_w, dwp = _give(d_w, "d_w", wsh, dtype, d) if want_d_w else (None, None)
+    ws, nb = _space(workspace, d)
+    st, sm = _status_ptr(status, d), _raw(stream, d)
+    f = lib().moe_grouped_gemm_backward
+    rc = f(xp, wp, gp, dt, S, K, N, E, op, dxp, dwp, ws, nb, st, sm)
+    if rc:
+        _again("moe_grouped_gemm_backward", rc, lambda: moe_grouped_gemm_backward_workspace_size(dt, S, K, N, E),
+               workspace, d, stream, lambda p, n: f(xp, wp, gp, dt, S, K, N, E, op, dxp, dwp, p, n, st, sm))
     return d_x, d_w
 
 
@@ -507,36 +534,44 @@ def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, workspace=None, st
     Blocks of 32 values share the power of two ``2^(scale - 127)``; two codes to a byte, the first one low.
     ``rows [R]`` int32 picks the rows (row r from ``x[rows[r]]``); without it R is T. ``x`` may have more
     than two dimensions when no rows are given: they are kept."""
-    xp = _take(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
-    d = x.device
-    dt = _code(x.dtype)
-    lead, K = x.shape[:-1], x.shape[-1] if x.dim() else 0
-    if x.dim() < 2 or K % 32:
+    xp, dtype, d = _first(x, "x")
+    dt = _code(dtype)
+    xs = x.shape
+    if len(xs) < 2 or xs[-1] % 32:
         raise ValueError("x must be [T, K] (or [..., K] without rows) with K a multiple of 32")
-    T = lead.numel()
-    rp, R = None, T
-    if rows is not None:
-        rp = _take(rows, "rows", torch.int32, d)
-        if x.dim() != 2 or rows.dim() != 1:
-            raise ValueError("rows must be [R] and x [T, K]")
+    K = xs[-1]
+    if rows is None:
+        rp, lead = None, tuple(xs[:-1])
+        T = R = xs[:-1].numel()
+    else:
+        rp = _take(rows, "rows", _I32, d)
         lead = rows.shape
-        R = lead[0]
-    codes, cp = _give(codes, "codes", (*lead, K // 2), torch.uint8, d)
-    scales, sp = _give(scales, "scales", (*lead, K // 32), torch.uint8, d)
-    _call(lib().moe_mxfp4_quantize, "moe_mxfp4_quantize", lambda: moe_mxfp4_quantize_workspace_size(T, K, rows is not None, R),
-          d, workspace, (xp, dt, T, K, rp, R, cp, sp), (_status_ptr(status, d), _raw(stream, d)))
+        if len(xs) != 2 or len(lead) != 1:
+            raise ValueError("rows must be [R] and x [T, K]")
+        T, R = xs[0], lead[0]
+    codes, cp = _give(codes, "codes", (*lead, K // 2), _U8, d)
+    scales, sp = _give(scales, "scales", (*lead, K // 32), _U8, d)
+    ws, nb = _space(workspace, d)
+    st, sm = _status_ptr(status, d), _raw(stream, d)
+    f = lib().moe_mxfp4_quantize
+    rc = f(xp, dt, T, K, rp, R, cp, sp, ws, nb, st, sm)
+    if rc:
+        _again("moe_mxfp4_quantize", rc, lambda: moe_mxfp4_quantize_workspace_size(T, K, rows is not None, R), workspace,
+               d, stream, lambda p, n: f(xp, dt, T, K, rp, R, cp, sp, p, n, st, sm))
     return codes, scales
 
 
 def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values that ``codes [..., K/2]`` and ``scales [..., K/32]`` stand for -> [..., K] of ``dtype``."""
-    cp = _take(codes, "codes", torch.uint8)
-    d = codes.device
-    sp = _take(scales, "scales", torch.uint8, d)
+    cp, _, d = _first(codes, "codes")
+    if codes.dtype is not _U8:
+        _refuse(codes, "codes", _U8, d)
+    sp = _take(scales, "scales", _U8, d)
     dt = _code(dtype)
-    if codes.dim() < 1 or codes.shape[-1] % 16:
+    cs = codes.shape
+    if len(cs) < 1 or cs[-1] % 16:
         raise ValueError("codes must be [..., K / 2] with K a multiple of 32")
-    lead, K = codes.shape[:-1], 2 * codes.shape[-1]
+    lead, K = cs[:-1], 2 * cs[-1]
     if scales.shape != (*lead, K // 32):
         raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32]")
     out, op = _give(out, "out", (*lead, K), dtype, d)
@@ -558,22 +593,24 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
     ``x_codes [S, K/2]``, ``x_scales [S, K/32]``, ``w_codes [E, N, K/2]``, ``w_scales [E, N, K/32]`` from
     :func:`moe_mxfp4_quantize`. ``activation="silu_and_mul"`` returns [S, N/2]: silu of the first half of
     the columns times the second half."""
-    u8 = torch.uint8
-    xp = _take(x_codes, "x_codes", u8)
-    d = x_codes.device
-    xsp = _take(x_scales, "x_scales", u8, d)
-    wp = _take(w_codes, "w_codes", u8, d)
-    wsp = _take(w_scales, "w_scales", u8, d)
-    op = _take(offsets, "offsets", torch.int32, d)
+    xp, dtype, d = _first(x_codes, "x_codes")
+    if dtype is not _U8:
+        _refuse(x_codes, "x_codes", _U8, d)
+    xsp = _take(x_scales, "x_scales", _U8, d)
+    wp = _take(w_codes, "w_codes", _U8, d)
+    wsp = _take(w_scales, "w_scales", _U8, d)
+    op = _take(offsets, "offsets", _I32, d)
     dt = _code(out_dtype)
-    if x_codes.dim() != 2 or w_codes.dim() != 3:
+    xs, wsh = x_codes.shape, w_codes.shape
+    if len(xs) != 2 or len(wsh) != 3:
         raise ValueError("shapes must be x_codes [S, K / 2], w_codes [E, N, K / 2]")
-    S, K = x_codes.shape
-    E, N, Kw = w_codes.shape
-    if Kw != K or K % 16 or x_scales.shape != (S, K // 16) or w_scales.shape != (E, N, K // 16) or offsets.shape != (E + 1,):
+    S, half = xs
+    E, N, same = wsh
+    if (same != half or half % 16 or x_scales.shape != (S, half // 16) or w_scales.shape != (E, N, half // 16)
+            or offsets.shape != (E + 1,)):
         raise ValueError("shapes must be x_codes [S, K / 2], x_scales [S, K / 32], w_codes [E, N, K / 2], "
                          "w_scales [E, N, K / 32], offsets [E + 1] with K a multiple of 32")
-    K *= 2
+    K = 2 * half
     cols, act = N, MOE_ACT_NONE
     if activation is not None:
         if activation != "silu_and_mul":
@@ -582,9 +619,13 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
             raise ValueError("silu_and_mul needs an even N")
         cols, act = N // 2, MOE_ACT_SILU_AND_MUL
     out, yp = _give(out, "out", (S, cols), out_dtype, d)
-    _call(lib().moe_mxfp4_grouped_gemm, "moe_mxfp4_grouped_gemm",
-          lambda: moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation), d, workspace,
-          (xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp), (_status_ptr(status, d), _raw(stream, d)))
+    ws, nb = _space(workspace, d)
+    st, sm = _status_ptr(status, d), _raw(stream, d)
+    f = lib().moe_mxfp4_grouped_gemm
+    rc = f(xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, ws, nb, st, sm)
+    if rc:
+        _again("moe_mxfp4_grouped_gemm", rc, lambda: moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation),
+               workspace, d, stream, lambda p, n: f(xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, p, n, st, sm))
     return out
 
 

@@ -218,6 +218,105 @@ def test_bad_offsets_are_reported(moe, dtype):
         assert int(status.item()) == moe.MOE_STATUS_BAD_INDEX
 
 
+def test_no_more_than_the_workspace_is_written(moe):
+    """A workspace of just the size asked for, with guards on both sides."""
+    off = torch.tensor([0, 200, 200, 600], dtype=torch.int32, device=DEV)
+    for dtype, K, N in (("bf16", 129, 515), ("f32", 513, 515), ("f16", 257, 130)):
+        t = TYPES[dtype][0]
+        x, _ = draw((600, K), dtype, 1)
+        w, _ = draw((3, N, K), dtype, 2)
+        g, _ = draw((600, N), dtype, 3)
+        code = {"f32": moe.MOE_F32, "bf16": moe.MOE_BF16, "f16": moe.MOE_F16}[dtype]
+        n = moe.moe_grouped_gemm_workspace_size(code, 600, K, N, 3)
+        m = moe.moe_grouped_gemm_backward_workspace_size(code, 600, K, N, 3)
+        assert n > 0 and m > 0
+        buf = torch.full((max(n, m) + 8192,), 77, dtype=torch.uint8, device=DEV)
+        y = moe.moe_grouped_gemm(x, w, off, workspace=buf[4096:4096 + n])
+        assert torch.equal(y, moe.moe_grouped_gemm(x, w, off))
+        assert (buf[:4096] == 77).all() and (buf[4096 + n:] == 77).all()
+        moe.moe_grouped_gemm_backward(x, w, off, g, workspace=buf[4096:4096 + m])
+        assert (buf[:4096] == 77).all() and (buf[4096 + m:] == 77).all()
+        with pytest.raises(moe.MoeError, match="too small"):
+            moe.moe_grouped_gemm(x, w, off, workspace=buf[4096:4096 + n - 256])
+    c, s = moe.moe_mxfp4_quantize(torch.randn(600, 288, device=DEV))
+    wc, ws = moe.moe_mxfp4_quantize(torch.randn(3, 260, 288, device=DEV))
+    for act in (None, "silu_and_mul"):
+        n = moe.moe_mxfp4_grouped_gemm_workspace_size(600, 288, 260, 3, act)
+        assert n > 0
+        buf = torch.full((n + 8192,), 77, dtype=torch.uint8, device=DEV)
+        y = moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, off, activation=act, workspace=buf[4096:4096 + n])
+        assert torch.equal(y, moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, off, activation=act))
+        assert (buf[:4096] == 77).all() and (buf[4096 + n:] == 77).all()
+
+
+def test_binding_refusals(moe):
+    x, _ = draw((10, 64), "bf16", 1)
+    w, _ = draw((2, 32, 64), "bf16", 2)
+    off = torch.tensor([0, 4, 10], dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_grouped_gemm(x.t().contiguous().t(), w, off)
+    with pytest.raises(ValueError, match="w must be torch.bfloat16"):
+        moe.moe_grouped_gemm(x, w.half(), off)
+    with pytest.raises(ValueError, match="shapes"):
+        moe.moe_grouped_gemm(x, w[:, :, :32].contiguous(), off)
+    with pytest.raises(ValueError, match="shapes"):
+        moe.moe_grouped_gemm(x, w, off[:2].contiguous())
+    with pytest.raises(ValueError, match="int32"):
+        moe.moe_grouped_gemm(x, w, off.long())
+    with pytest.raises(ValueError, match="out must have shape"):
+        moe.moe_grouped_gemm(x, w, off, out=torch.empty(10, 31, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        moe.moe_grouped_gemm(x.double(), w.double(), off)
+    with pytest.raises(ValueError, match="status"):
+        moe.moe_grouped_gemm(x, w, off, status=torch.zeros(1, device=DEV))
+    with pytest.raises(moe.MoeError, match="aligned"):
+        moe.moe_grouped_gemm(torch.zeros(10 * 64 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(10, 64), w, off)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        moe.moe_mxfp4_quantize(torch.zeros(4, 48, device=DEV))
+    with pytest.raises(ValueError, match="rows"):
+        moe.moe_mxfp4_quantize(torch.zeros(4, 2, 64, device=DEV), rows=off)
+    c, s = moe.moe_mxfp4_quantize(x)
+    wc, ws = moe.moe_mxfp4_quantize(w)
+    with pytest.raises(ValueError, match="activation"):
+        moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, off, activation="gelu")
+    with pytest.raises(ValueError, match="scales"):
+        moe.moe_mxfp4_grouped_gemm(c, s[:, :1].contiguous(), wc, ws, off)
+    with pytest.raises(ValueError, match="even"):
+        moe.moe_mxfp4_grouped_gemm(c, s, wc[:, :31].contiguous(), ws[:, :31].contiguous(), off, activation="silu_and_mul")
+    with pytest.raises(ValueError, match="scales"):
+        moe.moe_mxfp4_dequantize(c, s[:5])
+
+
+def test_wait_limits_give_up(moe):
+    """A limit too short for any wait: the kernels report it and the next call is right."""
+    off = torch.tensor([0, 300, 1000], dtype=torch.int32, device=DEV)
+    x, _ = draw((1000, 512), "bf16", 1)
+    w, _ = draw((2, 512, 512), "bf16", 2)
+    g, _ = draw((1000, 512), "bf16", 3)
+    c, s = moe.moe_mxfp4_quantize(x)
+    wc, ws = moe.moe_mxfp4_quantize(w)
+    calls = [lambda st: moe.moe_grouped_gemm(x, w, off, status=st),
+             lambda st: moe.moe_grouped_gemm(x.float(), w.float(), off, status=st),
+             lambda st: moe.moe_grouped_gemm_backward(x, w, off, g, status=st)[1],
+             lambda st: moe.moe_grouped_gemm(x[:20].contiguous(), w, off.clamp(max=20), status=st),
+             lambda st: moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, off, status=st),
+             lambda st: moe.moe_mxfp4_grouped_gemm(c[:20].contiguous(), s[:20].contiguous(), wc, ws, off.clamp(max=20), activation="silu_and_mul", status=st)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = [f(status).clone() for f in calls]
+    assert int(status.item()) == 0
+    for f, y in zip(calls, want):
+        before = moe.set_wait_limit_ns(1)
+        try:
+            status.zero_()
+            f(status)
+            torch.cuda.synchronize()
+            assert int(status.item()) == moe.MOE_STATUS_TIMEOUT
+        finally:
+            moe.set_wait_limit_ns(before)
+        status.zero_()
+        assert torch.equal(f(status), y) and int(status.item()) == 0
+
+
 def test_empty_sizes(moe):
     o = torch.zeros(3, dtype=torch.int32, device=DEV)
     for dtype in (torch.float32, torch.bfloat16):
@@ -264,6 +363,26 @@ def test_other_stream_and_graph(moe):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(dx, wx) and torch.equal(dw, ww) and torch.equal(y4, w4)
+
+
+def test_workspace_on_a_stream_of_the_callers(moe):
+    """A call on another stream with a workspace of its own making: what the current stream allocates
+    next must not be that workspace while the call may still run."""
+    off = torch.tensor([0, 200, 600], dtype=torch.int32, device=DEV)
+    x, _ = draw((600, 129), "bf16", 1)
+    w, _ = draw((2, 515, 129), "bf16", 2)
+    want = moe.moe_grouped_gemm(x, w, off)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2000000)
+        moe.moe_grouped_gemm(x, w, off, out=got, stream=stream)
+        junk = [torch.full((moe.moe_grouped_gemm_workspace_size(moe.MOE_BF16, 600, 129, 515, 2),), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and junk
 
 
 # ---- 4-bit microscaled values ----------------------------------------------------------

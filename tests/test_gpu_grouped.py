@@ -317,6 +317,60 @@ def test_wait_limits_give_up(moe):
         assert torch.equal(f(status), y) and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("S", [3000, 90000])
+def test_most_experts(moe, S):
+    """1024 experts, most with few rows, some with none, in every operator."""
+    rng = np.random.default_rng(S)
+    counts = rng.multinomial(S, rng.dirichlet(np.full(1024, 0.3)))
+    off = offsets_of(counts)
+    assert (counts == 0).any()
+    o = torch.from_numpy(off).to(DEV)
+    for dtype in ("f32", "bf16"):
+        x, x64 = draw((S, 64), dtype, 1)
+        w, w64 = draw((1024, 72, 64), dtype, 2)
+        g, g64 = draw((S, 72), dtype, 3)
+        check(moe.moe_grouped_gemm(x, w, o), grouped.grouped_gemm(x64, w64, off), grouped.grouped_gemm(abs(x64), abs(w64), off), 64, dtype, "y")
+        d_x, d_w = moe.moe_grouped_gemm_backward(x, w, o, g)
+        rx, rw = grouped.grouped_gemm_backward(x64, w64, off, g64)
+        ax, aw = grouped.grouped_gemm_backward(abs(x64), abs(w64), off, abs(g64))
+        check(d_x, rx, ax, 72, dtype, "d_x")
+        check(d_w, rw, aw, int(counts.max()), dtype, "d_w")
+    c, s = moe.moe_mxfp4_quantize(x)
+    wc, ws = moe.moe_mxfp4_quantize(w)
+    xv, wv = to64(moe.moe_mxfp4_dequantize(c, s)), to64(moe.moe_mxfp4_dequantize(wc, ws))
+    check(moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, o), grouped.grouped_gemm(xv, wv, off), grouped.grouped_gemm(abs(xv), abs(wv), off), 64, "bf16", "y4")
+
+
+def test_more_than_2_31_elements(moe):
+    """Rows whose element offsets pass 32 bits, in inputs and outputs: the last ones are those of a
+    call on them alone."""
+    S, n = 1100000, 777
+    off = torch.tensor([0, 5, S - n, S], dtype=torch.int32, device=DEV)
+    tail = torch.tensor([0, 0, 0, n], dtype=torch.int32, device=DEV)
+    x = torch.empty(S, 2048, dtype=torch.bfloat16, device=DEV)
+    x[:-n].fill_(1.0)
+    x[-n:] = draw((n, 2048), "bf16", 1)[0]
+    w, _ = draw((3, 64, 2048), "bf16", 2)
+    y = moe.moe_grouped_gemm(x, w, off)
+    assert torch.equal(y[-n:], moe.moe_grouped_gemm(x[-n:].contiguous(), w, tail))
+    w2, _ = draw((3, 2048, 64), "bf16", 3)
+    y2 = moe.moe_grouped_gemm(y, w2, off)                       # output past 2^31
+    assert torch.equal(y2[-n:], moe.moe_grouped_gemm(y[-n:].contiguous(), w2, tail))
+    d_x, _ = moe.moe_grouped_gemm_backward(x, w, off, y, d_x=y2, want_d_w=False)
+    want, dw = moe.moe_grouped_gemm_backward(x[-n:].contiguous(), w, tail, y[-n:].contiguous())
+    assert torch.equal(d_x[-n:], want)
+    _, d_w = moe.moe_grouped_gemm_backward(x, w, off, y, want_d_x=False)
+    assert torch.equal(d_w[2], dw[2])
+    c, s = moe.moe_mxfp4_quantize(x)
+    tc, ts = moe.moe_mxfp4_quantize(x[-n:].contiguous())
+    assert torch.equal(c[-n:], tc) and torch.equal(s[-n:], ts)
+    moe.moe_mxfp4_dequantize(c, s, out=y2)
+    assert torch.equal(y2[-n:], moe.moe_mxfp4_dequantize(tc, ts))
+    wc, ws = moe.moe_mxfp4_quantize(w)
+    y4 = moe.moe_mxfp4_grouped_gemm(c, s, wc, ws, off, out=y)
+    assert torch.equal(y4[-n:], moe.moe_mxfp4_grouped_gemm(tc, ts, wc, ws, tail))
+
+
 def test_empty_sizes(moe):
     o = torch.zeros(3, dtype=torch.int32, device=DEV)
     for dtype in (torch.float32, torch.bfloat16):

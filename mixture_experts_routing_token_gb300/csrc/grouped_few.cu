@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
         for (int i = 0; i < 6; ++i) {
           const int r = lane + 32 * (i < 4 ? i : i - 4);
           const uint8_t* row = nullptr;
+          const uint8_t* end = i < 4 ? P.w_scales + (long)P.E * P.N * P.count : P.x_scales + (long)P.S * P.count;
           if (i < 4) {
             const int c = SILU ? r & 63 : r;
             if (c < u.cols)
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            v[i][h] = row != nullptr ? mx::scale16(row, k0 * 8 + h * 16, P.count, P.vec) : make_uint4(0, 0, 0, 0);
+            v[i][h] = row != nullptr ? mx::scale16(row, k0 * 8 + h * 16, P.count, P.vec, end) : make_uint4(0, 0, 0, 0);
         }
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&sf_empty[me]), ((uint32_t)(turn >> 2) & 1u) ^ 1u,
                                                     abort_p, P.wait_ns));

@@ -507,25 +507,6 @@ Job job(int dtype, int R, int C, void* out, int a_mn, int b_mn) {
 
 long row_tiles(const GroupedArgs& a, int NT) { return ((long)(a.S + 2 * BM - 1) / (2 * BM) + a.E) * NT; }
 
-// Rows whose bytes are not a multiple of 16 cannot be read by TMA: a copy with rows padded
-// to one, zeros in between (an odd width is a small problem's; the copy is one pass over the
-// operand at memory speed, against falling off the tensor cores).
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ src, long rows, int cols, int padded,
-                                                       uint4* __restrict__ dst) {
-  pdl_wait();
-  pdl_trigger();
-  const int P8 = padded / 8;
-  const long n = rows * P8;
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
-    const long r = i / P8;
-    const int c = (int)(i - r * P8) * 8;
-    uint32_t v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(src + r * cols + c + j) : 0u;
-    dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-  }
-}
-
 struct Mat {
   const void* p;
   int cols;      // of a row as stored (a multiple of 8)
@@ -533,19 +514,57 @@ struct Mat {
 
 int pad8(int c) { return (c + 7) / 8 * 8; }
 
-// The matrix itself, or a padded copy of it in the workspace.
-int padded(const void* src, long rows, int cols, Carver& c, Mat* m, cudaStream_t s) {
+// Rows whose bytes are not a multiple of 16 cannot be read by TMA: copies with rows padded to one,
+// zeros in between (an odd width is a small problem's; the copy is one pass over the operand at
+// memory speed, against falling off the tensor cores).
+struct Pad {
+  const uint16_t* src;
+  uint4* dst;
+  long n;               // pieces of 8 columns
+  int cols, pieces;     // columns; pieces of a row
+};
+
+struct PadParams {
+  Pad m[3];
+  int count;
+};
+
+__global__ void __launch_bounds__(256) pad_rows_kernel(const PadParams P) {
+  pdl_wait();
+  pdl_trigger();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (k >= P.count) break;
+    const Pad M = P.m[k];
+    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < M.n; i += (long)gridDim.x * blockDim.x) {
+      const long r = M.n < (1L << 31) ? (long)((uint32_t)i / (uint32_t)M.pieces) : i / M.pieces;
+      const int c = (int)(i - r * M.pieces) * 8;
+      const uint16_t* p = M.src + r * M.cols + c;
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < M.cols ? __ldg(p + j) : 0u;
+      M.dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+}
+
+// The matrix itself, or the place of its padded copy in the workspace (made by launch_pads).
+void padded(PadParams& p, const void* src, long rows, int cols, Carver& c, Mat* m) {
   *m = Mat{src, cols};
-  if (cols % 8 == 0) return MOE_OK;
+  if (cols % 8 == 0) return;
   m->cols = pad8(cols);
   uint16_t* dst = c.take<uint16_t>((size_t)rows * m->cols);
   m->p = dst;
-  if (rows == 0) return MOE_OK;
-  const long n = rows * (m->cols / 8);
+  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * (m->cols / 8), cols, m->cols / 8};
+}
+
+int launch_pads(const PadParams& p, cudaStream_t s) {
+  if (p.count == 0) return MOE_OK;
+  long n = 0;
+  for (int i = 0; i < p.count; ++i) n = std::max(n, p.m[i].n);
+  const int grid = (int)std::max(1L, std::min((n + 255) / 256, (long)num_sms() * 16));
   ProfScope ps("grouped_pad_rows", s);
-  const int grid = (int)std::min((n + 255) / 256, (long)num_sms() * 16);
-  const cudaError_t e = launch_pdl(pad_rows_kernel, grid, 256, 0, s, static_cast<const uint16_t*>(src), rows, cols,
-                                   m->cols, reinterpret_cast<uint4*>(dst));
+  const cudaError_t e = launch_pdl(pad_rows_kernel, grid, 256, 0, s, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "grouped_pad_rows: %s", cudaGetErrorString(e));
   return check_launch("grouped_pad_rows");
 }
@@ -669,8 +688,10 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
     add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    if ((rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
-    if ((rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
+    PadParams q{};
+    padded(q, a.x, a.S, a.K, c, &x);
+    padded(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    if ((rc = launch_pads(q, s))) return rc;
     if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
   }
   const uint64_t parts = f32 ? 3 : 1;
@@ -703,9 +724,11 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
     if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    if ((rc = padded(a.d_y, a.S, a.N, c, &dy, s))) return rc;
-    if (a.d_x && (rc = padded(a.w, (long)a.E * a.N, a.K, c, &w, s))) return rc;
-    if (a.d_w && (rc = padded(a.x, a.S, a.K, c, &x, s))) return rc;
+    PadParams q{};
+    padded(q, a.d_y, a.S, a.N, c, &dy);
+    if (a.d_x) padded(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    if (a.d_w) padded(q, a.x, a.S, a.K, c, &x);
+    if ((rc = launch_pads(q, s))) return rc;
   }
   long tiles = 0;
   if (a.d_x) {

@@ -66,20 +66,39 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// 16 scale bytes of a row from byte b on; those past its end are 0 (their codes are, too).
-__device__ __forceinline__ uint4 scale16(const uint8_t* row, int b, int count, int vec) {
+// 16 scale bytes of a row from byte b on; those past its end are 0 (their codes are, too). `end` is
+// the end of the whole array. Rows that are no multiple of 4 bytes (vec 1) are read in the aligned
+// words around them and shifted into place; words that would pass the array's end byte by byte.
+__device__ __forceinline__ uint4 scale16(const uint8_t* row, int b, int count, int vec, const uint8_t* end) {
   if (vec == 16) return b < count ? __ldg(reinterpret_cast<const uint4*>(row + b)) : make_uint4(0, 0, 0, 0);
   uint32_t w[4];
+  if (vec == 4) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = b + 4 * j;
-    w[j] = 0;
-    if (vec == 4) {
-      if (at < count) w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
+    for (int j = 0; j < 4; ++j)
+      w[j] = b + 4 * j < count ? __ldg(reinterpret_cast<const uint32_t*>(row + b + 4 * j)) : 0u;
+  } else {
+    const uint8_t* p = row + b;
+    const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint8_t* a = p - shift;
+    uint32_t q[5];
+    if (a + 20 <= end) {
+#pragma unroll
+      for (int j = 0; j < 5; ++j) q[j] = b + 4 * j - (int)shift < count ? __ldg(reinterpret_cast<const uint32_t*>(a) + j) : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(q[j], q[j + 1], 8 * shift);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (at + i < count) w[j] |= (uint32_t)__ldg(row + at + i) << (8 * i);
+      for (int j = 0; j < 4; ++j) {
+        w[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (b + 4 * j + i < count) w[j] |= (uint32_t)__ldg(p + 4 * j + i) << (8 * i);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {      // what belongs to the next row
+      const int left = count - b - 4 * j;
+      if (left < 4) w[j] = left <= 0 ? 0u : w[j] & ((1u << (8 * left)) - 1u);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(256) mxfp4_scales_kernel(const ScaleParams P) 
     const uint8_t* rows[4];
     uint4* dst;
     int step_stride;        // uint4 between the atoms of one step and the next
+    const uint8_t* end = block < x_blocks ? P.x_scales + (long)P.S * P.count : P.w_scales + (long)P.E * P.N * P.count;
     if (block < x_blocks) {
       const int e = grouped::find(G.start, P.E, block);
       const grouped::Span g = G.span(e);
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(256) mxfp4_scales_kernel(const ScaleParams P) 
     }
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mx::scale16(rows[i], step * 8, P.count, P.vec);
+    for (int i = 0; i < 4; ++i) v[i] = mx::scale16(rows[i], step * 8, P.count, P.vec, end);
     dst[lane] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
     dst[32 + lane] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
     if (step + 1 < P.steps) {

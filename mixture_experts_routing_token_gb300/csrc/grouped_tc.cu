@@ -174,10 +174,12 @@ __device__ __forceinline__ Tile tile_at(int t, At& at, const grouped::Groups& G,
 }
 
 // GRAD = false: P.rows is y, tmA / tmB its operands. GRAD: P.rows is d_x (tmA, tmB), P.dw d_w (tmC, tmD).
+// tmRows, tmDw: the outputs, where they are 16-bit and stored by TMA.
 template <bool GRAD, class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 1)
     grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
+                        const __grid_constant__ CUtensorMap tmRows, const __grid_constant__ CUtensorMap tmDw,
                         const Params P) {
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE], tail_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
@@ -415,7 +417,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
           uint32_t words[32];
           grouped::pack_words<T, 32>(y[0], words);
           grouped::pack_words<T, 32>(y[1], words + 16);
-          if (nrows > 0 && c0 < J.C) grouped::store_rows(sbuf, words, dst - (long)lane * J.C, nrows, c0, 64, J.C);
+          // d_w: the tensor's own edge ends the rows; y, d_x: the group does, so a box needs all of its 32
+          if (nrows > 0 && c0 < J.C)
+            grouped::store_rows(sbuf, words, ti.dw ? &tmDw : &tmRows, c0, ti.dw ? m - lane : ti.g.lo + m - lane, ti.dw ? ti.e : 0,
+                                ti.dw || nrows >= 32, dst - (long)lane * J.C, nrows, J.C);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -428,6 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
       if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
       if (++acc == 2) { acc = 0; aph ^= 1u; }
     }
+    if (lane == 0) ptx::tma_store_wait();
     if (P.rows.out != nullptr && !*abort_p)
       grouped::zero_unowned(static_cast<T*>(P.rows.out), G, P.E, P.S, P.rows.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
@@ -483,12 +489,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
 static_assert(A_BYTES == 2 * (int)MN_BLOCK && B_BYTES == 2 * (int)MN_BLOCK, "a stage is four boxes of 64 x 64");
 
 template <bool GRAD, class T>
-int launch(const CUtensorMap (&m)[4], const Params& p, long most_tiles, cudaStream_t s, const char* name) {
+int launch(const CUtensorMap (&m)[4], const GroupedArgs& a, const Params& p, long most_tiles, cudaStream_t s, const char* name) {
   if (int rc = ensure_smem_limit(grouped_pair_kernel<GRAD, T>, dsmem_bytes<T>(), name)) return rc;
   const int grid = 2 * (int)std::max(1L, std::min(most_tiles, (long)(num_sms() / 2)));
+  CUtensorMap rows = m[0], dw = m[0];      // not used where the job is not wanted or not stored by TMA
+  if (!is_f32<T>()) {
+    int rc;
+    if (p.rows.out && p.rows.vec && (rc = make_tmap_3d(&rows, p.rows.out, 2, (uint64_t)p.rows.C, (uint64_t)a.S, 1, 64, 32)))
+      return rc;
+    if (p.dw.out && p.dw.vec &&
+        (rc = make_tmap_3d(&dw, p.dw.out, 2, (uint64_t)p.dw.C, (uint64_t)p.dw.M, (uint64_t)a.E, 64, 32)))
+      return rc;
+  }
   ProfScope ps(name, s);
-  const cudaError_t e =
-      launch_pdl(grouped_pair_kernel<GRAD, T>, grid, threads<GRAD, T>(), dsmem_bytes<T>(), s, m[0], m[1], m[2], m[3], p);
+  const cudaError_t e = launch_pdl(grouped_pair_kernel<GRAD, T>, grid, threads<GRAD, T>(), dsmem_bytes<T>(), s, m[0], m[1],
+                                   m[2], m[3], rows, dw, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }
@@ -701,11 +716,11 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   m[2] = m[3] = m[0];      // not read
   const long tiles = row_tiles(a, p.rows.NT);
   if (f32) {
-    if ((rc = launch<false, float>(m, p, tiles, s, "grouped_gemm"))) return rc;
+    if ((rc = launch<false, float>(m, a, p, tiles, s, "grouped_gemm"))) return rc;
     return launch_grouped_simt(a, p.flags, s);
   }
-  return a.dtype == MOE_BF16 ? launch<false, __nv_bfloat16>(m, p, tiles, s, "grouped_gemm")
-                             : launch<false, __half>(m, p, tiles, s, "grouped_gemm");
+  return a.dtype == MOE_BF16 ? launch<false, __nv_bfloat16>(m, a, p, tiles, s, "grouped_gemm")
+                             : launch<false, __half>(m, a, p, tiles, s, "grouped_gemm");
 }
 
 int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
@@ -750,12 +765,12 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   p.dw_first = a.S / a.E > a.N;
   const char* name = "grouped_gemm_backward";
   if (f32) {
-    if ((rc = launch<true, float>(m, p, tiles, s, name))) return rc;
+    if ((rc = launch<true, float>(m, a, p, tiles, s, name))) return rc;
     if (a.d_x && (rc = launch_grouped_simt_dx(a, p.flags, s))) return rc;
     return a.d_w ? launch_grouped_simt_dw(a, p.flags, s) : MOE_OK;
   }
-  return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, p, tiles, s, name)
-                             : launch<true, __half>(m, p, tiles, s, name);
+  return a.dtype == MOE_BF16 ? launch<true, __nv_bfloat16>(m, a, p, tiles, s, name)
+                             : launch<true, __half>(m, a, p, tiles, s, name);
 }
 
 }  // namespace moe

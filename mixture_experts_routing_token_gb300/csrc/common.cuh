@@ -250,7 +250,8 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s);
 // Measured, us, that kernel / the SM-pair kernel, 64 experts [2816, 2048]: 16-bit 115 / 128 at 16
 // rows, 118 / 130 at 32, 148 / 133 at 64; 4-bit 38.7 / 48.9, 45.0 / 49.2, 80.5 / 50.1. 8 experts
 // [14336, 4096]: 16-bit 142 / 153 at 32, 173 / 156 at 64; 4-bit 45.4 / 57.4, 55.8 / 58.4.
-inline bool grouped_few_rows(int S, int E) { return S <= 32L * E; }
+constexpr int kFewRows = 32;
+inline bool grouped_few_rows(int S, int E) { return S <= (long)kFewRows * E; }
 // Few rows per expert (grouped_few.cu): x, w with rows of `cols` elements (a multiple of 8).
 int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s);
 

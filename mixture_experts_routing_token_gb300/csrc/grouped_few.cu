@@ -21,7 +21,7 @@
 // be 176 units for 152 SMs, two rounds of which the second is nearly empty; 80 columns make 288.
 // The box has f rows because TMA instructions are what limits a unit otherwise: with boxes of 16
 // rows a step took 600 cycles whatever its size (33 GB/s an SM at f = 80).
-// A group of more than 64 rows is several units that read the same weights next to each other.
+// A group of more than 64 rows is several heads, whose units read the same weights at about the same time.
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -35,6 +35,7 @@ constexpr int BOX = 16;                  // rows per TMA box
 constexpr int BOX_BYTES = BOX * ROWB;
 constexpr int MAXF = 128;                // MMA M
 constexpr int MAXR = 64;                 // rows of x per unit (MMA N at most)
+constexpr int MAXHEADS = MOE_MAX_EXPERTS + kFewRows * MOE_MAX_EXPERTS / MAXR;   // (expert, 64 rows) of a launch
 constexpr int CHUNK = 4;                 // steps whose scales one warp loads together
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
@@ -71,18 +72,18 @@ struct Unit {
   int e, row, rows, n0, cols;    // group row of its first row of x; columns [n0, n0 + cols)
 };
 
-__device__ __forceinline__ Unit unit_at(int t, const grouped::Groups& G, const Params& P, int f, int tiles) {
-  // G.start counts heads; the heads of an expert that share a column tile follow each other
-  const int e = grouped::find(G.start, P.E, grouped::quick_div(t, tiles));
+// Unit t: head t / tiles (an expert's next 64 rows), column tile t % tiles. Every role looks its units
+// up, and with short reductions that is what the MMA issuer waits for (a search over the experts and
+// two divisions took 1000 of 3000 cycles a unit at K = 352), so the heads have a list.
+__device__ __forceinline__ Unit unit_at(int t, const grouped::Groups& G, const uint16_t* expert_of, const Params& P, int tiles) {
+  const int head = grouped::quick_div(t, tiles), tile = t - head * tiles, e = expert_of[head];
   const grouped::Span g = G.span(e);
-  const int heads = G.start[e + 1] - G.start[e], local = t - G.start[e] * tiles;
-  const int tile = grouped::quick_div(local, heads), head = local - tile * heads;
   Unit u;
   u.e = e;
-  u.row = g.lo + head * MAXR;
+  u.row = g.lo + (head - G.start[e]) * MAXR;
   u.rows = min(MAXR, g.hi - u.row);
-  u.n0 = tile * f;
-  u.cols = min(f, P.cols - u.n0);
+  u.n0 = tile * P.f;
+  u.cols = min(P.f, P.cols - u.n0);
   return u;
 }
 
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
   __shared__ int abort_flag;
   __shared__ int s_most;
   __shared__ grouped::Groups G;
+  __shared__ uint16_t expert_of[MAXHEADS];
   __shared__ float up_part[SILU ? 64 : 1][17];      // up columns of 16 rows, on their way to the gate's warps
   extern __shared__ uint8_t dsmem_raw[];
 
@@ -150,6 +152,9 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
     const int most =
         grouped::group_list(P.offsets, P.E, P.S, [](int rows) { return (rows + MAXR - 1) / MAXR; }, G);
     if (lane == 0) s_most = min(most, MAXR);
+    __syncwarp();
+    for (int e = lane; e < P.E; e += 32)
+      for (int h = G.start[e]; h < G.start[e + 1]; ++h) expert_of[h] = (uint16_t)e;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Unit u = unit_at(t, G, P, f, tiles);
+        const Unit u = unit_at(t, G, expert_of, P, tiles);
         const int nb = (u.rows + BOX - 1) / BOX;
         for (int k = 0; k < P.steps; ++k) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
       int stage = 0, acc = 0, set = 0, turn = 0;   // turn: chunks of scales so far
       uint32_t ph = 0, aph = 0;
       for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const Unit u = unit_at(t, G, P, f, tiles);
+        const Unit u = unit_at(t, G, expert_of, P, tiles);
         const int n = (u.rows + BOX - 1) / BOX * BOX;
         const uint32_t idesc = P.idesc | ((uint32_t)(n >> 3) << 17);
         if (!ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns)) break;
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
     int acc = 0;
     uint32_t aph = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const Unit u = unit_at(t, G, P, f, tiles);
+      const Unit u = unit_at(t, G, expert_of, P, tiles);
       // every epilogue warp sees the same outcome: the gate's exchange needs all four
       bool ok = ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns);
       if (SILU) ok = !named_bar_or(1, 128, !ok);
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
     int turn = 0;                        // chunks so far, over all units
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Unit u = unit_at(t, G, P, f, tiles);
+      const Unit u = unit_at(t, G, expert_of, P, tiles);
       for (int k0 = 0; k0 < P.steps && ok; k0 += CHUNK, ++turn) {
         if ((turn & 3) != me) continue;
         // rows l, l + 32, l + 64, l + 96 of w and l, l + 32 of x; what the unit does not have is 0

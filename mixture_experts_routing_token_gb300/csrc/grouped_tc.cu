@@ -537,40 +537,85 @@ struct Pad {
   uint4* dst;
   long n;               // pieces of 8 columns
   int cols, pieces;     // columns; pieces of a row
+  int per;              // rows of an expert's matrix (0: not by expert)
 };
 
+// The experts that have rows, in shared memory: nothing reads the weights of the others, and a few
+// tokens reach few experts. (A group needs offsets[e] < offsets[e + 1], whatever the list is like.)
+struct Live {
+  uint16_t expert[MOE_MAX_EXPERTS];
+  int count;
+};
+
+// Whole block.
+__device__ __forceinline__ void live_list(const int32_t* offsets, int E, Live& live) {
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + (int)threadIdx.x;
+      const bool on = e < E && __ldg(offsets + e) < __ldg(offsets + e + 1);
+      const unsigned m = __ballot_sync(0xffffffffu, on);
+      if (on) live.expert[n + __popc(m & ((1u << threadIdx.x) - 1u))] = (uint16_t)e;
+      n += __popc(m);
+    }
+    if (threadIdx.x == 0) live.count = n;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ long div_by(long n, int d) {
+  return n < (1L << 31) ? (long)((uint32_t)n / (uint32_t)d) : n / d;
+}
+
+// Row and piece of the i-th piece of a matrix, of live experts only where it is by expert.
+__device__ __forceinline__ long piece_row(long i, int pieces, int per, const Live& live, int& piece) {
+  long r = div_by(i, pieces);
+  piece = (int)(i - r * pieces);
+  if (per) {
+    const long k = div_by(r, per);
+    r += (live.expert[k] - k) * per;
+  }
+  return r;
+}
+
 struct PadParams {
+  const int32_t* offsets;
+  int E;
   Pad m[3];
   int count;
 };
 
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadParams P) {
+  __shared__ Live live;
   pdl_wait();
   pdl_trigger();
+  live_list(P.offsets, P.E, live);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (k >= P.count) break;
     const Pad M = P.m[k];
-    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < M.n; i += (long)gridDim.x * blockDim.x) {
-      const long r = M.n < (1L << 31) ? (long)((uint32_t)i / (uint32_t)M.pieces) : i / M.pieces;
-      const int c = (int)(i - r * M.pieces) * 8;
+    const long n = M.per ? (long)live.count * M.per * M.pieces : M.n;
+    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
+      int piece;
+      const long r = piece_row(i, M.pieces, M.per, live, piece);
+      const int c = piece * 8;
       const uint16_t* p = M.src + r * M.cols + c;
       uint32_t v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = c + j < M.cols ? __ldg(p + j) : 0u;
-      M.dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      M.dst[r * M.pieces + piece] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
   }
 }
 
 // The matrix itself, or the place of its padded copy in the workspace (made by launch_pads).
-void padded(PadParams& p, const void* src, long rows, int cols, Carver& c, Mat* m) {
+void padded(PadParams& p, const void* src, long rows, int cols, int per, Carver& c, Mat* m) {
   *m = Mat{src, cols};
   if (cols % 8 == 0) return;
   m->cols = pad8(cols);
   uint16_t* dst = c.take<uint16_t>((size_t)rows * m->cols);
   m->p = dst;
-  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * (m->cols / 8), cols, m->cols / 8};
+  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * (m->cols / 8), cols, m->cols / 8, per};
 }
 
 int launch_pads(const PadParams& p, cudaStream_t s) {
@@ -591,9 +636,12 @@ struct Split {
   uint4* dst;           // [3 parts, rows, padded columns] bf16
   long n;               // pieces of 8 columns of one part
   int cols, pieces;     // columns; pieces of a row
+  int per;              // rows of an expert's matrix (0: not by expert)
 };
 
 struct SplitParams {
+  const int32_t* offsets;
+  int E;
   Split m[3];
   int count;
   int* flags;           // grouped::kFlagWords, one per block and zeros
@@ -605,16 +653,20 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
 
 // x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out.
 __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
+  __shared__ Live live;
   pdl_wait();
   pdl_trigger();
+  live_list(P.offsets, P.E, live);
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (k >= P.count) break;
     const Split M = P.m[k];
-    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < M.n; i += (long)gridDim.x * blockDim.x) {
-      const long r = M.n < (1L << 31) ? (long)((uint32_t)i / (uint32_t)M.pieces) : i / M.pieces;
-      const int c = (int)(i - r * M.pieces) * 8;
+    const long n = M.per ? (long)live.count * M.per * M.pieces : M.n;
+    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
+      int piece;
+      const long r = piece_row(i, M.pieces, M.per, live, piece);
+      const int c = piece * 8;
       const float* p = M.src + r * M.cols + c;
       float v[8];
       if ((M.cols & 3) == 0 && c + 8 <= M.cols) {
@@ -638,7 +690,7 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
         }
       }
 #pragma unroll
-      for (int part = 0; part < 3; ++part) M.dst[part * M.n + i] = make_uint4(q[part][0], q[part][1], q[part][2], q[part][3]);
+      for (int part = 0; part < 3; ++part) M.dst[part * M.n + r * M.pieces + piece] = make_uint4(q[part][0], q[part][1], q[part][2], q[part][3]);
     }
   }
   const int any = __syncthreads_or(bad);
@@ -647,11 +699,11 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
     for (int i = gridDim.x + threadIdx.x; i < grouped::kFlagWords; i += blockDim.x) P.flags[i] = 0;
 }
 
-void add_split(SplitParams& p, const void* src, long rows, int cols, Carver& c, Mat* m) {
+void add_split(SplitParams& p, const void* src, long rows, int cols, int per, Carver& c, Mat* m) {
   const int pc = pad8(cols);
   uint16_t* dst = c.take<uint16_t>((size_t)3 * rows * pc);
   *m = Mat{dst, pc};
-  p.m[p.count++] = Split{static_cast<const float*>(src), reinterpret_cast<uint4*>(dst), rows * (pc / 8), cols, pc / 8};
+  p.m[p.count++] = Split{static_cast<const float*>(src), reinterpret_cast<uint4*>(dst), rows * (pc / 8), cols, pc / 8, per};
 }
 
 int launch_split(SplitParams& p, Params* out, cudaStream_t s) {
@@ -698,14 +750,16 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
   const bool f32 = a.dtype == MOE_F32;
   if (f32) {
     SplitParams q{};
+    q.offsets = a.offsets;
+    q.E = a.E;
     q.flags = c.take<int>(grouped::kFlagWords);
-    add_split(q, a.x, a.S, a.K, c, &x);
-    add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    add_split(q, a.x, a.S, a.K, 0, c, &x);
+    add_split(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    PadParams q{};
-    padded(q, a.x, a.S, a.K, c, &x);
-    padded(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    PadParams q{a.offsets, a.E, {}, 0};
+    padded(q, a.x, a.S, a.K, 0, c, &x);
+    padded(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_pads(q, s))) return rc;
     if (grouped_few_rows(a.S, a.E)) return launch_grouped_few(a, x.p, w.p, x.cols, s);
   }
@@ -733,16 +787,18 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
   const uint64_t parts = f32 ? 3 : 1;
   if (f32) {
     SplitParams q{};
+    q.offsets = a.offsets;
+    q.E = a.E;
     q.flags = c.take<int>(grouped::kFlagWords);
-    add_split(q, a.d_y, a.S, a.N, c, &dy);
-    if (a.d_w) add_split(q, a.x, a.S, a.K, c, &x);
-    if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, c, &w);
+    add_split(q, a.d_y, a.S, a.N, 0, c, &dy);
+    if (a.d_w) add_split(q, a.x, a.S, a.K, 0, c, &x);
+    if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    PadParams q{};
-    padded(q, a.d_y, a.S, a.N, c, &dy);
-    if (a.d_x) padded(q, a.w, (long)a.E * a.N, a.K, c, &w);
-    if (a.d_w) padded(q, a.x, a.S, a.K, c, &x);
+    PadParams q{a.offsets, a.E, {}, 0};
+    padded(q, a.d_y, a.S, a.N, 0, c, &dy);
+    if (a.d_x) padded(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
+    if (a.d_w) padded(q, a.x, a.S, a.K, 0, c, &x);
     if ((rc = launch_pads(q, s))) return rc;
   }
   long tiles = 0;

@@ -230,6 +230,8 @@ struct GroupedArgs {
   void* ws;
   int32_t* status;
 };
+// The CUDA cores (float32); the workspace holds the pieces of reductions that are cut.
+size_t grouped_simt_workspace(int S, int K, int N, int E, bool fwd);
 int launch_grouped_simt(const GroupedArgs& a, const int* flags, cudaStream_t s);
 int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, cudaStream_t s);
 int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t s);

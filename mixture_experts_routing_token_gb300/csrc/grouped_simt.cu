@@ -30,6 +30,8 @@ struct SimtParams {
   float* out;
   const int32_t* offsets;
   int S, K, N, E;
+  int parts, chunk;     // the reduction in `parts` pieces of `chunk` (row outputs): piece k goes to partial + k S cols
+  float* partial;
   const int* flags;     // null, or grouped::any_flag must hold for the kernel to do anything
   int32_t* status;
 };
@@ -51,14 +53,18 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
   __syncthreads();
   if (G.bad && blockIdx.x == 0 && tid == 0 && P.status) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
   const float *A = P.a, *B = P.b;
-  float* out = P.out;
+  const int parts = MODE == GRADW ? 1 : P.parts;
   const int tx = tid & 7, ty = tid >> 3;
-  for (int t = blockIdx.x; t < G.start[P.E]; t += gridDim.x) {
+  const int total = G.start[P.E] * parts;
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int t = parts == 1 ? u : u / parts, part = u - t * parts;
     const int e = grouped::find(G.start, P.E, t);
     const grouped::Span g = G.span(e);
     const int local = t - G.start[e];
     const int m0 = local / NT * TM, n0 = (local - local / NT * NT) * TN;
-    const int red = MODE == ROWS ? P.K : MODE == GRADX ? P.N : g.rows();
+    const int whole = MODE == ROWS ? P.K : MODE == GRADX ? P.N : g.rows();
+    const int begin = parts == 1 ? 0 : part * P.chunk, red = parts == 1 ? whole : min(whole, begin + P.chunk);
+    float* out = parts == 1 ? P.out : P.partial + (long)part * P.S * cols;
     const int mcount = MODE == GRADW ? P.N : g.rows();
     // Thread t moves values i = t, t + 64, ...: along the operand's contiguous index within a warp.
     // Reduction-contiguous (x, w, d_y rows): r = t % 16, row t / 16 + 4 q; else column t % width,
@@ -94,12 +100,12 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
       for (int q = 0; q < LB; ++q) sb[buf][B_RED ? rb : rb + B_TURN * q][B_RED ? nb + B_TURN * q : nb] = pb[q];
     };
     uint64_t acc[MR][4] = {};       // pairs of columns
-    fetch(0);
+    fetch(begin);
     __syncthreads();       // the previous tile's last reads
     put(0);
     __syncthreads();
     int buf = 0;
-    for (int r0 = 0; r0 < red; r0 += TK, buf ^= 1) {
+    for (int r0 = begin; r0 < red; r0 += TK, buf ^= 1) {
       const bool more = r0 + TK < red;
       if (more) fetch(r0 + TK);
 #pragma unroll
@@ -143,19 +149,49 @@ __global__ void __launch_bounds__(TT) grouped_simt_kernel(const SimtParams P) {
       }
     }
   }
-  if (MODE != GRADW)
-    grouped::zero_unowned(out, G, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
+  if (MODE != GRADW && parts == 1)
+    grouped::zero_unowned(P.out, G, P.E, P.S, cols, (long)blockIdx.x * TT + tid, (long)gridDim.x * TT);
+}
+
+// out = the pieces' sum, in order; 0 for rows that no group owns.
+__global__ void __launch_bounds__(256) grouped_join_kernel(const float* __restrict__ partial, int parts, const int32_t* offsets,
+                                                           int E, int S, int cols, float* __restrict__ out) {
+  __shared__ grouped::Groups G;
+  if (threadIdx.x < 32) grouped::group_list(offsets, E, S, [](int) { return 0; }, G);
+  __syncthreads();
+  const long first = (long)G.off[0] * cols, last = (long)G.off[E] * cols, n = (long)S * cols;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
+    float v = 0.0f;
+    if (i >= first && i < last)
+      for (int k = 0; k < parts; ++k) v += __ldg(partial + k * n + i);
+    out[i] = v;
+  }
+}
+
+// Rows per tile: 16 where experts have few, so that CTAs mostly stream weights (128 rows, 32 experts of
+// [2048, 1024]: 128 us instead of 234; 19 rows per expert 176 / 187, 32 rows 244 / 200).
+int tile_rows(int S, int E) { return S <= 16L * E ? 16 : 64; }
+long resident(int TM) { return (long)num_sms() * (TM == 64 ? 6 : 11); }
+
+// Pieces of the reduction: where a launch has fewer tiles than fit the GPU and long reductions, as many
+// as fill it, of 256 steps at least (a tile takes a microsecond or so for 16 steps, however idle the rest).
+int reduction_parts(int S, int E, long cols, int R) {
+  const int TM = tile_rows(S, E);
+  const long tiles = ((long)(S + TM - 1) / TM + std::min(S, E)) * ((cols + TN - 1) / TN);
+  const long parts = std::min(std::min(resident(TM) / tiles, (long)R / 256), 16L);
+  return parts < 2 || S * cols * parts > (1L << 24) ? 1 : (int)parts;
 }
 
 template <int MODE, int TM>
 int launch_tiles(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
-  const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt : ((long)(p.S + TM - 1) / TM + p.E) * nt;
+  const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt
+                                   : ((long)(p.S + TM - 1) / TM + p.E) * nt * p.parts;
   // Six CTAs of 64 x 64 fit an SM. When all tiles are resident at once some SMs get six and others
   // four, and the six set the time; with room for four (the unused shared memory says so) the rest go
   // where one ends: 2000 rows, 8 experts of [1030, 517], 680 tiles: 69 us instead of 88. With more
   // tiles than that six are the faster: 8000 rows, [2048, 1024]: 740 us instead of 798.
-  const long full = (long)num_sms() * (TM == 64 ? 6 : 11);
+  const long full = resident(TM);
   const size_t unused = TM == 64 && tiles <= full ? 22000 : 0;
   ProfScope ps(name, s);
   grouped_simt_kernel<MODE, TM><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, unused, s>>>(p);
@@ -163,30 +199,48 @@ int launch_tiles(const SimtParams& p, cudaStream_t s, const char* name) {
 }
 
 template <int MODE>
-int launch(const SimtParams& p, cudaStream_t s, const char* name) {
-  // few rows per expert: tiles of 16 rows, so that CTAs mostly stream weights (128 rows, 32 experts of
-  // [2048, 1024]: 128 us instead of 234; 19 rows per expert 176 / 187, 32 rows 244 / 200)
-  if (MODE != GRADW && p.flags == nullptr && p.S <= 16L * p.E) return launch_tiles<MODE, 16>(p, s, name);
-  return launch_tiles<MODE, 64>(p, s, name);
+int launch(SimtParams& p, cudaStream_t s, const char* name) {
+  const int cols = MODE == ROWS ? p.N : p.K, R = MODE == ROWS ? p.K : p.N;
+  p.parts = MODE == GRADW || p.flags ? 1 : reduction_parts(p.S, p.E, cols, R);
+  p.chunk = ((R + p.parts - 1) / p.parts + TK - 1) / TK * TK;
+  int rc;
+  if (MODE != GRADW && p.flags == nullptr && tile_rows(p.S, p.E) == 16) rc = launch_tiles<MODE, 16>(p, s, name);
+  else rc = launch_tiles<MODE, 64>(p, s, name);
+  if (rc || p.parts == 1) return rc;
+  const long n = (long)p.S * cols;
+  ProfScope ps("grouped_join", s);
+  grouped_join_kernel<<<(unsigned)std::min((n + 255) / 256, (long)num_sms() * 8), 256, 0, s>>>(p.partial, p.parts, p.offsets, p.E,
+                                                                                         p.S, cols, p.out);
+  return check_launch("grouped_join");
 }
 
 SimtParams params(const GroupedArgs& a, const void* left, const void* right, void* out, const int* flags) {
   return SimtParams{static_cast<const float*>(left), static_cast<const float*>(right), static_cast<float*>(out),
-                    a.offsets, a.S, a.K, a.N, a.E, flags, a.status};
+                    a.offsets, a.S, a.K, a.N, a.E, 1, 0, static_cast<float*>(a.ws), flags, a.status};
 }
 
 }  // namespace
 
+size_t grouped_simt_workspace(int S, int K, int N, int E, bool fwd) {
+  if (S < 1) return 0;
+  const long cols = fwd ? N : K;
+  const int parts = reduction_parts(S, E, cols, fwd ? K : N);
+  return parts == 1 ? 0 : align_up((size_t)S * cols * parts * sizeof(float), 256);
+}
+
 int launch_grouped_simt(const GroupedArgs& a, const int* flags, cudaStream_t s) {
-  return launch<ROWS>(params(a, a.x, a.w, a.y, flags), s, "grouped_gemm");
+  SimtParams p = params(a, a.x, a.w, a.y, flags);
+  return launch<ROWS>(p, s, "grouped_gemm");
 }
 
 int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, cudaStream_t s) {
-  return launch<GRADX>(params(a, a.d_y, a.w, a.d_x, flags), s, "grouped_gemm_dx");
+  SimtParams p = params(a, a.d_y, a.w, a.d_x, flags);
+  return launch<GRADX>(p, s, "grouped_gemm_dx");
 }
 
 int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t s) {
-  return launch<GRADW>(params(a, a.d_y, a.x, a.d_w, flags), s, "grouped_gemm_dw");
+  SimtParams p = params(a, a.d_y, a.x, a.d_w, flags);
+  return launch<GRADW>(p, s, "grouped_gemm_dw");
 }
 
 }  // namespace moe

@@ -727,7 +727,7 @@ size_t split_bytes(Carver& c, long rows, int cols) {
 size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd) {
   Carver c(nullptr);
   if (dtype == MOE_F32) {
-    if (!grouped_f32_uses_tensor_cores(S, K, N, E, !fwd)) return 0;
+    if (!grouped_f32_uses_tensor_cores(S, K, N, E, !fwd)) return grouped_simt_workspace(S, K, N, E, fwd);
     c.take<int>(grouped::kFlagWords);
     split_bytes(c, S, K);
     split_bytes(c, (long)E * N, K);

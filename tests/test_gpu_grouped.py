@@ -65,8 +65,11 @@ SHAPES = [
 ]
 
 
-# float32 products this large go to the tensor cores in parts
+# float32: reductions cut into pieces; then products that go to the tensor cores in parts
 SHAPES_F32 = [
+    ([3, 0, 9, 1], 2, 4100, 130),
+    ([20, 7], 0, 90, 3001),
+    ([200, 90], 1, 2500, 70),
     ([257, 255, 0, 256, 1], 3, 520, 523),
     ([63, 65, 1, 0, 500], 0, 777, 333),
     ([700], 1, 129, 1100),

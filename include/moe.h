@@ -292,9 +292,14 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
  *   outside [0, S] or below its predecessor sets MOE_STATUS_BAD_INDEX (groups
  *   are cut to [0, S]; the rows concerned are then undefined).
  *   ws / ws_bytes: at least moe_grouped_gemm_workspace_size(...) bytes (0 for
- *   float32 and for 16-bit K % 8 == 0: then ws may be null).
+ *   16-bit K % 8 == 0 and for small float32 problems: then ws may be null; the
+ *   size for float32 depends on the current device's SM count).
  * S, K, N may have any size >= 0 (K = 0 gives zeros). 16-bit types run on the
- * tcgen05 tensor cores, float32 on the CUDA cores (full float32 products).
+ * tcgen05 tensor cores. float32 keeps float32's accuracy: on the CUDA cores, or
+ * for large products on the tensor cores in three bf16 parts per value (2^-26
+ * of each value, sums rounded to nearest every 128 terms; values below 2^-103
+ * keep an absolute 2^-126; operands with infinities, NaN or magnitudes of
+ * 2^127 and more take the CUDA cores, decided on the device).
  */
 MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E);
 MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
@@ -349,7 +354,8 @@ MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, in
  *   float32.
  *   activation MOE_ACT_NONE: y [S, N]; MOE_ACT_SILU_AND_MUL (N even): y [S, N / 2]
  *   = silu(columns 0 .. N/2 - 1) * (columns N/2 .. N - 1), as w13 is laid out in
- *   moe_grouped_ffn. y is of out_dtype (any of the three), rounded once.
+ *   moe_grouped_ffn (silu of arguments below -87 is 0). y is of out_dtype (any of
+ *   the three), rounded once.
  * offsets, rows without an expert and status as moe_grouped_gemm. A scale byte
  * of 255 makes its row's (or column's) sums NaN.
  * ws / ws_bytes: at least moe_mxfp4_grouped_gemm_workspace_size(...) bytes (the

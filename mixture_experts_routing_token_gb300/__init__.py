@@ -5,7 +5,9 @@ The compute lives in ``libmoe_gb300.so`` (hand-written CUDA for sm_103a behind
 the C ABI of ``include/moe.h``); this package is its thin Python binding with
 the same entry-point names. Build the library with :func:`build`.
 ``expert_parallel`` runs the layer with its experts split over the ranks of a
-process group (one GPU each).
+process group (one GPU each); ``mxfp4_layer`` holds the experts' weights in 4 bits.
+Products of rows grouped by expert, their gradients and the 4-bit calls also stand
+by themselves (``moe_grouped_gemm``, ``moe_grouped_gemm_backward``, ``moe_mxfp4_*``).
 """
 from ._binding import (  # noqa: F401
     MOE_ACT_NONE, MOE_ACT_SILU_AND_MUL, MOE_BF16, MOE_F16, MOE_F32, MOE_GROUP_TOPK_GREEDY, MOE_GROUP_TOPK_NOAUX_TC, MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT,

@@ -202,9 +202,10 @@ __device__ __forceinline__ void store_turned(uint32_t (&y)[32], T* row0, int cou
 // own (1024-byte aligned): `q` holds 64 packed 16-bit columns. A box of 32 whole rows goes out as one
 // TMA store of tensor `m` at (x, y, z), which runs on while the warp reads its next columns; rows that
 // end before (count < 32, the next group follows) are read back and stored with ordinary
-// instructions, four rows of 128 bytes each. Measured at K = 128, where the epilogue sets the pace, f16
-// output of 270 MB: 65 us, with ordinary stores alone 93. Needs rows that are a multiple of 16 bytes, 16-byte aligned. The 16-byte pieces lie in the
-// order of the tensor's 128-byte swizzle, with which neither side meets bank conflicts.
+// instructions, four rows of 128 bytes each. Measured at K = 128, where the epilogue sets the pace,
+// float16 output of 270 MB: 65 us, with ordinary stores alone 93. Needs rows that are a multiple of
+// 16 bytes, 16-byte aligned. The 16-byte pieces lie in the order of the tensor's 128-byte swizzle,
+// with which neither side meets bank conflicts.
 template <class T>
 __device__ __forceinline__ void store_rows(uint32_t buf, const uint32_t (&q)[32], const CUtensorMap* m, int x, int y, int z,
                                            bool whole, T* row0, int count, int cols) {

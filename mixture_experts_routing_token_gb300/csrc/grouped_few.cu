@@ -8,9 +8,9 @@
 // rows of x, 16 to 64 of them, its N; a TMEM lane then holds one output column of every row.
 // One CTA per SM takes units of (expert, rows of x, f columns of y) by turns:
 //   warp 0     TMA producer: per step 128 bytes of each of the unit's rows (one box of f rows of
-//              w, boxes of 16 rows of x), through a ring whose stages are as large as the launch's units need (their
-//              columns, the rows of the largest group), so that there are up to 20 of them and
-//              about 160 KB of weights in flight per SM;
+//              w, boxes of 16 rows of x), through a ring whose stages are as large as the
+//              launch's units need (their columns, the rows of the largest group), so that
+//              there are up to 20 of them and about 160 KB of weights in flight per SM;
 //   warp 1     MMA issuer (M = 128, N = 16 .. 64);
 //   warps 2-5  epilogue: a warp stores 32 neighbouring columns of a row at a time;
 //   warps 6-9  4-bit only: scales, each warp every fourth chunk of four steps, through a buffer
@@ -21,7 +21,8 @@
 // be 176 units for 152 SMs, two rounds of which the second is nearly empty; 80 columns make 288.
 // The box has f rows because TMA instructions are what limits a unit otherwise: with boxes of 16
 // rows a step took 600 cycles whatever its size (33 GB/s an SM at f = 80).
-// A group of more than 64 rows is several heads, whose units read the same weights at about the same time.
+// A group of more than 64 rows is several heads, whose units read the same weights at about the
+// same time.
 #include <algorithm>
 
 #include "grouped.cuh"

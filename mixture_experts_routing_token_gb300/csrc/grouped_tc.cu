@@ -350,6 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
     At at;
     int acc = 0;
     uint32_t aph = 0;
+    bool zeroed = false;      // the buffer holds zeros
     for (int t = cluster_id; t < total; t += nclusters) {
       const Tile ti = tile_at<GRAD>(t, at, G, dw_tiles, P);
       const Job& J = ti.dw ? P.dw : P.rows;
@@ -358,11 +359,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
       const bool mine = lane < nrows;
       T* dst = static_cast<T*>(J.out) + (ti.dw ? (long)ti.e * J.M + m : (long)ti.g.lo + m) * J.C;
       if (ti.blocks == 0) {
-        uint32_t z[32] = {};
-        if (mine)
-          for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 32) grouped::store_cols(dst, c, J.C, J.vec, z);
+        // an expert without rows: zeros, a buffer of them sent as often as tiles ask, or neighbouring
+        // columns by neighbouring lanes
+        const int rows = min(32, nrows);
+        T* row0 = dst - (long)lane * J.C;
+        if (!F32 && J.vec > 0) {
+          if (!zeroed) {
+            if (lane == 0) ptx::tma_store_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sbuf + lane * 128 + p * 16), "r"(0) : "memory");
+            fence_async_shared();
+            __syncwarp();
+            zeroed = true;
+          }
+          if (lane == 0 && rows > 0)
+            for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 64) ptx::tma_store_3d(&tmDw, sbuf, c, m, ti.e);
+        } else if (!F32 || warp < 6) {
+          for (int r = 0; r < rows; ++r)
+            for (int c = ti.n * BN + lane; c < min(J.C, (ti.n + 1) * BN); c += 32) row0[(long)r * J.C + c] = from_float<T>(0.0f);
+        }
         continue;
       }
+      zeroed = false;
       if constexpr (F32) {
         // this warp's 128 of the 256 columns, over the accumulators of the tile
         const int half = (warp - 2) >> 2;
@@ -435,8 +455,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
     }
     if (lane == 0) ptx::tma_store_wait();
     if (P.rows.out != nullptr && !*abort_p)
-      grouped::zero_unowned(static_cast<T*>(P.rows.out), G, P.E, P.S, P.rows.C, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
-                            (long)gridDim.x * EPI_WARPS * 32);
+      grouped::zero_unowned(static_cast<T*>(P.rows.out), G, P.E, P.S, P.rows.C,
+                            ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane, (long)gridDim.x * EPI_WARPS * 32);
   } else if (GRAD) {
     // ------------------------------------------------------------ tail (both CTAs): clears rows past a group's end
     At at;
@@ -615,7 +635,8 @@ void padded(PadParams& p, const void* src, long rows, int cols, int per, Carver&
   m->cols = pad8(cols);
   uint16_t* dst = c.take<uint16_t>((size_t)rows * m->cols);
   m->p = dst;
-  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * (m->cols / 8), cols, m->cols / 8, per};
+  const int pieces = m->cols / 8;
+  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * pieces, cols, pieces, per};
 }
 
 int launch_pads(const PadParams& p, cudaStream_t s) {
@@ -690,7 +711,8 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
         }
       }
 #pragma unroll
-      for (int part = 0; part < 3; ++part) M.dst[part * M.n + r * M.pieces + piece] = make_uint4(q[part][0], q[part][1], q[part][2], q[part][3]);
+      for (int part = 0; part < 3; ++part)
+        M.dst[part * M.n + r * M.pieces + piece] = make_uint4(q[part][0], q[part][1], q[part][2], q[part][3]);
     }
   }
   const int any = __syncthreads_or(bad);

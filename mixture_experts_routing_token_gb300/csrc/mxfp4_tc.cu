@@ -374,8 +374,8 @@ int launch(const Mxfp4Args& a, cudaStream_t s) {
   uint4* x_atoms = c.take<uint4>((size_t)xa * 32);
   uint4* w_atoms = c.take<uint4>((size_t)wa * 32);
   {
-    ScaleParams q{a.x_scales, a.w_scales, a.offsets, a.S, a.E, a.N, NT, steps, a.K / 32, mx::scale_vec(a.K / 32), SILU ? a.N / 2 : a.N,
-                  x_atoms, w_atoms};
+    ScaleParams q{a.x_scales, a.w_scales, a.offsets, a.S, a.E, a.N, NT, steps, a.K / 32, mx::scale_vec(a.K / 32),
+                  SILU ? a.N / 2 : a.N, x_atoms, w_atoms};
       ProfScope ps("mxfp4_scales", s);
     const long warps = (xa / (2 * steps) + wa / (2 * steps)) * ((steps + 1) / 2);
     const int grid = (int)std::max(1L, std::min((warps + 7) / 8, (long)num_sms() * 8));

@@ -26,45 +26,58 @@ struct Groups {
   __device__ __forceinline__ Span span(int e) const { return Span{off[e], off[e + 1]}; }
 };
 
-// Whole warp: fills G; tiles(rows) is the tile count of a group. Entries are taken 32 at a time,
-// the loads of four such turns under way together (one latency for up to 127 experts).
-// Returns (in every lane) the rows of the largest group.
+// Whole warp: fills G; tiles(rows) is the tile count of a group. A lane takes four neighbouring
+// entries, so up to 127 experts are one load latency and two scans, which every kernel here waits
+// for before its first tile. Returns (in every lane) the rows of the largest group.
 template <class Tiles>
 __device__ __forceinline__ int group_list(const int32_t* offsets, int E, int S, Tiles tiles, Groups& G) {
   const int lane = threadIdx.x & 31;
   int top = 0, last = 0, wrong = 0, sum = 0, most = 0;    // over all entries before this turn
   for (int i0 = 0; i0 <= E; i0 += 128) {
+    const int i = i0 + 4 * lane;
     int v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i0 + 32 * u + lane <= E ? __ldg(offsets + i0 + 32 * u + lane) : 0;
+    for (int u = 0; u < 4; ++u) v[u] = i + u <= E ? __ldg(offsets + i + u) : 0;
+    int raw = __shfl_up_sync(0xffffffffu, v[3], 1);
+    if (lane == 0) raw = last;
+    last = __shfl_sync(0xffffffffu, v[3], 31);
+    int up = 0;                                       // largest of the lane's entries, then of all up to it
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = i0 + 32 * u + lane;
-      if (i - lane > E) break;
-      int prev = __shfl_up_sync(0xffffffffu, v[u], 1);
-      if (lane == 0) prev = last;
-      last = __shfl_sync(0xffffffffu, v[u], 31);
-      wrong |= i <= E && (v[u] < 0 || v[u] > S || (i > 0 && v[u] < prev));
-      int off = max(i <= E ? min(max(v[u], 0), S) : 0, top);
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) off = max(off, __shfl_up_sync(0xffffffffu, off, d));
-      int before = __shfl_up_sync(0xffffffffu, off, 1);   // the entry before: group i - 1 ends at off
-      if (lane == 0) before = top;
-      top = __shfl_sync(0xffffffffu, off, 31);
-      const int rows = i > 0 && i <= E ? off - before : 0;
-      most = max(most, rows);
-      int incl = i > 0 && i <= E ? tiles(rows) : 0;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      if (i <= E) {
-        G.off[i] = off;
-        G.start[i] = sum + incl;       // the tiles of groups 0 .. i - 1
-      }
-      sum += __shfl_sync(0xffffffffu, incl, 31);
+      if (i + u > E) continue;
+      wrong |= v[u] < 0 || v[u] > S || (i + u > 0 && v[u] < raw);
+      raw = v[u];
+      up = max(up, min(max(v[u], 0), S));
     }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) up = max(up, __shfl_up_sync(0xffffffffu, up, d));
+    int before = __shfl_up_sync(0xffffffffu, up, 1);  // offset of the entry before the lane's
+    before = max(top, lane == 0 ? 0 : before);
+    top = max(top, __shfl_sync(0xffffffffu, up, 31));
+    int off[4], count[4], total = 0;                  // count[u]: tiles of the lane's groups up to entry u
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      off[u] = max(before, i + u <= E ? min(max(v[u], 0), S) : 0);
+      if (i + u > 0 && i + u <= E) {                  // the group that ends here; one without rows may have tiles
+        most = max(most, off[u] - before);
+        total += tiles(off[u] - before);
+      }
+      count[u] = total;
+      before = off[u];
+    }
+    int incl = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u <= E) {
+        G.off[i + u] = off[u];
+        G.start[i + u] = sum + incl - total + count[u];      // the tiles of groups 0 .. i + u - 1
+      }
+    sum += __shfl_sync(0xffffffffu, incl, 31);
   }
   wrong = __any_sync(0xffffffffu, wrong);
   if (lane == 0) G.bad = wrong;

@@ -418,10 +418,23 @@ def _take(t, name, dtype, index):
     return t.data_ptr()
 
 
-def _give(t, name, shape, dtype, index):
+def _new(shape, dtype, index, stream):
+    """Memory for a call on ``stream``, from that stream's pool: a block that the current stream has given back may
+    still be read by what is queued there. The current stream is noted with it, where outputs are used next."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
+    t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
+def _give(t, name, shape, dtype, index, stream):
     """(tensor, address) of an output: the caller's after its checks, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
+        t = _new(shape, dtype, index, stream)
         return t, t.data_ptr()
     p = _take(t, name, dtype, index)
     if t.shape != shape:
@@ -453,13 +466,11 @@ def _space(workspace, index):
 
 
 def _again(name, rc, size, workspace, index, stream, call):
-    """A call came back with an error: without a workspace where one is needed, one is made. It goes back to
-    the current stream's pool when this returns, so a call on another stream is noted with it."""
+    """A call came back with an error: without a workspace where one is needed, one is made, which goes back to
+    the pool of the call's stream when this returns."""
     if rc == MOE_ERR_WORKSPACE and workspace is None:
-        buf = torch.empty(size(), dtype=_U8, device=f"cuda:{index}")
+        buf = _new(size(), _U8, index, stream)
         rc = call(buf.data_ptr(), buf.numel())
-        if stream is not None:
-            buf.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
     _check(name, rc)
 
 
@@ -481,7 +492,7 @@ def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, strea
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1]")
     S, K = xs
     E, N, _ = wsh
-    out, yp = _give(out, "out", (S, N), dtype, d)
+    out, yp = _give(out, "out", (S, N), dtype, d, stream)
     ws, nb = _space(workspace, d)
     st, sm = _status_ptr(status, d), _raw(stream, d)
     f = lib().moe_grouped_gemm
@@ -512,8 +523,8 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
         raise ValueError("shapes must be x [S, K], w [E, N, K], offsets [E + 1], d_y [S, N]")
     S, K = xs
     E, N, _ = wsh
-    d_x, dxp = _give(d_x, "d_x", xs, dtype, d) if want_d_x else (None, None)
-    d_w, dwp = _give(d_w, "d_w", wsh, dtype, d) if want_d_w else (None, None)
+    d_x, dxp = _give(d_x, "d_x", xs, dtype, d, stream) if want_d_x else (None, None)
+    d_w, dwp = _give(d_w, "d_w", wsh, dtype, d, stream) if want_d_w else (None, None)
     ws, nb = _space(workspace, d)
     st, sm = _status_ptr(status, d), _raw(stream, d)
     f = lib().moe_grouped_gemm_backward
@@ -549,8 +560,8 @@ def moe_mxfp4_quantize(x, rows=None, codes=None, scales=None, workspace=None, st
         if len(xs) != 2 or len(lead) != 1:
             raise ValueError("rows must be [R] and x [T, K]")
         T, R = xs[0], lead[0]
-    codes, cp = _give(codes, "codes", (*lead, K // 2), _U8, d)
-    scales, sp = _give(scales, "scales", (*lead, K // 32), _U8, d)
+    codes, cp = _give(codes, "codes", (*lead, K // 2), _U8, d, stream)
+    scales, sp = _give(scales, "scales", (*lead, K // 32), _U8, d, stream)
     ws, nb = _space(workspace, d)
     st, sm = _status_ptr(status, d), _raw(stream, d)
     f = lib().moe_mxfp4_quantize
@@ -574,7 +585,7 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     lead, K = cs[:-1], 2 * cs[-1]
     if scales.shape != (*lead, K // 32):
         raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32]")
-    out, op = _give(out, "out", (*lead, K), dtype, d)
+    out, op = _give(out, "out", (*lead, K), dtype, d, stream)
     rc = lib().moe_mxfp4_dequantize(cp, sp, lead.numel(), K, dt, op, _raw(stream, d))
     if rc:
         _check("moe_mxfp4_dequantize", rc)
@@ -618,7 +629,7 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
         if N % 2:
             raise ValueError("silu_and_mul needs an even N")
         cols, act = N // 2, MOE_ACT_SILU_AND_MUL
-    out, yp = _give(out, "out", (S, cols), out_dtype, d)
+    out, yp = _give(out, "out", (S, cols), out_dtype, d, stream)
     ws, nb = _space(workspace, d)
     st, sm = _status_ptr(status, d), _raw(stream, d)
     f = lib().moe_mxfp4_grouped_gemm

@@ -442,6 +442,36 @@ def test_workspace_on_a_stream_of_the_callers(moe):
         assert torch.equal(got, want) and junk
 
 
+def test_memory_of_a_call_on_another_stream(moe):
+    """Outputs and workspaces made for a call on a stream of the caller's: what the current stream has given
+    back, but not yet read, must not be among them; nor may an output that the current stream still reads be
+    given out again on the other stream."""
+    off = torch.tensor([0, 200, 600], dtype=torch.int32, device=DEV)
+    x, _ = draw((600, 129), "bf16", 1)
+    w, _ = draw((2, 515, 129), "bf16", 2)
+    want = moe.moe_grouped_gemm(x, w, off)
+    size = moe.moe_grouped_gemm_workspace_size(moe.MOE_BF16, 600, 129, 515, 2)
+    assert size > 0
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        torch.cuda.synchronize()
+        mine = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in (size, 600 * 515 * 2) for _ in range(2)]
+        s.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(2000000)
+        copies = [m.clone() for m in mine]
+        del mine
+        got = moe.moe_grouped_gemm(x, w, off, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all((c == 7).all() for c in copies)
+        torch.cuda._sleep(2000000)
+        kept = got.clone()
+        del got
+        with torch.cuda.stream(s):
+            junk = [torch.full((600, 515), 3, dtype=want.dtype, device=DEV) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want) and junk
+
+
 # ---- 4-bit microscaled values ----------------------------------------------------------
 
 

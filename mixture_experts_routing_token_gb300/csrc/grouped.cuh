@@ -252,6 +252,63 @@ __device__ __forceinline__ void store_rows(uint32_t buf, const uint32_t (&q)[32]
   __syncwarp();
 }
 
+// The same for rows that are not a multiple of 16 bytes: each row is read back from the buffer by the
+// whole warp and leaves in 4-byte words (a row that starts between two words gives its first value
+// alone and shifts the others by one), 128 bytes an instruction, eight rows under way together. 16000
+// float16 rows, K = 136, [*, 4093]: 109 us, and 139 where the lanes
+// exchanged the block by shuffles and stored single values. `count` > 0 rows, columns from c0 on.
+template <class T>
+__device__ __forceinline__ void store_ragged(uint32_t buf, const uint32_t (&q)[32], T* row0, int count, int c0, int cols) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();                                   // the last columns have been read
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                 "r"(q[4 * p]), "r"(q[4 * p + 1]), "r"(q[4 * p + 2]), "r"(q[4 * p + 3])
+                 : "memory");
+  __syncwarp();
+  const int left = min(64, cols - c0);            // values of a row
+  uint16_t* row = reinterpret_cast<uint16_t*>(row0) + c0;
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    if (r0 >= count) break;
+    uint32_t w[8], next[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w[i])
+                   : "r"(buf + (r0 + i) * 128 + ((((lane >> 2) ^ i) << 4) | ((lane & 3) << 2)))
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) next[i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t* p = row + (long)(r0 + i) * cols;
+      const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+      const uint32_t v = __byte_perm(w[i], next[i], odd ? 0x5432 : 0x3210);
+      const int e = 2 * lane + odd;
+      const bool in = r0 + i < count;
+      if (in && e + 1 < left) *reinterpret_cast<uint32_t*>(p + e) = v;
+      // the values without a pair: a row's first, lane 0's; its last, of the lane that ends there
+      const bool head = odd && lane == 0;
+      if (in && (head || e + 1 == left)) p[head ? 0 : e] = (uint16_t)(head ? w[i] : v);
+      if (in && head && e + 1 == left) p[e] = (uint16_t)v;
+    }
+  }
+}
+
+// Whole warp: n >= 0 neighbouring values to zero, 16 bytes a lane between the first and the last boundary.
+template <class T>
+__device__ __forceinline__ void zero_values(T* p, int n) {
+  const int lane = threadIdx.x & 31;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), e = a + (uintptr_t)n * sizeof(T);
+  const uintptr_t first = min((a + 15) & ~(uintptr_t)15, e), last = max(first, e & ~(uintptr_t)15);
+  for (uintptr_t u = first + lane * 16; u < last; u += 512) *reinterpret_cast<uint4*>(u) = make_uint4(0, 0, 0, 0);
+  const uintptr_t head = a + lane * sizeof(T), tail = last + lane * sizeof(T);      // under 16 bytes each
+  if (head < first) *reinterpret_cast<T*>(head) = from_float<T>(0.0f);
+  if (tail < e) *reinterpret_cast<T*>(tail) = from_float<T>(0.0f);
+}
+
 // W float32 sums (as bits) as words of T.
 template <class T, int W>
 __device__ __forceinline__ void pack_words(const uint32_t (&y)[W], uint32_t* q) {

@@ -359,8 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
       const bool mine = lane < nrows;
       T* dst = static_cast<T*>(J.out) + (ti.dw ? (long)ti.e * J.M + m : (long)ti.g.lo + m) * J.C;
       if (ti.blocks == 0) {
-        // an expert without rows: zeros, a buffer of them sent as often as tiles ask, or neighbouring
-        // columns by neighbouring lanes
+        // an expert without rows: zeros, a buffer of them sent as often as tiles ask, or rows by the warp
         const int rows = min(32, nrows);
         T* row0 = dst - (long)lane * J.C;
         if (!F32 && J.vec > 0) {
@@ -377,8 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
           if (lane == 0 && rows > 0)
             for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 64) ptx::tma_store_3d(&tmDw, sbuf, c, m, ti.e);
         } else if (!F32 || warp < 6) {
-          for (int r = 0; r < rows; ++r)
-            for (int c = ti.n * BN + lane; c < min(J.C, (ti.n + 1) * BN); c += 32) row0[(long)r * J.C + c] = from_float<T>(0.0f);
+          const int c0 = ti.n * BN, n = min(BN, J.C - c0);
+          for (int r = 0; r < rows; ++r) grouped::zero_values(row0 + (long)r * J.C + c0, n);
         }
         continue;
       }
@@ -433,19 +432,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
         ptx::tmem_ld32(taddr + c + 32, y[1]);
         ptx::tmem_ld_wait();
         const int c0 = ti.n * BN + c;
+        if (nrows <= 0 || c0 >= J.C) continue;
+        uint32_t words[32];
+        grouped::pack_words<T, 32>(y[0], words);
+        grouped::pack_words<T, 32>(y[1], words + 16);
+        T* row0 = dst - (long)lane * J.C;
         if (J.vec > 0) {
-          uint32_t words[32];
-          grouped::pack_words<T, 32>(y[0], words);
-          grouped::pack_words<T, 32>(y[1], words + 16);
           // d_w: the tensor's own edge ends the rows; y, d_x: the group does, so a box needs all of its 32
-          if (nrows > 0 && c0 < J.C)
-            grouped::store_rows(sbuf, words, ti.dw ? &tmDw : &tmRows, c0, ti.dw ? m - lane : ti.g.lo + m - lane, ti.dw ? ti.e : 0,
-                                ti.dw || nrows >= 32, dst - (long)lane * J.C, nrows, J.C);
+          grouped::store_rows(sbuf, words, ti.dw ? &tmDw : &tmRows, c0, ti.dw ? m - lane : ti.g.lo + m - lane, ti.dw ? ti.e : 0,
+                              ti.dw || nrows >= 32, row0, nrows, J.C);
         } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (nrows > 0 && c0 + h * 32 < J.C)
-              grouped::store_turned(y[h], dst - (long)lane * J.C, nrows, c0 + h * 32, J.C);
+          grouped::store_ragged(sbuf, words, row0, nrows, c0, J.C);
         }
       }
       ptx::tc_fence_before();

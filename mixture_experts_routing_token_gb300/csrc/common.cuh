@@ -237,12 +237,28 @@ int launch_grouped_simt_dx(const GroupedArgs& a, const int* flags, cudaStream_t 
 int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t s);
 // The tensor cores; the workspace holds padded copies of 16-bit operands whose rows are not a multiple
 // of 16 bytes, and float32 operands in three parts.
-// float32 takes the tensor cores where there is enough to multiply for what making the parts costs
-// (ten bytes moved per value of x and w). Measured, us, tensor cores / CUDA cores: 64 rows per expert,
-// 64 experts of [1200, 800] 256 / 266, at 32 rows 248 / 200; 8 experts of [512, 512] 31 / 48 at 2000 rows,
-// [512, 256] 22 / 23 at 512; gradients, 16 rows per expert, 32 of [1024, 512] 107 / 116, 8 of [256, 256] 27 / 21.
+// Whether float32 takes the tensor cores: both sides' time is estimated, in us, from what they pad, move
+// and do one after the other, with constants fitted to 200 random calls of up to 4e9 operations. The side
+// taken was the faster one or within 28% of it, on average 1% (with one limit on rows per expert and one
+// on operations up to 2.8 times slower, on average 7%). CUDA cores: padded tiles of 64 columns and 16 or
+// 64 rows, weights once. Tensor cores: parts of all operands (16 bytes a value), tiles of 256 x 256 in
+// rounds of 76 SM pairs, 1.35 us for 64 steps of the reduction in the product and 1.75 in the gradients.
+// Full tiles and sums of 256 terms or more take the tensor cores up to 15% earlier: their sums are the
+// more exact ones (2-norm 1.3e-7 against 4e-7 at 517 terms), and it cost 0.1% on average.
 inline bool grouped_f32_uses_tensor_cores(int S, int K, int N, int E, bool grad) {
-  return 2.0 * S * K * N >= 1.5e8 && S >= (grad ? 16L : 64L) * E;
+  const auto up = [](int v, int m) { return (double)((v + m - 1) / m); };
+  const double s = S, k = K, n = N, e = E, half = 0.5 * (E < S ? E : S);     // groups that end inside a tile
+  const double rows = s + half * (S <= 16L * E ? 16 : 64), tiles = s / 256 + half, each = s / e;
+  const auto most = [](double a, double b) { return a > b ? a : b; };
+  const double exact = K >= 256 && S >= 256L * E ? 1.15 : 1.0;
+  if (!grad)
+    return 15 + 2.9e-6 * (s * k + e * n * k) + 1.35 * most(1, tiles * up(N, 256) / 76) * up(K, 64) + 1.1e-6 * s * n <
+           exact * (14 + 42e-9 * rows * up(N, 64) * 64 * k + 0.7e-6 * e * n * k);
+  const double dx = tiles * up(K, 256), dw = e * up(N, 256) * up(K, 256);
+  const double steps = most((dx * up(N, 64) + dw * (each / 64 + 0.5)) / 76, most(up(N, 64), each / 64 + 1));
+  return 19 + 3.1e-6 * (s * k + e * n * k + s * n) + 1.75 * steps + 2.8 * most(1, (dx + dw) / 76) <
+         15 + 14e-9 * rows * up(K, 64) * 64 * n + 1.9e-6 * e * n * k + 74e-9 * (s + 8 * e) * up(N, 64) * up(K, 64) * 4096 +
+             0.1 * each;
 }
 size_t grouped_tc_workspace(int dtype, int S, int K, int N, int E, bool fwd);
 int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);

@@ -75,6 +75,9 @@ SHAPES_F32 = [
     ([700], 1, 129, 1100),
     ([128, 64, 0, 192, 320], 0, 512, 640),
     ([5, 900, 0, 33], 2, 64, 1700),
+    ([900, 0, 700, 1], 3, 517, 1030),
+    ([2000, 30], 0, 129, 1100),
+    ([1100, 600, 0, 300], 2, 1030, 264),
 ]
 
 
@@ -204,6 +207,28 @@ def test_f32_infinities_follow_float32(moe):
         fin = torch.isfinite(want)
         assert torch.equal(torch.sign(y[p][~torch.isnan(want)]), torch.sign(want[~torch.isnan(want)]))
         assert (y[p][fin] - want[fin]).abs().max() <= 1e-5 * max(1e-30, float(want[fin].abs().max())) if fin.any() else True
+
+
+def test_f32_values_without_parts_in_a_large_product(moe):
+    """Infinities, NaN and 3e38 among the rows of a product that is large enough for the tensor cores."""
+    off = offsets_of([1100, 0, 900])
+    o = torch.from_numpy(off).to(DEV)
+    x, x64 = draw((2003, 517), "f32", 1)
+    w, w64 = draw((3, 1030, 517), "f32", 2)
+    plain = moe.moe_grouped_gemm(x, w, o)
+    for value in (float("inf"), float("nan"), 3.0e38):
+        y = x.clone()
+        y[1500, 516] = value
+        got = moe.moe_grouped_gemm(y, w, o)
+        want = (y[1500].double() * w[2].double()).sum(1).float()
+        assert torch.equal(torch.isnan(got[1500]), torch.isnan(want)) and torch.equal(torch.isinf(got[1500]), torch.isinf(want))
+        ok = torch.isfinite(want)
+        if ok.any():
+            assert ((got[1500] - want)[ok].abs() <= 1e-5 * want[ok].abs().max()).all()
+        rest = torch.arange(2003, device=DEV) != 1500
+        # both float32: 517 rounded additions each, in the 2-norm far below 517 2^-24
+        assert (got[rest] - plain[rest]).double().norm() <= 2 * 517 * 2.0 ** -24 * plain[rest].double().norm()
+    assert not plain[2000:].any()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

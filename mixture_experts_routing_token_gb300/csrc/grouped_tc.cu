@@ -547,7 +547,7 @@ struct Mat {
 int pad8(int c) { return (c + 7) / 8 * 8; }
 
 // Rows whose bytes are not a multiple of 16 cannot be read by TMA: copies with rows padded to one,
-// zeros in between (an odd width is a small problem's; the copy is one pass over the operand at
+// zeros in between (the copy is one pass over the operand at
 // memory speed, against falling off the tensor cores).
 struct Pad {
   const uint16_t* src;
@@ -555,6 +555,7 @@ struct Pad {
   long n;               // pieces of 8 columns
   int cols, pieces;     // columns; pieces of a row
   int per;              // rows of an expert's matrix (0: not by expert)
+  uintptr_t end;        // of the matrix
 };
 
 // The experts that have rows, in shared memory: nothing reads the weights of the others, and a few
@@ -595,6 +596,34 @@ __device__ __forceinline__ long piece_row(long i, int pieces, int per, const Liv
   return r;
 }
 
+// Eight 16-bit values from p on, of which the first `count` are wanted (zeros else), as words: two aligned
+// 16-byte loads, shifted by whole words and then by half of one, where both lie before `end`. 8192 rows,
+// 8 experts of [2047, 1001]: 63 us, with eight single loads a piece 66.
+__device__ __forceinline__ uint4 load_any(const uint16_t* p, int count, uintptr_t end) {
+  uint32_t v[4];
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), base = a & ~(uintptr_t)15;
+  if (base + 32 <= end) {
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(base)), hi = __ldg(reinterpret_cast<const uint4*>(base) + 1);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int by = (int)(a - base);
+    uint32_t two[6], one[5];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) two[j] = by & 8 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) one[j] = by & 4 ? two[j + 1] : two[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = by & 2 ? __byte_perm(one[j], one[j + 1], 0x5432) : one[j];
+      if (count < 2 * j + 2) v[j] = count > 2 * j ? v[j] & 0xffffu : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = (2 * j < count ? (uint32_t)__ldg(p + 2 * j) : 0u) | (2 * j + 1 < count ? (uint32_t)__ldg(p + 2 * j + 1) << 16 : 0u);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 struct PadParams {
   const int32_t* offsets;
   int E;
@@ -616,11 +645,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadParams P) {
       int piece;
       const long r = piece_row(i, M.pieces, M.per, live, piece);
       const int c = piece * 8;
-      const uint16_t* p = M.src + r * M.cols + c;
-      uint32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = c + j < M.cols ? __ldg(p + j) : 0u;
-      M.dst[r * M.pieces + piece] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      M.dst[r * M.pieces + piece] = load_any(M.src + r * M.cols + c, M.cols - c, M.end);
     }
   }
 }
@@ -633,7 +658,8 @@ void padded(PadParams& p, const void* src, long rows, int cols, int per, Carver&
   uint16_t* dst = c.take<uint16_t>((size_t)rows * m->cols);
   m->p = dst;
   const int pieces = m->cols / 8;
-  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * pieces, cols, pieces, per};
+  p.m[p.count++] = Pad{static_cast<const uint16_t*>(src), reinterpret_cast<uint4*>(dst), rows * pieces, cols, pieces, per,
+                     reinterpret_cast<uintptr_t>(src) + (uintptr_t)rows * cols * 2};
 }
 
 int launch_pads(const PadParams& p, cudaStream_t s) {

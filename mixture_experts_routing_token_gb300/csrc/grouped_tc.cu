@@ -326,9 +326,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
           const uint64_t ad = a_mn ? sdesc_mn128(a0, MN_BLOCK) : ptx::sdesc_k128(a0);
           const uint64_t bd = GRAD ? sdesc_mn128(b0, MN_BLOCK) : ptx::sdesc_k128(b0);
           const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (GRAD ? 2048u : 32u) >> 4;
+          // d_w: no steps past the group's last row, of which the tail warp clears less then: 64 rows, 16
+          // experts of [2048, 2048], 31 us instead of 37 (float32, six products a block: 4% slower, not done)
+          const int left = GRAD && !F32 && ti.dw ? ti.g.rows() - sp.block * BK : BK;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, !sp.first || kk != 0);
+            if (kk * 16 < left) mma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, !sp.first || kk != 0);
           commit_pair(ptx::smem_u32(&empty_bar[stage]), 0x3);
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
           if (sp.last) {
@@ -359,9 +362,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
       const bool mine = lane < nrows;
       T* dst = static_cast<T*>(J.out) + (ti.dw ? (long)ti.e * J.M + m : (long)ti.g.lo + m) * J.C;
       if (ti.blocks == 0) {
-        // an expert without rows: zeros, a buffer of them sent as often as tiles ask, or rows by the warp
-        const int rows = min(32, nrows);
-        T* row0 = dst - (long)lane * J.C;
+        // d_w of an expert without rows: a buffer of zeros sent as often as the tile asks (18 rows, 113 experts of
+        // [512, 2048], 41 us; by the stretch 46), or this warp's share of the zeros as one stretch of memory
+        // (4 rows, 32 experts of [714, 1030], 24 us; by the tile's rows 45; float32 by the
+        // tile's rows: the stretch cost its other tiles 8%)
         if (!F32 && J.vec > 0) {
           if (!zeroed) {
             if (lane == 0) ptx::tma_store_wait_read();
@@ -373,11 +377,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
             __syncwarp();
             zeroed = true;
           }
-          if (lane == 0 && rows > 0)
+          if (lane == 0 && nrows > 0)
             for (int c = ti.n * BN; c < min(J.C, (ti.n + 1) * BN); c += 64) ptx::tma_store_3d(&tmDw, sbuf, c, m, ti.e);
-        } else if (!F32 || warp < 6) {
-          const int c0 = ti.n * BN, n = min(BN, J.C - c0);
-          for (int r = 0; r < rows; ++r) grouped::zero_values(row0 + (long)r * J.C + c0, n);
+        } else if constexpr (F32) {
+          T* row0 = dst - (long)lane * J.C;
+          if (warp < 6)
+            for (int r = 0; r < min(32, nrows); ++r)
+              for (int c = ti.n * BN + lane; c < min(J.C, (ti.n + 1) * BN); c += 32) row0[(long)r * J.C + c] = from_float<T>(0.0f);
+        } else {
+          constexpr int W = 2 * EPI_WARPS;
+          const long all = (long)J.M * J.C, shares = (long)J.MT * J.NT * W;
+          const long share = ((all + shares - 1) / shares + 7) / 8 * 8;
+          const long from = ((long)(ti.m * J.NT + ti.n) * W + (int)rank * EPI_WARPS + warp - 2) * share;
+          if (from < all) grouped::zero_values(static_cast<T*>(J.out) + ti.e * all + from, (int)min(share, all - from));
         }
         continue;
       }
@@ -471,7 +483,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
         ok = ptx::mbar_wait(ptx::smem_u32(&tail_bar[s]), (tph >> s) & 1u, abort_p, P.wait_ns);
         if (!ok) break;
         tph ^= 1u << s;
-        const int lines = (BK - keep) * 4;               // 128-byte lines to clear, in four boxes of 64
+        // 128-byte lines to clear, in four boxes of 64: the MMAs' rows past the group's
+        const int lines = (F32 ? BK - keep : (16 - keep % 16) % 16) * 4;
         for (int i = lane; i < lines * 8; i += 32) {
           const int line = i >> 3, box = line & 3;
           const uint32_t a = sA(s) + (uint32_t)(box * (int)MN_BLOCK + (keep + (line >> 2)) * 128 + (i & 7) * 16);

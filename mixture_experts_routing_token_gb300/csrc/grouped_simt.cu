@@ -1,5 +1,6 @@
-// Products grouped by expert in float32, on the CUDA cores: small sizes, and operands that hold
-// infinities or NaN (then launched behind the tensor-core kernel, with the flags that it gives way to).
+// Products grouped by expert in float32, on the CUDA cores: small sizes, few rows per expert, narrow
+// outputs, and operands that hold infinities or NaN (then launched behind the tensor-core kernel, with
+// the flags that it gives way to).
 //
 //   ROWS   y[p, n]    = sum_k x[p, k] w[e, n, k]     (rows p of expert e)
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
@@ -190,14 +191,9 @@ int launch_tiles(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
   const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt
                                    : ((long)(p.S + TM - 1) / TM + p.E) * nt * p.parts;
-  // Six CTAs of 64 x 64 fit an SM. When all tiles are resident at once some SMs get six and others
-  // four, and the six set the time; with room for four (the unused shared memory says so) the rest go
-  // where one ends: 2000 rows, 8 experts of [1030, 517], 680 tiles: 69 us instead of 88. With more
-  // tiles than that six are the faster: 8000 rows, [2048, 1024]: 740 us instead of 798.
   const long full = resident(TM);
-  const size_t unused = TM == 64 && tiles <= full ? 22000 : 0;
   ProfScope ps(name, s);
-  grouped_simt_kernel<MODE, TM><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, unused, s>>>(p);
+  grouped_simt_kernel<MODE, TM><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, 0, s>>>(p);
   return check_launch(name);
 }
 

@@ -292,8 +292,7 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
  *   outside [0, S] or below its predecessor sets MOE_STATUS_BAD_INDEX (groups
  *   are cut to [0, S]; the rows concerned are then undefined).
  *   ws / ws_bytes: at least moe_grouped_gemm_workspace_size(...) bytes (0 for
- *   16-bit K % 8 == 0 and for small float32 problems: then ws may be null; the
- *   size for float32 depends on the current device's SM count).
+ *   16-bit K % 8 == 0 and for small float32 problems: then ws may be null).
  * S, K, N may have any size >= 0 (K = 0 gives zeros). 16-bit types run on the
  * tcgen05 tensor cores. float32 keeps float32's accuracy: on the CUDA cores, or
  * for large products on the tensor cores in three bf16 parts per value (2^-26

@@ -172,17 +172,18 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(const float* __restri
 // Rows per tile: 16 where experts have few, so that CTAs mostly stream weights (128 rows, 32 experts of
 // [2048, 1024]: 128 us instead of 234; 19 rows per expert 176 / 187, 32 rows 244 / 200).
 int tile_rows(int S, int E) { return S <= 16L * E ? 16 : 64; }
-long resident(int TM) { return (long)num_sms() * (TM == 64 ? 6 : 11); }
+long resident(int TM, int sms) { return (long)sms * (TM == 64 ? 6 : 11); }
 
 // Pieces of the reduction, of 128 steps at least: as many as make four times the CTAs that fit the GPU
 // (a tile alone takes a microsecond for 16 steps, however idle the rest, and tiles that are all resident
 // leave some schedulers two warps and others none). 1685 rows, 58 experts of [344, 2944]: 206 us, with
 // one time the CTAs 373, with two 239; 2000 rows, 32 experts of [512, 512]: 52 us, with one 70, with pieces
 // of 256 steps 56.
+constexpr int kSms = 152;       // a GB300's, so that workspace sizes and sums do not depend on the device asked
 int reduction_parts(int S, int E, long cols, int R) {
   const int TM = tile_rows(S, E);
   const long tiles = ((long)(S + TM - 1) / TM + std::min(S, E)) * ((cols + TN - 1) / TN);
-  const long parts = std::min(std::min(4 * resident(TM) / tiles, (long)R / 128), 16L);
+  const long parts = std::min(std::min(4 * resident(TM, kSms) / tiles, (long)R / 128), 16L);
   return parts < 2 || S * cols * parts > (1L << 24) ? 1 : (int)parts;
 }
 
@@ -191,7 +192,7 @@ int launch_tiles(const SimtParams& p, cudaStream_t s, const char* name) {
   const long cols = MODE == ROWS ? p.N : p.K, nt = (cols + TN - 1) / TN;
   const long tiles = MODE == GRADW ? (long)p.E * ((p.N + TM - 1) / TM) * nt
                                    : ((long)(p.S + TM - 1) / TM + p.E) * nt * p.parts;
-  const long full = resident(TM);
+  const long full = resident(TM, num_sms());
   ProfScope ps(name, s);
   grouped_simt_kernel<MODE, TM><<<(unsigned)std::min(tiles, p.flags ? full : full * 16), TT, 0, s>>>(p);
   return check_launch(name);

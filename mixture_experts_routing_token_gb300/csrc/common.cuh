@@ -246,7 +246,7 @@ int launch_grouped_simt_dw(const GroupedArgs& a, const int* flags, cudaStream_t 
 // Full tiles and sums of 256 terms or more take the tensor cores up to 15% earlier: their sums are the
 // more exact ones (2-norm 1.3e-7 against 4e-7 at 517 terms), and it cost 0.1% on average.
 inline bool grouped_f32_uses_tensor_cores(int S, int K, int N, int E, bool grad) {
-  const auto up = [](int v, int m) { return (double)((v + m - 1) / m); };
+  const auto up = [](int v, int m) { return (double)((v - 1) / m + 1); };
   const double s = S, k = K, n = N, e = E, half = 0.5 * (E < S ? E : S);     // groups that end inside a tile
   const double rows = s + half * (S <= 16L * E ? 16 : 64), tiles = s / 256 + half, each = s / e;
   const auto most = [](double a, double b) { return a > b ? a : b; };

@@ -182,7 +182,7 @@ long resident(int TM, int sms) { return (long)sms * (TM == 64 ? 6 : 11); }
 constexpr int kSms = 152;       // a GB300's, so that workspace sizes and sums do not depend on the device asked
 int reduction_parts(int S, int E, long cols, int R) {
   const int TM = tile_rows(S, E);
-  const long tiles = ((long)(S + TM - 1) / TM + std::min(S, E)) * ((cols + TN - 1) / TN);
+  const long tiles = (((long)S + TM - 1) / TM + std::min(S, E)) * ((cols + TN - 1) / TN);
   const long parts = std::min(std::min(4 * resident(TM, kSms) / tiles, (long)R / 128), 16L);
   return parts < 2 || S * cols * parts > (1L << 24) ? 1 : (int)parts;
 }
@@ -222,7 +222,7 @@ SimtParams params(const GroupedArgs& a, const void* left, const void* right, voi
 }  // namespace
 
 size_t grouped_simt_workspace(int S, int K, int N, int E, bool fwd) {
-  if (S < 1) return 0;
+  if (S < 1 || K < 1 || N < 1) return 0;     // nothing is launched
   const long cols = fwd ? N : K;
   const int parts = reduction_parts(S, E, cols, fwd ? K : N);
   return parts == 1 ? 0 : align_up((size_t)S * cols * parts * sizeof(float), 256);

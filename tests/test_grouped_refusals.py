@@ -47,6 +47,26 @@ def test_workspace_sizes(moe):
         assert f(moe.MOE_BF16, -1, 64, 64, 4) == 0
 
 
+@pytest.mark.parametrize("empty", ["S", "K", "N", "SK", "KN", "SN", "SKN"])
+def test_empty_calls_need_no_workspace(moe, empty):
+    S, K, N = (0 if c in empty else n for c, n in zip("SKN", (50, 640, 96)))
+    assert moe.moe_grouped_gemm_workspace_size(moe.MOE_F32, S, K, N, 3) == 0
+    assert moe.moe_grouped_gemm_backward_workspace_size(moe.MOE_F32, S, K, N, 3) == 0
+    for dtype in (moe.MOE_BF16, moe.MOE_F16):       # rows of 640 or 96 values need no padded copies
+        assert moe.moe_grouped_gemm_workspace_size(dtype, S, K, N, 3) == 0
+        assert moe.moe_grouped_gemm_backward_workspace_size(dtype, S, K, N, 3) == 0
+    moe.moe_mxfp4_grouped_gemm_workspace_size(S, K, N, 3)
+    moe.moe_mxfp4_quantize_workspace_size(S, K, 1, S)
+
+
+def test_largest_sizes_are_answered(moe):
+    big = 2 ** 31 - 1
+    for dtype in (moe.MOE_F32, moe.MOE_BF16):
+        for S, K, N in ((big, 64, 64), (64, big, 64), (64, 64, big)):
+            moe.moe_grouped_gemm_workspace_size(dtype, S, K, N, 3)
+            moe.moe_grouped_gemm_backward_workspace_size(dtype, S, K, N, 3)
+
+
 def test_quantize_sizes_and_types(moe):
     f = moe.lib().moe_mxfp4_quantize
     one = ctypes.c_void_p(16)

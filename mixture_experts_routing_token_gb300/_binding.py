@@ -133,9 +133,29 @@ def _dtype_code(t):
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
-def _out(t, shape, dtype, device, name):
+_device = functools.lru_cache(maxsize=None)(lambda index: torch.device("cuda", index))
+
+
+def _new(shape, dtype, index, stream):
+    """Memory for a call on ``stream``, from that stream's pool: a block that the current stream has given back may
+    still be read by what is queued there, and one of the current stream's that is dropped on return may be given out
+    again while the call still runs. The current stream is noted with it, where outputs are used next."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=_device(index))
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if _raw_stream is not None and handle == _raw_stream(index):
+        return torch.empty(shape, dtype=dtype, device=_device(index))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=index)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=_device(index))
+    t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
+def _out(t, shape, dtype, device, name, stream):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device.index, stream)
     _dev(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
@@ -150,8 +170,8 @@ def moe_gating_softmax_topk(logits, k, norm_topk_prob=True, weights=None, indice
     """Top-k experts per row of ``logits [T,E]`` (float32) -> (weights [T,k] f32, indices [T,k] i32)."""
     _dev(logits, "logits", torch.float32)
     T, E = logits.shape
-    weights = _out(weights, (T, k), torch.float32, logits.device, "weights")
-    indices = _out(indices, (T, k), torch.int32, logits.device, "indices")
+    weights = _out(weights, (T, k), torch.float32, logits.device, "weights", stream)
+    indices = _out(indices, (T, k), torch.int32, logits.device, "indices", stream)
     _check("moe_gating_softmax_topk", lib().moe_gating_softmax_topk(
         _ptr(logits), T, E, k, int(bool(norm_topk_prob)), _ptr(weights), _ptr(indices),
         _stream(stream, logits.device)))
@@ -162,8 +182,8 @@ def moe_gating_softmax_topk_bf16(logits, k, norm_topk_prob=True, weights=None, i
     """Top-k experts per row of bf16 ``logits [T,E]`` -> (weights [T,k] f32, indices [T,k] i32)."""
     _dev(logits, "logits", torch.bfloat16)
     T, E = logits.shape
-    weights = _out(weights, (T, k), torch.float32, logits.device, "weights")
-    indices = _out(indices, (T, k), torch.int32, logits.device, "indices")
+    weights = _out(weights, (T, k), torch.float32, logits.device, "weights", stream)
+    indices = _out(indices, (T, k), torch.int32, logits.device, "indices", stream)
     _check("moe_gating_softmax_topk_bf16", lib().moe_gating_softmax_topk_bf16(
         _ptr(logits), T, E, k, int(bool(norm_topk_prob)), _ptr(weights), _ptr(indices),
         _stream(stream, logits.device)))
@@ -180,8 +200,8 @@ def moe_group_limited_topk(scores, k, n_group, topk_group, method="group_limited
     code = {"group_limited_greedy": MOE_GROUP_TOPK_GREEDY, "noaux_tc": MOE_GROUP_TOPK_NOAUX_TC}[method]
     if bias is not None:
         _dev(bias, "bias", torch.float32)
-    weights = _out(weights, (T, k), torch.float32, scores.device, "weights")
-    indices = _out(indices, (T, k), torch.int32, scores.device, "indices")
+    weights = _out(weights, (T, k), torch.float32, scores.device, "weights", stream)
+    indices = _out(indices, (T, k), torch.int32, scores.device, "indices", stream)
     _check("moe_group_limited_topk", lib().moe_group_limited_topk(
         _ptr(scores), _ptr(bias), T, E, k, n_group, topk_group, code, _ptr(weights), _ptr(indices),
         _stream(stream, scores.device)))
@@ -196,9 +216,9 @@ def moe_indices_to_multihot(indices, probs, num_experts, multihot=None, probs_in
     T, k = indices.shape
     E = int(num_experts)
     d = indices.device
-    multihot = _out(multihot, (T, E), torch.uint8, d, "multihot")
-    probs_in_multihot = _out(probs_in_multihot, (T, E), torch.float32, d, "probs_in_multihot")
-    position_map = _out(position_map, (T, E), torch.int32, d, "position_map")
+    multihot = _out(multihot, (T, E), torch.uint8, d, "multihot", stream)
+    probs_in_multihot = _out(probs_in_multihot, (T, E), torch.float32, d, "probs_in_multihot", stream)
+    position_map = _out(position_map, (T, E), torch.int32, d, "position_map", stream)
     _check("moe_indices_to_multihot", lib().moe_indices_to_multihot(
         _ptr(indices), _ptr(probs), T, k, E, _ptr(multihot), _ptr(probs_in_multihot),
         _ptr(position_map), _stream(stream, d)))
@@ -212,9 +232,9 @@ def moe_multihot_to_indices(probs_in_multihot, position_map, k, probs=None, indi
     _dev(position_map, "position_map", torch.int32)
     T, E = probs_in_multihot.shape
     d = probs_in_multihot.device
-    probs = _out(probs, (T, k), torch.float32, d, "probs")
+    probs = _out(probs, (T, k), torch.float32, d, "probs", stream)
     if with_indices or indices is not None:
-        indices = _out(indices, (T, k), torch.int32, d, "indices")
+        indices = _out(indices, (T, k), torch.int32, d, "indices", stream)
     _check("moe_multihot_to_indices", lib().moe_multihot_to_indices(
         _ptr(probs_in_multihot), _ptr(position_map), T, E, k, _ptr(probs), _ptr(indices),
         _stream(stream, d)))
@@ -235,14 +255,14 @@ def moe_align_by_expert(indices, weights, num_experts, out=None, workspace=None,
     S = T * k
     d = indices.device
     out = dict(out or {})
-    counts = _out(out.get("counts"), (E,), torch.int32, d, "counts")
-    offsets = _out(out.get("offsets"), (E + 1,), torch.int32, d, "offsets")
-    ids = _out(out.get("sorted_token_ids"), (S,), torch.int32, d, "sorted_token_ids")
-    sw = _out(out.get("sorted_weights"), (S,), torch.float32, d, "sorted_weights")
-    rev = _out(out.get("reverse_indices"), (S,), torch.int32, d, "reverse_indices")
+    counts = _out(out.get("counts"), (E,), torch.int32, d, "counts", stream)
+    offsets = _out(out.get("offsets"), (E + 1,), torch.int32, d, "offsets", stream)
+    ids = _out(out.get("sorted_token_ids"), (S,), torch.int32, d, "sorted_token_ids", stream)
+    sw = _out(out.get("sorted_weights"), (S,), torch.float32, d, "sorted_weights", stream)
+    rev = _out(out.get("reverse_indices"), (S,), torch.int32, d, "reverse_indices", stream)
     need = moe_align_workspace_size(T, k, E)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=d)
+        workspace = _new(need, torch.uint8, d.index, stream)
     _check("moe_align_by_expert", lib().moe_align_by_expert(
         _ptr(indices), _ptr(weights), T, k, E, _ptr(counts), _ptr(offsets), _ptr(ids), _ptr(sw),
         _ptr(rev), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
@@ -267,11 +287,11 @@ def moe_align_by_expert_noalloc(indices, weights, num_experts, out=None, status=
     S = T * k
     d = indices.device
     out = dict(out or {})
-    counts = _out(out.get("counts"), (E,), torch.int32, d, "counts")
-    offsets = _out(out.get("offsets"), (E + 1,), torch.int32, d, "offsets")
-    ids = _out(out.get("sorted_token_ids"), (S,), torch.int32, d, "sorted_token_ids")
-    sw = _out(out.get("sorted_weights"), (S,), torch.float32, d, "sorted_weights")
-    rev = _out(out.get("reverse_indices"), (S,), torch.int32, d, "reverse_indices")
+    counts = _out(out.get("counts"), (E,), torch.int32, d, "counts", stream)
+    offsets = _out(out.get("offsets"), (E + 1,), torch.int32, d, "offsets", stream)
+    ids = _out(out.get("sorted_token_ids"), (S,), torch.int32, d, "sorted_token_ids", stream)
+    sw = _out(out.get("sorted_weights"), (S,), torch.float32, d, "sorted_weights", stream)
+    rev = _out(out.get("reverse_indices"), (S,), torch.int32, d, "reverse_indices", stream)
     _check("moe_align_by_expert_noalloc", lib().moe_align_by_expert_noalloc(
         _ptr(indices), _ptr(weights), T, k, E, _ptr(counts), _ptr(offsets), _ptr(ids), _ptr(sw),
         _ptr(rev), _ptr(status), _stream(stream, d)))
@@ -296,10 +316,10 @@ def moe_grouped_ffn(hidden, w13, w2, k, counts, offsets, sorted_token_ids, sorte
     if H2 != H or tuple(w2.shape) != (E, H, I):
         raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
     d = hidden.device
-    out = _out(out, (T, H), hidden.dtype, d, "out")
+    out = _out(out, (T, H), hidden.dtype, d, "out", stream)
     need = moe_grouped_ffn_workspace_size(dt, T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d)
+        workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_grouped_ffn", lib().moe_grouped_ffn(
         _ptr(hidden), _ptr(w13), _ptr(w2), dt, T, H, I, E, k, _ptr(counts), _ptr(offsets),
         _ptr(sorted_token_ids), _ptr(sorted_weights), _ptr(reverse_indices), _ptr(out),
@@ -327,14 +347,14 @@ def moe_grouped_ffn_backward(hidden, w13, w2, k, counts, offsets, sorted_token_i
     if H2 != H or tuple(w2.shape) != (E, H, I) or tuple(d_out.shape) != (T, H):
         raise ValueError("shape mismatch")
     d = hidden.device
-    d_hidden = _out(d_hidden, (T, H), hidden.dtype, d, "d_hidden")
-    d_w13 = _out(d_w13, (E, 2 * I, H), hidden.dtype, d, "d_w13")
-    d_w2 = _out(d_w2, (E, H, I), hidden.dtype, d, "d_w2")
+    d_hidden = _out(d_hidden, (T, H), hidden.dtype, d, "d_hidden", stream)
+    d_w13 = _out(d_w13, (E, 2 * I, H), hidden.dtype, d, "d_w13", stream)
+    d_w2 = _out(d_w2, (E, H, I), hidden.dtype, d, "d_w2", stream)
     if want_d_weights:
-        d_weights = _out(d_weights, (T, k), torch.float32, d, "d_weights")
+        d_weights = _out(d_weights, (T, k), torch.float32, d, "d_weights", stream)
     need = moe_grouped_ffn_backward_workspace_size(dt, T, H, I, E, k)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d)
+        workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_grouped_ffn_backward", lib().moe_grouped_ffn_backward(
         _ptr(hidden), _ptr(w13), _ptr(w2), dt, T, H, I, E, k, _ptr(counts), _ptr(offsets),
         _ptr(sorted_token_ids), _ptr(sorted_weights), _ptr(reverse_indices), _ptr(d_out), _ptr(d_hidden),
@@ -362,14 +382,14 @@ def moe_layer_forward(hidden, router_logits, w13, w2, k, norm_topk_prob=True, ou
     if H2 != H or tuple(w2.shape) != (E, H, I) or tuple(router_logits.shape) != (T, E):
         raise ValueError("shapes must be hidden [T,H], router_logits [T,E], w13 [E,2I,H], w2 [E,H,I]")
     d = hidden.device
-    out = _out(out, (T, H), hidden.dtype, d, "out")
+    out = _out(out, (T, H), hidden.dtype, d, "out", stream)
     if topk_weights is not None:
-        _out(topk_weights, (T, k), torch.float32, d, "topk_weights")
+        _out(topk_weights, (T, k), torch.float32, d, "topk_weights", stream)
     if topk_indices is not None:
-        _out(topk_indices, (T, k), torch.int32, d, "topk_indices")
+        _out(topk_indices, (T, k), torch.int32, d, "topk_indices", stream)
     if workspace is None:
         need = moe_layer_workspace_size(dt, T, H, I, E, k)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d)
+        workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_layer_forward", lib().moe_layer_forward(
         _ptr(hidden), _ptr(router_logits), _ptr(w13), _ptr(w2), dt, T, H, I, E, k,
         int(bool(norm_topk_prob)), _ptr(out), _ptr(topk_weights), _ptr(topk_indices),
@@ -419,19 +439,6 @@ def _take(t, name, dtype, index):
     return t.data_ptr()
 
 
-def _new(shape, dtype, index, stream):
-    """Memory for a call on ``stream``, from that stream's pool: a block that the current stream has given back may
-    still be read by what is queued there. The current stream is noted with it, where outputs are used next."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=_device(index))
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=_device(index))
-    t.record_stream(torch.cuda.current_stream(index))
-    return t
-
-
 def _give(t, name, shape, dtype, index, stream):
     """(tensor, address) of an output: the caller's after its checks, or a new one."""
     if t is None:
@@ -463,7 +470,6 @@ def _raw(stream, index):
 # of 0.8): a 4-bit product that makes its workspace takes the host 13.7 us, and 20.1 where the library is called once to
 # say that it needs one.
 _sizes = functools.lru_cache(maxsize=4096)
-_device = functools.lru_cache(maxsize=None)(lambda index: torch.device("cuda", index))
 
 
 def _space(workspace, need, index, stream):
@@ -644,7 +650,7 @@ def moe_gather_rows(hidden, sorted_token_ids, offsets, k, out=None, stream=None)
     T, H = hidden.shape
     E = offsets.numel() - 1
     d = hidden.device
-    out = _out(out, (T * k, H), hidden.dtype, d, "out")
+    out = _out(out, (T * k, H), hidden.dtype, d, "out", stream)
     _check("moe_gather_rows", lib().moe_gather_rows(
         _ptr(hidden), _ptr(sorted_token_ids), _ptr(offsets), dt, T, H, E, k, _ptr(out), _stream(stream, d)))
     return out
@@ -657,12 +663,12 @@ def moe_ep_receive_index(recv_counts, R, local_counts=None, local_offsets=None, 
     _dev(recv_counts, "recv_counts", torch.int32)
     G, El = recv_counts.shape
     d = recv_counts.device
-    local_counts = _out(local_counts, (El,), torch.int32, d, "local_counts")
-    local_offsets = _out(local_offsets, (El + 1,), torch.int32, d, "local_offsets")
-    perm = _out(perm, (R,), torch.int32, d, "perm")
+    local_counts = _out(local_counts, (El,), torch.int32, d, "local_counts", stream)
+    local_offsets = _out(local_offsets, (El + 1,), torch.int32, d, "local_offsets", stream)
+    perm = _out(perm, (R,), torch.int32, d, "perm", stream)
     need = int(lib().moe_ep_receive_workspace_size(G, El))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d)
+        workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_ep_receive_index", lib().moe_ep_receive_index(
         _ptr(recv_counts), G, El, int(R), _ptr(local_counts), _ptr(local_offsets), _ptr(perm), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream, d)))
@@ -677,10 +683,10 @@ def moe_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, out=None, w
     H = y_sorted.shape[1]
     E = offsets.numel() - 1
     d = y_sorted.device
-    out = _out(out, (T, H), y_sorted.dtype, d, "out")
+    out = _out(out, (T, H), y_sorted.dtype, d, "out", stream)
     need = int(lib().moe_ep_combine_workspace_size(T, k))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d)
+        workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_ep_combine", lib().moe_ep_combine(
         _ptr(y_sorted), _ptr(topk_weights), _ptr(reverse_indices), _ptr(offsets), dt, T, k, H, E, _ptr(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, d)))

@@ -238,8 +238,9 @@ unsigned blocks_for(long n) { return (unsigned)((n + 256 * kUnroll - 1) / (256 *
 // With rows that repeat, quantising each source row once into the workspace and copying the packed
 // rows moves T (b + 17/32) + R 17/16 bytes a value instead of R (b + 17/32), most of the copies'
 // reads from L2. Measured, 16384 bf16 rows of 2048 to 131072: 191 us in one kernel (the rows do not
-// stay in L2 beside the output), 51 in two. Small calls take the single launch.
-bool in_two(int T, int K, bool with_rows, long R) { return with_rows && R >= 2L * T && R * K >= (1L << 22); }
+// stay in L2 beside the output), 51 in two. Small calls take the single launch, and so do rows of a
+// matrix without any, which are all zero and reported.
+bool in_two(int T, int K, bool with_rows, long R) { return with_rows && T > 0 && R >= 2L * T && R * K >= (1L << 22); }
 
 template <class T>
 int quantize(const void* x, int Tr, int K, const int32_t* rows, int R, uint8_t* codes, uint8_t* scales, void* ws,

@@ -16,6 +16,7 @@ namespace moe {
 static thread_local char g_err[512] = "";
 
 int fail(int code, const char* fmt, ...) {
+  if (code == MOE_ERR_CUDA) cudaGetLastError();   // this call reports the error; the thread's next one must not find it
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);

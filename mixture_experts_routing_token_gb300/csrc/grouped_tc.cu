@@ -576,20 +576,28 @@ struct Pad {
 struct Live {
   uint16_t expert[MOE_MAX_EXPERTS];
   int count;
+  int lo, hi;       // the rows that some group owns (off[0] and off[E] of grouped::group_list)
 };
 
 // Whole block.
-__device__ __forceinline__ void live_list(const int32_t* offsets, int E, Live& live) {
+__device__ __forceinline__ void live_list(const int32_t* offsets, int E, int S, Live& live) {
   if (threadIdx.x < 32) {
-    int n = 0;
+    int n = 0, top = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + (int)threadIdx.x;
-      const bool on = e < E && __ldg(offsets + e) < __ldg(offsets + e + 1);
+      const int a = e < E ? __ldg(offsets + e) : 0, b = e < E ? __ldg(offsets + e + 1) : 0;
+      const bool on = a < b;
+      top = max(top, max(a, b));
       const unsigned m = __ballot_sync(0xffffffffu, on);
       if (on) live.expert[n + __popc(m & ((1u << threadIdx.x) - 1u))] = (uint16_t)e;
       n += __popc(m);
+      if (e == 0) live.lo = min(max(a, 0), S);
     }
-    if (threadIdx.x == 0) live.count = n;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (threadIdx.x == 0) {
+      live.count = n;
+      live.hi = min(top, S);
+    }
   }
   __syncthreads();
 }
@@ -598,15 +606,20 @@ __device__ __forceinline__ long div_by(long n, int d) {
   return n < (1L << 31) ? (long)((uint32_t)n / (uint32_t)d) : n / d;
 }
 
-// Row and piece of the i-th piece of a matrix, of live experts only where it is by expert.
+// Pieces of a matrix that some group reads: rows that one owns, or, where it is by expert, those of live experts.
+__device__ __forceinline__ long live_pieces(int pieces, int per, const Live& live) {
+  return (long)(per ? (long)live.count * per : live.hi - live.lo) * pieces;
+}
+
+// Row and piece of the i-th of them.
 __device__ __forceinline__ long piece_row(long i, int pieces, int per, const Live& live, int& piece) {
   long r = div_by(i, pieces);
   piece = (int)(i - r * pieces);
   if (per) {
     const long k = div_by(r, per);
-    r += (live.expert[k] - k) * per;
+    return r + (live.expert[k] - k) * per;
   }
-  return r;
+  return r + live.lo;
 }
 
 // Eight 16-bit values from p on, of which the first `count` are wanted (zeros else), as words: two aligned
@@ -639,7 +652,7 @@ __device__ __forceinline__ uint4 load_any(const uint16_t* p, int count, uintptr_
 
 struct PadParams {
   const int32_t* offsets;
-  int E;
+  int E, S;
   Pad m[3];
   int count;
 };
@@ -648,12 +661,12 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadParams P) {
   __shared__ Live live;
   pdl_wait();
   pdl_trigger();
-  live_list(P.offsets, P.E, live);
+  live_list(P.offsets, P.E, P.S, live);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (k >= P.count) break;
     const Pad M = P.m[k];
-    const long n = M.per ? (long)live.count * M.per * M.pieces : M.n;
+    const long n = live_pieces(M.pieces, M.per, live);
     for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
       int piece;
       const long r = piece_row(i, M.pieces, M.per, live, piece);
@@ -698,7 +711,7 @@ struct Split {
 
 struct SplitParams {
   const int32_t* offsets;
-  int E;
+  int E, S;
   Split m[3];
   int count;
   int* flags;           // grouped::kFlagWords, one per block and zeros
@@ -708,18 +721,19 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
   return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out.
+// x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out. Rows that no group
+// owns stay out: they may never have been written, and what they hold must not choose the kernel.
 __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
   __shared__ Live live;
   pdl_wait();
   pdl_trigger();
-  live_list(P.offsets, P.E, live);
+  live_list(P.offsets, P.E, P.S, live);
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     if (k >= P.count) break;
     const Split M = P.m[k];
-    const long n = M.per ? (long)live.count * M.per * M.pieces : M.n;
+    const long n = live_pieces(M.pieces, M.per, live);
     for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long)gridDim.x * blockDim.x) {
       int piece;
       const long r = piece_row(i, M.pieces, M.per, live, piece);
@@ -810,12 +824,13 @@ int launch_grouped_tc(const GroupedArgs& a, cudaStream_t s) {
     SplitParams q{};
     q.offsets = a.offsets;
     q.E = a.E;
+    q.S = a.S;
     q.flags = c.take<int>(grouped::kFlagWords);
     add_split(q, a.x, a.S, a.K, 0, c, &x);
     add_split(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    PadParams q{a.offsets, a.E, {}, 0};
+    PadParams q{a.offsets, a.E, a.S, {}, 0};
     padded(q, a.x, a.S, a.K, 0, c, &x);
     padded(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_pads(q, s))) return rc;
@@ -847,13 +862,14 @@ int launch_grouped_tc_backward(const GroupedArgs& a, cudaStream_t s) {
     SplitParams q{};
     q.offsets = a.offsets;
     q.E = a.E;
+    q.S = a.S;
     q.flags = c.take<int>(grouped::kFlagWords);
     add_split(q, a.d_y, a.S, a.N, 0, c, &dy);
     if (a.d_w) add_split(q, a.x, a.S, a.K, 0, c, &x);
     if (a.d_x) add_split(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if ((rc = launch_split(q, &p, s))) return rc;
   } else {
-    PadParams q{a.offsets, a.E, {}, 0};
+    PadParams q{a.offsets, a.E, a.S, {}, 0};
     padded(q, a.d_y, a.S, a.N, 0, c, &dy);
     if (a.d_x) padded(q, a.w, (long)a.E * a.N, a.K, a.N, c, &w);
     if (a.d_w) padded(q, a.x, a.S, a.K, 0, c, &x);

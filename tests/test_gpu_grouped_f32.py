@@ -58,3 +58,21 @@ def test_close_as_float32_is(moe, counts, K, N, positive):
     x, w, g = x.double().numpy(), w.double().numpy(), g.double().numpy()
     for name, a, b in zip(("y", "d_x", "d_w"), got, (grouped.grouped_gemm(x, w, off), *grouped.grouped_gemm_backward(x, w, off, g))):
         assert np.linalg.norm(to64(a) - b) <= 1e-6 * np.linalg.norm(b), name
+
+
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), 3.0e38])
+def test_rows_without_an_expert_change_nothing(moe, junk):
+    """Rows before the first group and after the last one: whatever they hold, the same bits come out."""
+    off, o = offsets([1100, 0, 900], first=2)
+    S, K, N, E = 2005, 517, 1030, 3
+    assert takes_parts(moe, S, K, N, E)
+    x, w, g = normal((S, K), 1).to(DEV), normal((E, N, K), 2).to(DEV), normal((S, N), 3).to(DEV)
+    none = torch.ones(S, dtype=torch.bool, device=DEV)
+    none[2:2002] = False
+    x[none], g[none] = 0.0, 0.0
+    want = run(moe, x, w, o, g)
+    x[none], g[none] = junk, junk
+    got = run(moe, x, w, o, g)
+    for name, a, b in zip(("y", "d_x", "d_w"), got, want):
+        assert torch.equal(a, b), name
+    assert not got[0][none].any() and not got[1][none].any()

@@ -34,8 +34,10 @@
 // bf16 operands: 5e-7 at 512 terms, 9e-6 at 8192). So an accumulator holds two steps (K = 128, the
 // small products first) and is then added in registers, rounded to nearest, by eight epilogue warps
 // with 128 sums a thread, while the next two steps go into the other one. Parts make no sense of
-// infinities and NaN (nor of 2^127 and above, which may round to infinity): the first kernel flags
-// them, and then this one leaves everything to the kernel on the CUDA cores, which follows.
+// infinities and NaN, and leading parts may be larger than their values by 2^-8, so that sums of their
+// products leave float32's range where those of the values do not: below 2^60 a value, 128 products
+// stay below 2^127 (1 + 2^-8)^2. The first kernel flags what lies above, and then this one leaves
+// everything to the kernel on the CUDA cores, which follows.
 //
 // Barriers as in the FFN's pair kernel: full[s] in the leader CTA (the pair's bytes, and in
 // the gradients one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
@@ -751,7 +753,7 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
       uint32_t q[3][4] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        bad |= (__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f000000u;     // 2^127 and above, infinity, NaN
+        bad |= (__float_as_uint(v[j]) & 0x7fffffffu) >= 0x5d800000u;     // 2^60 and above, infinity, NaN
         float left = v[j];
 #pragma unroll
         for (int part = 0; part < 3; ++part) {

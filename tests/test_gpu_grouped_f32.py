@@ -16,6 +16,8 @@ from oracle import grouped
 
 pytestmark = pytest.mark.gpu
 
+TERM = 8 * 2.0 ** -23      # a sum with one term: six products, added with truncation, and what is left out
+
 
 @pytest.fixture(scope="module")
 def moe():
@@ -76,3 +78,79 @@ def test_rows_without_an_expert_change_nothing(moe, junk):
     for name, a, b in zip(("y", "d_x", "d_w"), got, want):
         assert torch.equal(a, b), name
     assert not got[0][none].any() and not got[1][none].any()
+
+
+def few_terms(S, K, N, E, off, terms):
+    """Operands whose sums are all the given numbers times 4, `terms` in places 16 apart: for the product, for d_x and
+    for d_w (one output column of it), and the operand that holds a 4 everywhere."""
+    at = 16 * torch.arange(len(terms))
+    v = torch.tensor(terms)
+    x, g = torch.zeros(S, K), torch.zeros(S, N)
+    x[:, at], g[:, at] = v, v
+    gw = torch.zeros(S, N)
+    for e in range(E):
+        if off[e + 1] - off[e] > int(at[-1]):
+            gw[off[e] + at] = v[:, None].expand(-1, N)
+    return x.to(DEV), g.to(DEV), gw.to(DEV)
+
+
+def test_sums_that_pass_near_the_largest_float32(moe):
+    """A first term just below the largest float32 and three negative ones whose leading parts are too large: the small
+    products of parts, which are added first, then carry the first term over the edge. In order all sums are finite."""
+    off, o = offsets([1100, 0, 900])
+    S, K, N, E = 2000, 517, 1030, 3
+    assert takes_parts(moe, S, K, N, E)
+    # 255/256 has 8 bits; 1/2 + 3/512 + 2^-20 rounds up to 1/2 + 4/512 in 8 bits, by almost half a step of 2^-8
+    terms = [255 / 256 * 2.0 ** 126] + 3 * [-(0.5 + 3 / 512 + 2.0 ** -20) * 2.0 ** 126]
+    want = sum(4 * t for t in terms)
+    tol = 8 * 2.0 ** -23 * sum(abs(4 * t) for t in terms)
+    x, g, gw = few_terms(S, K, N, E, off, terms)
+    w, four = torch.full((E, N, K), 4.0, device=DEV), torch.full((S, K), 4.0, device=DEV)
+    y = moe.moe_grouped_gemm(x, w, o)
+    d_x, _ = moe.moe_grouped_gemm_backward(four, w, o, g, want_d_w=False)
+    _, d_w = moe.moe_grouped_gemm_backward(four, w, o, gw, want_d_x=False)
+    for name, got in (("y", y), ("d_x", d_x), ("d_w", d_w[[0, 2]])):
+        assert torch.isfinite(got).all() and ((got.double() - want).abs() <= tol).all(), name
+
+
+def test_largest_values_in_parts(moe):
+    """128 terms of values just below those that leave the parts: the sum is half the largest float32."""
+    off, o = offsets([1100, 0, 900])
+    S, K, N, E = 2000, 517, 1030, 3
+    rng = np.random.default_rng(4)
+    x, w = np.zeros((S, K), np.float32), (1.9 + 0.099 * rng.random((E, N, K))).astype(np.float32) * np.float32(2.0 ** 59)
+    x[:, :128] = (1.9 + 0.099 * rng.random((S, 128))).astype(np.float32) * np.float32(2.0 ** 59)
+    y = moe.moe_grouped_gemm(torch.from_numpy(x).to(DEV), torch.from_numpy(w).to(DEV), o)
+    want = grouped.grouped_gemm(x, w, off)
+    assert torch.isfinite(y).all() and np.linalg.norm((to64(y) - want) * 2.0 ** -127) <= 1e-6 * np.linalg.norm(want * 2.0 ** -127)
+
+
+def one_term(moe, a, b):
+    """Products and gradients all of whose sums have one term, a value of `a` times one of `b` -> pairs (got, exact)."""
+    off, o = offsets([1100, 0, 900])
+    S, K, N, E = 2000, 517, 1030, 3
+    assert takes_parts(moe, S, K, N, E)
+    left = lambda i: torch.tensor(a, device=DEV)[i % len(a)]  # noqa: E731
+    right = lambda *s: torch.tensor(b, device=DEV)[torch.arange(int(np.prod(s)), device=DEV) % len(b)].reshape(s)  # noqa: E731
+    p = torch.arange(S, device=DEV)
+    expert = torch.from_numpy(grouped.expert_of_rows(off, S)).to(DEV)
+    x, w, g = torch.zeros(S, K, device=DEV), right(E, N, K), torch.zeros(S, N, device=DEV)
+    x[p, p % K] = left(p)
+    yield moe.moe_grouped_gemm(x, w, o), x[p, p % K].double()[:, None] * w[expert, :, p % K].double()
+    g[p, p % N] = left(p)
+    d_x, _ = moe.moe_grouped_gemm_backward(x, w, o, g, want_d_w=False)
+    yield d_x, g[p, p % N].double()[:, None] * w[expert, p % N].double()
+    x, g = right(S, K), torch.zeros(S, N, device=DEV)
+    g[7], g[1500] = left(torch.arange(N, device=DEV)), left(torch.arange(N, device=DEV) + 1)
+    _, d_w = moe.moe_grouped_gemm_backward(x, w, o, g, want_d_x=False)
+    want = torch.zeros(E, N, K, dtype=torch.float64, device=DEV)
+    want[0], want[2] = g[7].double()[:, None] * x[7].double(), g[1500].double()[:, None] * x[1500].double()
+    yield d_w, want
+
+
+@pytest.mark.parametrize("a,b", [([1.999 * 2.0 ** 126], [1.999, -1.5]), ([1.999 * 2.0 ** 63, -(2.0 ** 63)], [1.999 * 2.0 ** 63]),
+                                 ([1.998 * 2.0 ** 20], [1.9985 * 2.0 ** 106, 3.0])])
+def test_results_next_to_the_largest_float32(moe, a, b):
+    """Values whose leading parts round up, with a product that then passes the largest float32 while theirs does not."""
+    for got, want in one_term(moe, a, b):
+        assert torch.isfinite(got).all() and ((got.double() - want).abs() <= TERM * want.abs()).all()

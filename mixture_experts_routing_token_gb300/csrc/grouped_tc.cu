@@ -26,7 +26,7 @@
 //     the rows past the end in shared memory (whole 128-byte lines, so the swizzle does
 //     not matter) and only then hands the step to the MMA issuer.
 //
-// float32. A value is h + m + l, three bf16 parts of 8 bits each (what is left is below 2^-26 of
+// float32. A value is h + m + l, three bf16 parts of 8 bits each (what is left is at most 2^-24 of
 // it; a first kernel writes the parts into the workspace), and a product of two values the six
 // products of parts hl + lh + mm + hm + mh + hh, each exact in float32; the three left out are below
 // 2^-25 of it. The tensor cores add to an accumulator with truncation, 2^-24 of it on average and
@@ -36,8 +36,9 @@
 // with 128 sums a thread, while the next two steps go into the other one. Parts make no sense of
 // infinities and NaN, and leading parts may be larger than their values by 2^-8, so that sums of their
 // products leave float32's range where those of the values do not: below 2^60 a value, 128 products
-// stay below 2^127 (1 + 2^-8)^2. The first kernel flags what lies above, and then this one leaves
-// everything to the kernel on the CUDA cores, which follows.
+// stay below 2^127 (1 + 2^-8)^2. Parts of small values are multiples of 2^-133, bf16's smallest, half
+// of which is 2^-24 of 2^-110. The first kernel flags what lies outside (zeros aside), and then this one
+// leaves everything to the kernel on the CUDA cores, which follows.
 //
 // Barriers as in the FFN's pair kernel: full[s] in the leader CTA (the pair's bytes, and in
 // the gradients one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
@@ -753,7 +754,8 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
       uint32_t q[3][4] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        bad |= (__float_as_uint(v[j]) & 0x7fffffffu) >= 0x5d800000u;     // 2^60 and above, infinity, NaN
+        const uint32_t size = __float_as_uint(v[j]) & 0x7fffffffu;
+        bad |= size != 0 && size - 0x08800000u >= 0x5d800000u - 0x08800000u;   // not in [2^-110, 2^60)
         float left = v[j];
 #pragma unroll
         for (int part = 0; part < 3; ++part) {

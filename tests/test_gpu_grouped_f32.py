@@ -17,6 +17,7 @@ from oracle import grouped
 pytestmark = pytest.mark.gpu
 
 TERM = 8 * 2.0 ** -23      # a sum with one term: six products, added with truncation, and what is left out
+GRID = 2.0 ** -149
 
 
 @pytest.fixture(scope="module")
@@ -62,7 +63,7 @@ def test_close_as_float32_is(moe, counts, K, N, positive):
         assert np.linalg.norm(to64(a) - b) <= 1e-6 * np.linalg.norm(b), name
 
 
-@pytest.mark.parametrize("junk", [float("nan"), float("inf"), 3.0e38])
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), 3.0e38, 1e-40])
 def test_rows_without_an_expert_change_nothing(moe, junk):
     """Rows before the first group and after the last one: whatever they hold, the same bits come out."""
     off, o = offsets([1100, 0, 900], first=2)
@@ -154,3 +155,30 @@ def test_results_next_to_the_largest_float32(moe, a, b):
     """Values whose leading parts round up, with a product that then passes the largest float32 while theirs does not."""
     for got, want in one_term(moe, a, b):
         assert torch.isfinite(got).all() and ((got.double() - want).abs() <= TERM * want.abs()).all()
+
+
+@pytest.mark.parametrize("exponent", [-104, -110, -126, -130, -140])
+def test_small_values_keep_their_bits(moe, exponent):
+    """Values next to float32's smallest, times large ones."""
+    small = (1 + np.random.default_rng(1).random(61)) * 2.0 ** exponent * np.random.default_rng(2).choice([-1, 1], 61)
+    large = (1 + np.random.default_rng(3).random(53)) * 2.0 ** 55
+    for a, b in ((small, large), (large, small)):
+        for got, want in one_term(moe, a.astype(np.float32).tolist(), b.astype(np.float32).tolist()):
+            assert ((got.double() - want).abs() <= TERM * want.abs()).all()
+
+
+@pytest.mark.parametrize("ex,ew", [(-60, -55), (-70, -50), (-75, -60)])
+def test_small_sums_of_values_of_either_size(moe, ex, ew):
+    """Sums whose low parts, or all of them, lie below float32's smallest normal value: a step of 2^-149 at most for
+    each of the additions, 49 for 128 terms."""
+    off, o = offsets([1100, 0, 900])
+    S, K, N, E = 2000, 517, 1030, 3
+    assert takes_parts(moe, S, K, N, E)
+    x, w, g = normal((S, K), 1, 2.0 ** ex), normal((E, N, K), 2, 2.0 ** ew), normal((S, N), 3, 2.0 ** ew)
+    y, d_x, d_w = run(moe, x.to(DEV), w.to(DEV), o, (g * 2.0 ** (ex - ew)).to(DEV))
+    d_w = moe.moe_grouped_gemm_backward(x.to(DEV), w.to(DEV), o, g.to(DEV), want_d_x=False)[1]
+    x, w, g = x.double().numpy(), w.double().numpy(), g.double().numpy()
+    d_x64, d_w64 = grouped.grouped_gemm_backward(x, w, off, g * 2.0 ** (ex - ew))[0], grouped.grouped_gemm_backward(x, w, off, g)[1]
+    for name, got, want, R in (("y", y, grouped.grouped_gemm(x, w, off), K), ("d_x", d_x, d_x64, N), ("d_w", d_w, d_w64, 1100)):
+        steps = 49 * (R // 128 + 1)
+        assert np.linalg.norm(to64(got) - want) <= 1e-6 * np.linalg.norm(want) + steps * GRID * want.size ** 0.5, name

@@ -322,6 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
           }
           ok = ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
           if (!ok) break;
+          // a step that the tail warps cleared, the other CTA's among them
+          if (GRAD && ti.dw && sp.block == ti.blocks - 1 && ti.g.rows() % BK != 0)
+            acquire_cluster(ptx::smem_u32(&full_bar[stage]), ph);
           ptx::tc_fence_after();
           const uint32_t a0 = sA(stage), b0 = sB(stage);
           // descriptors of the step's first MMA; K-major operands advance 32 bytes a K = 16, MN-major 2 KB
@@ -495,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
+        if (lane == 0) arrive_remote_release(map_to_rank(ptx::smem_u32(&full_bar[s]), 0));
       }
       if (!ok) break;
     }

@@ -65,6 +65,21 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same with a release that the other CTA's threads acquire (acquire_cluster): for shared memory
+// of this CTA's own that generic stores wrote and that an MMA issued by the other CTA reads.
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Acquire of what arrive_remote_release handed over, after a wait for that phase: the phase is
+// complete, so the test passes.
+__device__ __forceinline__ void acquire_cluster(uint32_t bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(parity)
+      : "memory");
+}
 
 // Shared-memory descriptor for an MN-major operand as a 128-byte-swizzled TMA
 // box of 64 MN elements x 64 K rows writes it: 8-row K groups 1024 bytes
@@ -97,11 +112,9 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Make this thread's shared-memory writes visible to TMA and tcgen05 (the async proxy). The
-// writes are complete when the fence is, so an arrive_remote after it (and a __syncwarp for the
-// warp's other lanes) may hand them to an MMA that the other CTA issues and that reads them on
-// this SM; a cluster-scope release, or an acquire fence in the issuer, would also wait for
-// unrelated global accesses.
+// Make this thread's shared-memory writes visible to TMA and tcgen05 (the async proxy). Where an
+// MMA that the other CTA issues reads them on this SM, the barrier has to order them at the cluster's
+// scope, too (arrive_remote_release).
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

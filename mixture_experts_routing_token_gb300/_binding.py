@@ -115,9 +115,22 @@ def _check(fn, rc):
         raise MoeError(fn, rc, lib().moe_last_error().decode())
 
 
+# Index of the current device, without the checks of torch.cuda.current_device: tensors that lie on a GPU came before.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_current(index, name):
+    """The library launches on the current device, so tensors of another one are refused: its kernels would run there
+    on this one's addresses."""
+    if index != _current_device():
+        raise ValueError(f"{name} is on cuda:{index}, but the current device is cuda:{_current_device()}: "
+                         f"make the call under torch.cuda.device({index})")
+
+
 def _dev(t, name, dtype=None):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise ValueError(f"{name} must be a CUDA tensor")
+    _on_current(t.get_device(), name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -429,6 +442,7 @@ def _first(t, name):
     index = t.get_device()
     if index < 0 or not t.is_contiguous():
         _refuse(t, name, None, index)
+    _on_current(index, name)
     return t.data_ptr(), t.dtype, index
 
 

@@ -486,6 +486,12 @@ def _raw(stream, index):
 _sizes = functools.lru_cache(maxsize=4096)
 
 
+def _fits(*sizes):
+    """The library's sizes are 32-bit, and ctypes cuts what is larger down to them without a word."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes must be below 2^31 (got {max(sizes)})")
+
+
 def _space(workspace, need, index, stream):
     """(tensor, address, bytes) of the caller's workspace, or of a new one where one is needed. The caller holds it
     until the launch; then it goes back to the pool of the call's stream."""
@@ -499,6 +505,7 @@ def _space(workspace, need, index, stream):
 
 @_sizes
 def moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E) -> int:
+    _fits(S, K, N, E)
     return int(lib().moe_grouped_gemm_workspace_size(dtype_code, S, K, N, E))
 
 
@@ -526,6 +533,7 @@ def moe_grouped_gemm(x, w, offsets, out=None, workspace=None, status=None, strea
 
 @_sizes
 def moe_grouped_gemm_backward_workspace_size(dtype_code, S, K, N, E) -> int:
+    _fits(S, K, N, E)
     return int(lib().moe_grouped_gemm_backward_workspace_size(dtype_code, S, K, N, E))
 
 
@@ -557,6 +565,7 @@ def moe_grouped_gemm_backward(x, w, offsets, d_y, d_x=None, d_w=None, workspace=
 
 @_sizes
 def moe_mxfp4_quantize_workspace_size(T, K, with_rows, R) -> int:
+    _fits(T, K, R)
     return int(lib().moe_mxfp4_quantize_workspace_size(T, K, int(bool(with_rows)), R))
 
 
@@ -603,6 +612,7 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
     lead, K = cs[:-1], 2 * cs[-1]
     if scales.shape != (*lead, K // 32):
         raise ValueError("shapes must be codes [..., K / 2], scales [..., K / 32]")
+    _fits(lead.numel(), K)
     out, op = _give(out, "out", (*lead, K), dtype, d, stream)
     rc = lib().moe_mxfp4_dequantize(cp, sp, lead.numel(), K, dt, op, _raw(stream, d))
     if rc:
@@ -612,6 +622,7 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
 
 @_sizes
 def moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation=None) -> int:
+    _fits(S, K, N, E)
     act = MOE_ACT_NONE if activation is None else MOE_ACT_SILU_AND_MUL
     return int(lib().moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, act))
 

@@ -412,6 +412,7 @@ def moe_layer_forward(hidden, router_logits, w13, w2, k, norm_topk_prob=True, ou
 
 
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_ACTIVATIONS = {None: MOE_ACT_NONE, "silu_and_mul": MOE_ACT_SILU_AND_MUL}
 _U8, _I32 = torch.uint8, torch.int32
 
 
@@ -623,7 +624,7 @@ def moe_mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=N
 @_sizes
 def moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation=None) -> int:
     _fits(S, K, N, E)
-    act = MOE_ACT_NONE if activation is None else MOE_ACT_SILU_AND_MUL
+    act = _ACTIVATIONS.get(activation, activation)        # as the product takes it, or the library's code
     return int(lib().moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, act))
 
 
@@ -652,13 +653,13 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
         raise ValueError("shapes must be x_codes [S, K / 2], x_scales [S, K / 32], w_codes [E, N, K / 2], "
                          "w_scales [E, N, K / 32], offsets [E + 1] with K a multiple of 32")
     K = 2 * half
-    cols, act = N, MOE_ACT_NONE
-    if activation is not None:
-        if activation != "silu_and_mul":
-            raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+    cols, act = N, _ACTIVATIONS[activation]
+    if act:
         if N % 2:
             raise ValueError("silu_and_mul needs an even N")
-        cols, act = N // 2, MOE_ACT_SILU_AND_MUL
+        cols = N // 2
     out, yp = _give(out, "out", (S, cols), out_dtype, d, stream)
     space, ws, nb = _space(workspace, moe_mxfp4_grouped_gemm_workspace_size(S, K, N, E, activation), d, stream)
     rc = lib().moe_mxfp4_grouped_gemm(xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, ws, nb, _status_ptr(status, d),

@@ -295,11 +295,10 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
  *   16-bit K % 8 == 0 and for small float32 problems: then ws may be null).
  * S, K, N may have any size >= 0 (K = 0 gives zeros). 16-bit types run on the
  * tcgen05 tensor cores. float32 keeps float32's accuracy: on the CUDA cores, or
- * for large products on the tensor cores in three bf16 parts per value (2^-24
- * of each value at most, sums rounded to nearest every 128 terms; where rows of
- * an expert or weights of one with rows hold infinities, NaN or magnitudes of
- * 2^60 and more or, zeros aside, below 2^-110, the CUDA cores compute the call,
- * decided on the device).
+ * for large products on the tensor cores in three bf16 parts per value (all of
+ * its bits; sums rounded to nearest every 128 terms; where rows of an expert or
+ * weights of one with rows hold infinities, NaN or magnitudes of 2^44 and more,
+ * the CUDA cores compute the call, decided on the device).
  */
 MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E);
 MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,

@@ -26,19 +26,20 @@
 //     the rows past the end in shared memory (whole 128-byte lines, so the swizzle does
 //     not matter) and only then hands the step to the MMA issuer.
 //
-// float32. A value is h + m + l, three bf16 parts of 8 bits each (what is left is at most 2^-24 of
-// it; a first kernel writes the parts into the workspace), and a product of two values the six
+// float32. A value is h + m + l, three bf16 parts of 8 bits each (all of its 24; a first kernel writes
+// the parts into the workspace), and a product of two values the six
 // products of parts hl + lh + mm + hm + mh + hh, each exact in float32; the three left out are below
 // 2^-25 of it. The tensor cores add to an accumulator with truncation, 2^-24 of it on average and
 // always toward zero, which a float32 result must not collect over a long reduction (measured on
 // bf16 operands: 5e-7 at 512 terms, 9e-6 at 8192). So an accumulator holds two steps (K = 128, the
 // small products first) and is then added in registers, rounded to nearest, by eight epilogue warps
-// with 128 sums a thread, while the next two steps go into the other one. Parts make no sense of
-// infinities and NaN, and leading parts may be larger than their values by 2^-8, so that sums of their
-// products leave float32's range where those of the values do not: below 2^60 a value, 128 products
-// stay below 2^127 (1 + 2^-8)^2. Parts of small values are multiples of 2^-133, bf16's smallest, half
-// of which is 2^-24 of 2^-110. The first kernel flags what lies outside (zeros aside), and then this one
-// leaves everything to the kernel on the CUDA cores, which follows.
+// with 128 sums a thread, while the next two steps go into the other one. The parts are those of 2^16 times
+// the value: every float32 is a multiple of 2^-149, bf16 ends at 2^-133, so the smallest keep all their
+// bits; the sums take 2^-32 back on their way into the registers, in the addition (fma). Parts make no sense
+// of infinities and NaN, and leading parts may be larger than their values by 2^-8, so that sums of their
+// products leave float32's range where those of the values do not: below 2^44 a value (2^60 with the factor),
+// 128 products stay below 2^127 (1 + 2^-8)^2. The first kernel flags what lies above, and then this one leaves
+// everything to the kernel on the CUDA cores, which follows.
 //
 // Barriers as in the FFN's pair kernel: full[s] in the leader CTA (the pair's bytes, and in
 // the gradients one arrival of each CTA for a cleared step), empty[s] in both, tfull / tempty per
@@ -100,6 +101,8 @@ struct Tile {
   int e, m, n, blocks;      // blocks: of 64 along the reduction
   grouped::Span g;
 };
+
+constexpr float kPartScale = 65536.0f, kSumScale = 1.0f / (65536.0f * 65536.0f);   // float32 in parts
 
 // Steps of a tile: its blocks, in order; in float32 two blocks (or the odd last one) at a time, with
 // six products of parts.
@@ -418,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<GRAD, T>(), 
             ptx::tmem_ld32(taddr + c * 32, y);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(y[j]);
+            for (int j = 0; j < 32; ++j) sum[c * 32 + j] = fmaf(__uint_as_float(y[j]), kSumScale, sum[c * 32 + j]);
           }
           ptx::tc_fence_before();
           __syncwarp();
@@ -727,7 +730,7 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
   return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out. Rows that no group
+// 2^16 x = h + m + l, each rounded to nearest from what is left. Bound by memory: 4 bytes in, 6 out. Rows that no group
 // owns stay out: they may never have been written, and what they hold must not choose the kernel.
 __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
   __shared__ Live live;
@@ -757,9 +760,8 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitParams P) {
       uint32_t q[3][4] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t size = __float_as_uint(v[j]) & 0x7fffffffu;
-        bad |= size != 0 && size - 0x08800000u >= 0x5d800000u - 0x08800000u;   // not in [2^-110, 2^60)
-        float left = v[j];
+        bad |= (__float_as_uint(v[j]) & 0x7fffffffu) >= 0x55800000u;     // 2^44 and above, infinity, NaN
+        float left = v[j] * kPartScale;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
           const uint32_t bits = bf16_bits(left);

@@ -288,17 +288,20 @@ MOE_API int moe_layer_forward(const void* hidden, const float* router_logits, co
  *   x [S, K], w [E, N, K], y [S, N], all of dtype (MOE_F32, MOE_BF16, MOE_F16;
  *   sums in float32, one rounding to dtype).
  *   offsets [E + 1] int32, ascending, in [0, S] (e.g. from moe_align_by_expert).
- *   Rows of y before offsets[0] and from offsets[E] on are zero. An entry
- *   outside [0, S] or below its predecessor sets MOE_STATUS_BAD_INDEX (groups
- *   are cut to [0, S]; the rows concerned are then undefined).
+ *   Rows of y before offsets[0] and from offsets[E] on are zero, and the same
+ *   rows of x are not looked at. An entry outside [0, S] or below its
+ *   predecessor sets MOE_STATUS_BAD_INDEX (groups are cut to [0, S]; the rows
+ *   concerned are then undefined); a call with S, K or N of 0 reads no offsets.
  *   ws / ws_bytes: at least moe_grouped_gemm_workspace_size(...) bytes (0 for
  *   16-bit K % 8 == 0 and for small float32 problems: then ws may be null).
  * S, K, N may have any size >= 0 (K = 0 gives zeros). 16-bit types run on the
- * tcgen05 tensor cores. float32 keeps float32's accuracy: on the CUDA cores, or
- * for large products on the tensor cores in three bf16 parts per value (all of
- * its bits; sums rounded to nearest every 128 terms; where rows of an expert or
- * weights of one with rows hold infinities, NaN or magnitudes of 2^44 and more,
- * the CUDA cores compute the call, decided on the device).
+ * tcgen05 tensor cores, whose float32 additions truncate: the sums before the
+ * rounding to dtype are below the exact ones by 5e-7 at 512 terms and 9e-6 at
+ * 8192 (2-norm, normal values). float32 keeps float32's accuracy: on the CUDA
+ * cores, or for large products on the tensor cores in three bf16 parts per value
+ * (all of its bits; sums rounded to nearest every 128 terms; where rows of an
+ * expert or weights of one with rows hold infinities, NaN or magnitudes of 2^44
+ * and more, the CUDA cores compute the call, decided on the device).
  */
 MOE_API size_t moe_grouped_gemm_workspace_size(int dtype, int S, int K, int N, int E);
 MOE_API int moe_grouped_gemm(const void* x, const void* w, int dtype, int S, int K, int N, int E,
@@ -355,6 +358,9 @@ MOE_API int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, in
  *   = silu(columns 0 .. N/2 - 1) * (columns N/2 .. N - 1), as w13 is laid out in
  *   moe_grouped_ffn (silu of arguments below -87 is 0). y is of out_dtype (any of
  *   the three), rounded once.
+ * The tensor cores' additions truncate where a sum needs more than 24 bits,
+ * which rows and weights with blocks of very different scales bring about; sums
+ * of 64 to 8192 products of normal values came out exact in float32.
  * offsets, rows without an expert and status as moe_grouped_gemm. A scale byte
  * of 255 makes its row's (or column's) sums NaN.
  * ws / ws_bytes: at least moe_mxfp4_grouped_gemm_workspace_size(...) bytes (the
@@ -422,9 +428,11 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
                            size_t ws_bytes, void* stream);
 
 /*
- * Bounded waits. Every wait of the tensor-core FFN kernels (forward
- * prefill and decode) on another role of the same kernel (a pipeline slot,
- * an accumulator buffer) gives up after `ns` nanoseconds of GPU global time:
+ * Bounded waits. Every wait of the tensor-core kernels (the FFN forward, the
+ * grouped products and their gradients, the 4-bit products; the FFN's backward
+ * has a fixed limit of its own) on
+ * another role of the same kernel (a pipeline slot, an accumulator buffer), and
+ * of the one-kernel decode FFN on its counters, gives up after `ns` nanoseconds of GPU global time:
  * the kernel then stops issuing work, lets the copies and MMAs it already
  * issued finish, frees its tensor memory, ORs MOE_STATUS_TIMEOUT into the
  * call's `status` word and returns, leaving the CUDA context usable (the

@@ -720,8 +720,8 @@ def moe_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, out=None, w
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Limit of the tensor-core FFN kernels' waits on their other roles (0: the default, 2 s);
-    returns the previous limit."""
+    """Limit of the waits of the tensor-core kernels (FFN, grouped and 4-bit products) on their other roles (0: the
+    default, 2 s); returns the previous limit."""
     return int(lib().moe_set_wait_limit_ns(int(ns)))
 
 

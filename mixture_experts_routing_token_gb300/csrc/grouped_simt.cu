@@ -1,6 +1,6 @@
 // Products grouped by expert in float32, on the CUDA cores: small sizes, few rows per expert, narrow
-// outputs, and operands that hold infinities or NaN (then launched behind the tensor-core kernel, with
-// the flags that it gives way to).
+// outputs, and operands that hold infinities, NaN or very large values (then launched behind the
+// tensor-core kernel, with the flags that it gives way to).
 //
 //   ROWS   y[p, n]    = sum_k x[p, k] w[e, n, k]     (rows p of expert e)
 //   GRADX  d_x[p, k]  = sum_n d_y[p, n] w[e, n, k]
@@ -12,8 +12,9 @@
 // registers on their way meanwhile, so a turn has one barrier and no exposed load. The multiply-adds
 // are issued in pairs (fma.f32x2, two columns), which leaves issue slots for everything else. Products
 // and sums are float32 in ascending order of the reduction index, so results do not depend on the
-// launch. Bound by shared memory and the FMA pipes (45 TFLOP/s at 8000 rows of [2048, 1024]), with
-// few rows by the weights.
+// launch. Bound by shared memory and the FMA pipes (45 TFLOP/s at 8000 rows of [2048, 1024]). With few
+// rows by the issue and latency of the weights' loads, a word at a time and one turn ahead: 128 rows, 32
+// experts of [2048, 1024], 116 us for 268 MB, 2.3 TB/s.
 #include <algorithm>
 
 #include "grouped.cuh"

@@ -21,8 +21,11 @@
 //
 // Bound at prompt sizes: what an SM can take in. A step brings 33 KB (codes and scales) for about 490
 // cycles of products and takes 550, 60 bytes a cycle; with the copies left out the same code took
-// 224 us where it takes 252 (131072 rows, 64 experts of [2816, 2048] with the gate: 6.0 PFLOP/s).
-// Prefetches of the next steps' weights into L2 made it slower (282 us).
+// 224 us where it takes 252 (131072 rows, 64 experts of [2816, 2048] with the gate, on a cold GPU: 6.0
+// PFLOP/s; under the power cap of a long run 287 us, 5.3). Half of a step's bytes are x, loaded again for
+// every column tile. Prefetches of the next steps' weights into L2 made it slower (282 us).
+// With the gate and N / 2 not a multiple of 8 each lane stores its row value by value, and that sets the
+// pace: 1749 us at N / 2 = 1412, 248 at 1408.
 #include <algorithm>
 
 #include "grouped.cuh"

@@ -34,8 +34,8 @@
  *     caller word `status` (device int32, zeroed by the caller). Kernels never
  *     trap.
  *   - Index tensors are int32; T*k must be below 2^31.
- *   - dtype is MOE_F32 or MOE_BF16 (the grouped products and the 4-bit calls
- *     also take MOE_F16) for hidden, w13, w2, out (and the FFN's
+ *   - dtype is MOE_F32 or MOE_BF16 (the grouped products, the 4-bit and 8-bit
+ *     calls, and the calls on sorted rows also take MOE_F16) for hidden, w13, w2, out (and the FFN's
  *     intermediate activation). Router logits, routing weights and probs are
  *     float32.
  *   - Logits must be finite. Rows of `indices` must name distinct experts.
@@ -66,9 +66,9 @@ extern "C" {
 /* dtypes */
 #define MOE_F32 0
 #define MOE_BF16 1
-#define MOE_F16 2               /* moe_grouped_gemm*, moe_mxfp4_* only */
+#define MOE_F16 2               /* moe_grouped_gemm*, moe_mxfp4_*, moe_*fp8*, moe_gather_rows*, moe_ep_combine* only */
 
-/* activations of moe_mxfp4_grouped_gemm */
+/* activations of moe_mxfp4_grouped_gemm and moe_fp8_grouped_gemm */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_SILU_AND_MUL 1
 
@@ -373,6 +373,67 @@ MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scal
                                    int32_t* status, void* stream);
 
 /*
+ * 8-bit values (e4m3: 448 the largest) with a float32 scale per block: 128
+ * neighbouring values of a row (block_rows 1), or 128 x 128 values of a matrix
+ * (block_rows 128; blocks at the edges are smaller). With m the block's largest
+ * magnitude, in float32 with each step rounded once,
+ *   s = max(m / 448, 2^-126);  code = e4m3(v * (1 / s)) (nearest, ties to even,
+ *   above 448 to 448). A block with inf or NaN has the scale NaN and codes 0.
+ *   x [M, N, K] of dtype, K % 16 == 0; codes [M, N, K] bytes;
+ *   scales [M, N, ceil(K / 128)] or [M, ceil(N / 128), ceil(K / 128)] float32.
+ * moe_fp8_dequantize writes code value * s in float32, rounded to dtype.
+ */
+MOE_API int moe_fp8_quantize(const void* x, int dtype, int M, int N, int K, int block_rows, uint8_t* codes,
+                             float* scales, void* stream);
+MOE_API int moe_fp8_dequantize(const uint8_t* codes, const float* scales, int M, int N, int K, int block_rows,
+                               int dtype, void* out, void* stream);
+
+/*
+ * Addition of the residual and root-mean-square norm, ending in 8-bit rows.
+ *   h = x + residual, rounded to dtype (h = x without one);
+ *   n = h * (1 / sqrt(mean over the row of h^2 + eps)) * weight  in float32;
+ *   codes, scales: n as moe_fp8_quantize with block_rows 1.
+ *   x, residual [T, H], weight [H] of dtype, H % 16 == 0, eps >= 0;
+ *   codes [T, H] bytes, scales [T, ceil(H / 128)] float32;
+ *   residual_out [T, H] = h: given if and only if residual is; it may be the
+ *   residual itself or x;
+ *   normed_or_null [T, H] = n rounded to dtype (e.g. for the router); may be x
+ *   where residual_out is not.
+ */
+MOE_API int moe_rms_norm_fp8(const void* x, const void* residual_or_null, const void* weight, int dtype, int T, int H,
+                             float eps, uint8_t* codes, float* scales, void* residual_out_or_null,
+                             void* normed_or_null, void* stream);
+
+/*
+ * 8-bit rows into expert order: row sorted_token_ids[p] of codes [T, H] and
+ * scales [T, ceil(H / 128)] to row p of codes_sorted [S, H] and scales_sorted
+ * for p < offsets[E] (rows beyond are left as they are; an offsets[E] outside
+ * [0, S] is cut to it). H % 16 == 0. A token id outside [0, T) gives a row of
+ * zeros; it and such an offset set MOE_STATUS_BAD_INDEX.
+ */
+MOE_API int moe_fp8_gather_rows(const uint8_t* codes, const float* scales, const int32_t* sorted_token_ids,
+                                const int32_t* offsets, int T, int H, int E, int S, uint8_t* codes_sorted,
+                                float* scales_sorted, int32_t* status, void* stream);
+
+/*
+ * moe_grouped_gemm on such operands (K % 16 == 0):
+ *   x_codes [S, K], x_scales [S, ceil(K / 128)]; w_codes [E, N, K],
+ *   w_scales [E, ceil(N / 128), ceil(K / 128)] (any float32 scales);
+ *   y[p, n] = sum over blocks b of x_scales[p, b] w_scales[e, n / 128, b]
+ *             * (sum over the k in b of x w), sums in float32.
+ *   activation MOE_ACT_NONE: y [S, N]; MOE_ACT_SILU_AND_MUL (N / 2 a multiple
+ *   of 16, as the next product's K): y [S, N / 2] = silu(columns 0 .. N/2 - 1) *
+ *   (columns N/2 .. N - 1) (silu of arguments below -87 is 0). y is of out_dtype
+ *   (any of the three), rounded once.
+ * Within a block the tensor cores add with truncation; the blocks' sums are added
+ * rounded to nearest. offsets, rows without an expert and status as
+ * moe_grouped_gemm. No workspace.
+ */
+MOE_API int moe_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes,
+                                 const float* w_scales, int S, int K, int N, int E, const int32_t* offsets,
+                                 int activation, int out_dtype, void* y, int32_t* status, void* stream);
+
+/*
  * Expert-parallel exchange: G ranks, rank r owning the E_local = E / G
  * consecutive experts [r*E_local, (r+1)*E_local). [mgt]
  * _indices_to_multihot_kernel restricts a rank's routing map to its local
@@ -393,9 +454,8 @@ MOE_API int moe_mxfp4_grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scal
 /*
  * x_sorted[p] = hidden[sorted_token_ids[p]] for p < offsets[E] (rows beyond are
  * left as they are). hidden [T, H] dtype; sorted_token_ids [T*k] and offsets
- * [E+1] from moe_align_by_expert; x_sorted [T*k, H] dtype. Rows must be a
- * multiple of 16 bytes (H % 8 == 0 for bf16, H % 4 for float32), else
- * MOE_ERR_UNSUPPORTED.
+ * [E+1] from moe_align_by_expert; x_sorted [T*k, H] dtype (any of the three).
+ * Rows of any width; those that are a multiple of 16 bytes are the faster ones.
  */
 MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids, const int32_t* offsets,
                             int dtype, int T, int H, int E, int k, void* x_sorted, void* stream);
@@ -419,8 +479,8 @@ MOE_API int moe_ep_receive_index(const int32_t* recv_counts, int G, int E_local,
  * expert output of sorted row p (its first offsets[E] rows are used);
  *   out[t] = sum_{j<k} topk_weights[t, j] * y_sorted[pos(t*k + j)]
  * where pos inverts reverse_indices (slots the align step dropped add
- * nothing); float32 accumulation in j order, one rounding to dtype. Rows must
- * be a multiple of 16 bytes. ws / ws_bytes: moe_ep_combine_workspace_size(T, k).
+ * nothing); float32 accumulation in j order, one rounding to dtype (any of the
+ * three). Rows of any width. ws / ws_bytes: moe_ep_combine_workspace_size(T, k).
  */
 MOE_API size_t moe_ep_combine_workspace_size(int T, int k);
 MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, const int32_t* reverse_indices,
@@ -428,8 +488,35 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
                            size_t ws_bytes, void* stream);
 
 /*
+ * Gradient of moe_gather_rows for the gradient d_x_sorted [T*k, H] of x_sorted:
+ *   d_hidden[t] = sum_{j<k} d_x_sorted[pos(t*k + j)]              [T, H]
+ * and of moe_ep_combine for the gradient d_out [T, H] of out:
+ *   d_y[pos(t*k + j)] = topk_weights[t, j] * d_out[t]             [T*k, H]
+ *   d_weights[t, j]   = <d_out[t], y_sorted[pos(t*k + j)]>        [T, k] float32
+ * dtype any of the three, rows of any width; sums in float32 (j ascending), one
+ * rounding. Slots that the align step dropped add nothing to d_hidden and have
+ * d_weights 0; rows of d_y from offsets[E] on are left as they are. Either of
+ * d_y and d_weights may be null (it is then not computed; y_sorted is read only
+ * for d_weights and may be null without). reverse_indices name distinct slots, as
+ * moe_align_by_expert writes them; an entry outside [0, T*k) or an offsets[E]
+ * outside it sets MOE_STATUS_BAD_INDEX (the results of the slots concerned are
+ * undefined). No atomics on the outputs: equal calls give equal bits.
+ * ws / ws_bytes: at least the matching *_workspace_size(T, k) bytes (0 for small
+ * calls: then ws may be null).
+ */
+MOE_API size_t moe_gather_rows_backward_workspace_size(int T, int k);
+MOE_API int moe_gather_rows_backward(const void* d_x_sorted, const int32_t* reverse_indices, const int32_t* offsets,
+                                     int dtype, int T, int H, int E, int k, void* d_hidden, void* ws, size_t ws_bytes,
+                                     int32_t* status, void* stream);
+MOE_API size_t moe_ep_combine_backward_workspace_size(int T, int k);
+MOE_API int moe_ep_combine_backward(const void* d_out, const void* y_sorted, const float* topk_weights,
+                                    const int32_t* reverse_indices, const int32_t* offsets, int dtype, int T, int k,
+                                    int H, int E, void* d_y_or_null, float* d_weights_or_null, void* ws,
+                                    size_t ws_bytes, int32_t* status, void* stream);
+
+/*
  * Bounded waits. Every wait of the tensor-core kernels (the FFN forward, the
- * grouped products and their gradients, the 4-bit products; the FFN's backward
+ * grouped products and their gradients, the 4-bit and 8-bit products; the FFN's backward
  * has a fixed limit of its own) on
  * another role of the same kernel (a pipeline slot, an accumulator buffer), and
  * of the one-kernel decode FFN on its counters, gives up after `ns` nanoseconds of GPU global time:

@@ -5,9 +5,11 @@ The compute lives in ``libmoe_gb300.so`` (hand-written CUDA for sm_103a behind
 the C ABI of ``include/moe.h``); this package is its thin Python binding with
 the same entry-point names. Build the library with :func:`build`.
 ``expert_parallel`` runs the layer with its experts split over the ranks of a
-process group (one GPU each); ``mxfp4_layer`` holds the experts' weights in 4 bits.
-Products of rows grouped by expert, their gradients and the 4-bit calls also stand
-by themselves (``moe_grouped_gemm``, ``moe_grouped_gemm_backward``, ``moe_mxfp4_*``).
+process group (one GPU each); ``mxfp4_layer`` holds the experts' weights in 4 bits,
+``fp8_layer`` in 8. Products of rows grouped by expert, their gradients, the 4-bit and
+the 8-bit calls also stand by themselves (``moe_grouped_gemm``,
+``moe_grouped_gemm_backward``, ``moe_mxfp4_*``, ``moe_fp8_*``, ``moe_rms_norm_fp8``), and so
+do the steps around them with their gradients (``moe_gather_rows``, ``moe_ep_combine``).
 """
 from ._binding import (  # noqa: F401
     MOE_ACT_NONE, MOE_ACT_SILU_AND_MUL, MOE_BF16, MOE_F16, MOE_F32, MOE_GROUP_TOPK_GREEDY, MOE_GROUP_TOPK_NOAUX_TC, MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_STATUS_BAD_INDEX, MOE_STATUS_TIMEOUT,
@@ -21,6 +23,9 @@ from ._binding import (  # noqa: F401
     moe_mxfp4_grouped_gemm_workspace_size, moe_mxfp4_quantize,
     moe_mxfp4_quantize_workspace_size,
     moe_gather_rows, moe_ep_receive_index, moe_ep_combine,
+    moe_gather_rows_backward, moe_gather_rows_backward_workspace_size, moe_ep_combine_backward,
+    moe_ep_combine_backward_workspace_size,
+    moe_fp8_dequantize, moe_fp8_gather_rows, moe_fp8_grouped_gemm, moe_fp8_quantize, moe_rms_norm_fp8,
     profiler_enable, profiler_report, set_wait_limit_ns, version,
 )
 

@@ -59,6 +59,15 @@ SIGNATURES = {
     "moe_ep_receive_index": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _sz, _p]),
     "moe_ep_combine_workspace_size": (_sz, [_i, _i]),
     "moe_ep_combine": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "moe_gather_rows_backward_workspace_size": (_sz, [_i, _i]),
+    "moe_gather_rows_backward": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _sz, _p, _p]),
+    "moe_ep_combine_backward_workspace_size": (_sz, [_i, _i]),
+    "moe_ep_combine_backward": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _sz, _p, _p]),
+    "moe_fp8_quantize": (_i, [_p, _i, _i, _i, _i, _i, _p, _p, _p]),
+    "moe_fp8_dequantize": (_i, [_p, _p, _i, _i, _i, _i, _i, _p, _p]),
+    "moe_rms_norm_fp8": (_i, [_p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _p]),
+    "moe_fp8_gather_rows": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p]),
+    "moe_fp8_grouped_gemm": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _p, _p]),
     "moe_set_wait_limit_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
     "moe_profiler_enable": (_i, [_i]),
     "moe_profiler_report": (_i, [ctypes.c_char_p, _sz]),
@@ -672,7 +681,7 @@ def moe_mxfp4_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activa
 def moe_gather_rows(hidden, sorted_token_ids, offsets, k, out=None, stream=None):
     """Expert-sorted copy of the routed token rows -> x_sorted [T*k, H] (rows p < offsets[E])."""
     _dev(hidden, "hidden")
-    dt = _dtype_code(hidden)
+    dt = _code(hidden.dtype)
     T, H = hidden.shape
     E = offsets.numel() - 1
     d = hidden.device
@@ -704,7 +713,7 @@ def moe_ep_receive_index(recv_counts, R, local_counts=None, local_offsets=None, 
 def moe_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, out=None, workspace=None, stream=None):
     """Sender side after the return exchange: out[t] = sum_j w[t,j] * y_sorted[pos(t, j)] -> [T, H]."""
     _dev(y_sorted, "y_sorted")
-    dt = _dtype_code(y_sorted)
+    dt = _code(y_sorted.dtype)
     T, k = topk_weights.shape
     H = y_sorted.shape[1]
     E = offsets.numel() - 1
@@ -719,8 +728,223 @@ def moe_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, out=None, w
     return out
 
 
+@_sizes
+def moe_gather_rows_backward_workspace_size(T, k) -> int:
+    _fits(T, k)
+    return int(lib().moe_gather_rows_backward_workspace_size(T, k))
+
+
+def moe_gather_rows_backward(d_x_sorted, reverse_indices, offsets, k, d_hidden=None, workspace=None, status=None, stream=None):
+    """Gradient of :func:`moe_gather_rows`: d_hidden[t] = sum_j d_x_sorted[pos(t, j)] -> [T, H] in d_x_sorted's dtype.
+
+    ``d_x_sorted [T*k, H]`` (float32, bf16 or float16), ``reverse_indices [T*k]`` and ``offsets [E+1]`` from
+    :func:`moe_align_by_expert`. Slots without an expert add nothing."""
+    xp, dtype, d = _first(d_x_sorted, "d_x_sorted")
+    rp = _take(reverse_indices, "reverse_indices", _I32, d)
+    op = _take(offsets, "offsets", _I32, d)
+    dt = _code(dtype)
+    xs, k = d_x_sorted.shape, int(k)
+    if len(xs) != 2 or k < 1 or xs[0] % k or reverse_indices.shape != xs[:1] or len(offsets.shape) != 1 or offsets.shape[0] < 2:
+        raise ValueError("shapes must be d_x_sorted [T * k, H], reverse_indices [T * k], offsets [E + 1]")
+    T, H, E = xs[0] // k, xs[1], offsets.shape[0] - 1
+    _fits(xs[0], H, E)
+    d_hidden, hp = _give(d_hidden, "d_hidden", (T, H), dtype, d, stream)
+    space, ws, nb = _space(workspace, moe_gather_rows_backward_workspace_size(T, k), d, stream)
+    rc = lib().moe_gather_rows_backward(xp, rp, op, dt, T, H, E, k, hp, ws, nb, _status_ptr(status, d), _raw(stream, d))
+    if rc:
+        _check("moe_gather_rows_backward", rc)
+    return d_hidden
+
+
+@_sizes
+def moe_ep_combine_backward_workspace_size(T, k) -> int:
+    _fits(T, k)
+    return int(lib().moe_ep_combine_backward_workspace_size(T, k))
+
+
+def moe_ep_combine_backward(d_out, y_sorted, topk_weights, reverse_indices, offsets, d_y=None, d_weights=None, workspace=None,
+                            status=None, stream=None, want_d_y=True, want_d_weights=True):
+    """Gradients of :func:`moe_ep_combine` for ``d_out [T, H]`` -> (d_y [T*k, H] in d_out's dtype, d_weights [T, k] float32).
+
+    One that is not wanted is None (``y_sorted`` is read for ``d_weights`` only and may be None without). Slots without
+    an expert have ``d_weights`` 0; rows of ``d_y`` behind the last expert's are left as they are."""
+    gp, dtype, d = _first(d_out, "d_out")
+    yp = _take(y_sorted, "y_sorted", dtype, d) if y_sorted is not None or want_d_weights else None
+    wp = _take(topk_weights, "topk_weights", torch.float32, d)
+    rp = _take(reverse_indices, "reverse_indices", _I32, d)
+    op = _take(offsets, "offsets", _I32, d)
+    dt = _code(dtype)
+    gs, ws_ = d_out.shape, topk_weights.shape
+    if (len(gs) != 2 or len(ws_) != 2 or ws_[0] != gs[0] or reverse_indices.shape != (ws_[0] * ws_[1],) or len(offsets.shape) != 1
+            or offsets.shape[0] < 2 or (y_sorted is not None and y_sorted.shape != (ws_[0] * ws_[1], gs[1]))):
+        raise ValueError("shapes must be d_out [T, H], y_sorted [T * k, H], topk_weights [T, k], reverse_indices [T * k], "
+                         "offsets [E + 1]")
+    (T, H), k, E = gs, ws_[1], offsets.shape[0] - 1
+    _fits(T * k, H, E)
+    d_y, dyp = _give(d_y, "d_y", (T * k, H), dtype, d, stream) if want_d_y else (None, None)
+    d_weights, dwp = _give(d_weights, "d_weights", (T, k), torch.float32, d, stream) if want_d_weights else (None, None)
+    space, ws, nb = _space(workspace, moe_ep_combine_backward_workspace_size(T, k), d, stream)
+    rc = lib().moe_ep_combine_backward(gp, yp, wp, rp, op, dt, T, k, H, E, dyp, dwp, ws, nb, _status_ptr(status, d), _raw(stream, d))
+    if rc:
+        _check("moe_ep_combine_backward", rc)
+    return d_y, d_weights
+
+
+_F8 = torch.float8_e4m3fn
+_F32 = torch.float32
+FP8_BLOCK = 128
+
+
+def _pieces(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _fp8_shape(shape, block_rows, name):
+    """(matrices, rows, columns, shape of the scales) of values [..., K], or of matrices [..., N, K] with 128 x 128 blocks."""
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK} (got {block_rows})")
+    if len(shape) < (1 if block_rows == 1 else 2) or shape[-1] % 16:
+        raise ValueError(f"{name} must be [..., K] ([..., N, K] with block_rows {FP8_BLOCK}) with K a multiple of 16")
+    K = shape[-1]
+    if block_rows == 1:
+        M, N, scales = 1, shape[:-1].numel(), (*shape[:-1], _pieces(K))
+    else:
+        M, N = shape[:-2].numel(), shape[-2]
+        scales = (*shape[:-2], _pieces(N), _pieces(K))
+    _fits(M, N, K, M * N)
+    return M, N, K, scales
+
+
+def moe_fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
+    """8-bit values of ``x`` with a float32 scale per block -> (codes float8_e4m3fn as x, scales).
+
+    ``block_rows=1``: ``x [..., K]`` and a scale for each 128 values of a row, ``scales [..., ceil(K/128)]`` (activations).
+    ``block_rows=128``: ``x [..., N, K]`` and a scale for 128 x 128 values, ``[..., ceil(N/128), ceil(K/128)]`` (weights).
+    K must be a multiple of 16."""
+    xp, dtype, d = _first(x, "x")
+    dt = _code(dtype)
+    M, N, K, ss = _fp8_shape(x.shape, block_rows, "x")
+    codes, cp = _give(codes, "codes", x.shape, _F8, d, stream)
+    scales, sp = _give(scales, "scales", ss, _F32, d, stream)
+    rc = lib().moe_fp8_quantize(xp, dt, M, N, K, block_rows, cp, sp, _raw(stream, d))
+    if rc:
+        _check("moe_fp8_quantize", rc)
+    return codes, scales
+
+
+def moe_fp8_dequantize(codes, scales, dtype=torch.bfloat16, block_rows=1, out=None, stream=None):
+    """The values that ``codes`` and ``scales`` of :func:`moe_fp8_quantize` stand for, in ``dtype``."""
+    cp, _, d = _first(codes, "codes")
+    if codes.dtype is not _F8:
+        _refuse(codes, "codes", _F8, d)
+    sp = _take(scales, "scales", _F32, d)
+    dt = _code(dtype)
+    M, N, K, ss = _fp8_shape(codes.shape, block_rows, "codes")
+    if scales.shape != ss:
+        raise ValueError(f"scales must have shape {tuple(ss)}")
+    out, op = _give(out, "out", codes.shape, dtype, d, stream)
+    rc = lib().moe_fp8_dequantize(cp, sp, M, N, K, block_rows, dt, op, _raw(stream, d))
+    if rc:
+        _check("moe_fp8_dequantize", rc)
+    return out
+
+
+def moe_rms_norm_fp8(x, weight, residual=None, eps=1e-6, want_normed=False, codes=None, scales=None, residual_out=None, normed=None,
+                     stream=None):
+    """Addition of the residual and root-mean-square norm, as 8-bit rows -> (codes, scales, residual_out, normed).
+
+    h = x + residual (rounded to x's dtype); n = h / sqrt(mean h^2 + eps) * weight in float32; ``codes`` and ``scales``
+    hold n as :func:`moe_fp8_quantize` does, ``residual_out`` h (None without a residual; pass the residual itself to
+    update it in place), ``normed`` n in x's dtype (None unless wanted or given). ``x``, ``residual [..., H]``,
+    ``weight [H]`` of one dtype, H a multiple of 16."""
+    xp, dtype, d = _first(x, "x")
+    wp = _take(weight, "weight", dtype, d)
+    rp = None if residual is None else _take(residual, "residual", dtype, d)
+    dt = _code(dtype)
+    xs = x.shape
+    _, T, H, ss = _fp8_shape(xs, 1, "x")
+    if weight.shape != (H,) or (residual is not None and residual.shape != xs):
+        raise ValueError("shapes must be x [..., H], weight [H], residual as x")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    codes, cp = _give(codes, "codes", xs, _F8, d, stream)
+    scales, sp = _give(scales, "scales", ss, _F32, d, stream)
+    residual_out, op = (None, None) if residual is None else _give(residual_out, "residual_out", xs, dtype, d, stream)
+    normed, np_ = _give(normed, "normed", xs, dtype, d, stream) if want_normed or normed is not None else (None, None)
+    rc = lib().moe_rms_norm_fp8(xp, rp, wp, dt, T, H, eps, cp, sp, op, np_, _raw(stream, d))
+    if rc:
+        _check("moe_rms_norm_fp8", rc)
+    return codes, scales, residual_out, normed
+
+
+def moe_fp8_gather_rows(codes, scales, sorted_token_ids, offsets, out=None, out_scales=None, status=None, stream=None):
+    """Expert-sorted copies of 8-bit rows -> (codes [S, H], scales [S, ceil(H/128)]), rows p < offsets[E].
+
+    ``codes [T, H]``, ``scales [T, ceil(H/128)]``; ``sorted_token_ids [S]`` and ``offsets [E+1]`` from
+    :func:`moe_align_by_expert`. Rows behind the last expert's are left as they are."""
+    cp, dtype, d = _first(codes, "codes")
+    if dtype is not _F8:
+        _refuse(codes, "codes", _F8, d)
+    sp = _take(scales, "scales", _F32, d)
+    ip = _take(sorted_token_ids, "sorted_token_ids", _I32, d)
+    op = _take(offsets, "offsets", _I32, d)
+    cs, ids = codes.shape, sorted_token_ids.shape
+    if len(cs) != 2 or cs[1] % 16 or scales.shape != (cs[0], _pieces(cs[1])) or len(ids) != 1 or len(offsets.shape) != 1 \
+            or offsets.shape[0] < 2:
+        raise ValueError("shapes must be codes [T, H], scales [T, ceil(H / 128)], sorted_token_ids [S], offsets [E + 1] with H a "
+                         "multiple of 16")
+    (T, H), S, E = cs, ids[0], offsets.shape[0] - 1
+    _fits(T, H, S, E)
+    out, xp = _give(out, "out", (S, H), _F8, d, stream)
+    out_scales, xsp = _give(out_scales, "out_scales", (S, _pieces(H)), _F32, d, stream)
+    rc = lib().moe_fp8_gather_rows(cp, sp, ip, op, T, H, E, S, xp, xsp, _status_ptr(status, d), _raw(stream, d))
+    if rc:
+        _check("moe_fp8_gather_rows", rc)
+    return out, out_scales
+
+
+def moe_fp8_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activation=None, out_dtype=torch.bfloat16, out=None,
+                         status=None, stream=None):
+    """:func:`moe_grouped_gemm` on 8-bit operands -> y [S, N] of ``out_dtype``.
+
+    ``x_codes [S, K]`` with ``x_scales [S, ceil(K/128)]``, ``w_codes [E, N, K]`` with
+    ``w_scales [E, ceil(N/128), ceil(K/128)]`` as :func:`moe_fp8_quantize` makes them (``block_rows`` 1 and 128), K a
+    multiple of 16. ``activation="silu_and_mul"`` returns [S, N/2]: silu of the first half of the columns times the
+    second half (N a multiple of 32)."""
+    xp, dtype, d = _first(x_codes, "x_codes")
+    if dtype is not _F8:
+        _refuse(x_codes, "x_codes", _F8, d)
+    xsp = _take(x_scales, "x_scales", _F32, d)
+    wp = _take(w_codes, "w_codes", _F8, d)
+    wsp = _take(w_scales, "w_scales", _F32, d)
+    op = _take(offsets, "offsets", _I32, d)
+    dt = _code(out_dtype)
+    xs, wsh = x_codes.shape, w_codes.shape
+    if len(xs) != 2 or len(wsh) != 3:
+        raise ValueError("shapes must be x_codes [S, K], w_codes [E, N, K]")
+    S, K = xs
+    E, N, same = wsh
+    if (same != K or K % 16 or x_scales.shape != (S, _pieces(K)) or w_scales.shape != (E, _pieces(N), _pieces(K))
+            or offsets.shape != (E + 1,)):
+        raise ValueError("shapes must be x_codes [S, K], x_scales [S, ceil(K / 128)], w_codes [E, N, K], "
+                         "w_scales [E, ceil(N / 128), ceil(K / 128)], offsets [E + 1] with K a multiple of 16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+    cols, act = N, _ACTIVATIONS[activation]
+    if act:
+        if N % 32:
+            raise ValueError("silu_and_mul needs N to be a multiple of 32")
+        cols = N // 2
+    _fits(S, K, N, E)
+    out, yp = _give(out, "out", (S, cols), out_dtype, d, stream)
+    rc = lib().moe_fp8_grouped_gemm(xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, _status_ptr(status, d), _raw(stream, d))
+    if rc:
+        _check("moe_fp8_grouped_gemm", rc)
+    return out
+
+
 def set_wait_limit_ns(ns: int) -> int:
-    """Limit of the waits of the tensor-core kernels (FFN, grouped and 4-bit products) on their other roles (0: the
+    """Limit of the waits of the tensor-core kernels (FFN, grouped, 4-bit and 8-bit products) on their other roles (0: the
     default, 2 s); returns the previous limit."""
     return int(lib().moe_set_wait_limit_ns(int(ns)))
 

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "fp8.cuh"
 
 namespace moe {
 
@@ -788,7 +789,7 @@ MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids,
   g_err[0] = 0;
   int rc;
   if ((rc = check_routing_dims(T, E, k))) return rc;
-  REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16, "dtype must be MOE_F32 or MOE_BF16 (got %d)", dtype);
+  if ((rc = check_any_dtype(dtype))) return rc;
   REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
   const long S = (long)T * k;
   if ((rc = check_tensor(hidden, (long)T * H, "hidden"))) return rc;
@@ -796,6 +797,8 @@ MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids,
   if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
   if ((rc = check_tensor(x_sorted, S * H, "x_sorted"))) return rc;
   if (S == 0) return MOE_OK;
+  if ((long)H * (long)dsize(dtype) % 16 != 0 || (long)H * (long)dsize(dtype) >= 1L << 31)
+    return launch_gather_any_rows(hidden, sorted_token_ids, offsets, (int)dsize(dtype), T, H, E, (int)S, x_sorted, (cudaStream_t)stream);
   return launch_gather_rows(hidden, sorted_token_ids, offsets, E, H * (int)dsize(dtype), x_sorted, nullptr,
                             (cudaStream_t)stream);
 }
@@ -833,7 +836,7 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
   g_err[0] = 0;
   int rc;
   if ((rc = check_routing_dims(T, E, k))) return rc;
-  REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16, "dtype must be MOE_F32 or MOE_BF16 (got %d)", dtype);
+  if ((rc = check_any_dtype(dtype))) return rc;
   REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
   const long S = (long)T * k;
   if ((rc = check_tensor(y_sorted, S * H, "y_sorted"))) return rc;
@@ -843,8 +846,183 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
   if ((rc = check_tensor(out, (long)T * H, "out"))) return rc;
   if ((rc = check_ws(ws, ws_bytes, (size_t)S * sizeof(int32_t)))) return rc;
   if (S == 0) return MOE_OK;
+  if (dtype == MOE_F16 || (long)H * (long)dsize(dtype) % 16 != 0)
+    return launch_sum_sorted_rows(SortedRows{reverse_indices, offsets, dtype, T, k, E, H, ws, nullptr}, topk_weights, y_sorted, out,
+                                  "ep_combine", (cudaStream_t)stream);
   return launch_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, dtype, T, k, H, E, out,
                            static_cast<int32_t*>(ws), (cudaStream_t)stream);
+}
+
+MOE_API size_t moe_gather_rows_backward_workspace_size(int T, int k) {
+  if (T < 0 || k < 1) return 0;
+  return sorted_rows_workspace(T, k);
+}
+
+MOE_API int moe_gather_rows_backward(const void* d_x_sorted, const int32_t* reverse_indices, const int32_t* offsets, int dtype,
+                                     int T, int H, int E, int k, void* d_hidden, void* ws, size_t ws_bytes, int32_t* status,
+                                     void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_routing_dims(T, E, k))) return rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
+  const long S = (long)T * k;
+  if ((rc = check_tensor(d_x_sorted, S * H, "d_x_sorted"))) return rc;
+  if ((rc = check_tensor(reverse_indices, S, "reverse_indices"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if ((rc = check_tensor(d_hidden, (long)T * H, "d_hidden"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_gather_rows_backward_workspace_size(T, k)))) return rc;
+  if (S == 0) return MOE_OK;
+  return launch_sum_sorted_rows(SortedRows{reverse_indices, offsets, dtype, T, k, E, H, ws, status}, nullptr, d_x_sorted, d_hidden,
+                                "gather_rows_backward", (cudaStream_t)stream);
+}
+
+MOE_API size_t moe_ep_combine_backward_workspace_size(int T, int k) {
+  if (T < 0 || k < 1) return 0;
+  return sorted_rows_workspace(T, k);
+}
+
+MOE_API int moe_ep_combine_backward(const void* d_out, const void* y_sorted, const float* topk_weights,
+                                    const int32_t* reverse_indices, const int32_t* offsets, int dtype, int T, int k, int H, int E,
+                                    void* d_y_or_null, float* d_weights_or_null, void* ws, size_t ws_bytes, int32_t* status,
+                                    void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_routing_dims(T, E, k))) return rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
+  const long S = (long)T * k;
+  if ((rc = check_tensor(d_out, (long)T * H, "d_out"))) return rc;
+  if (d_weights_or_null && (rc = check_tensor(y_sorted, S * H, "y_sorted"))) return rc;
+  if ((rc = check_tensor(topk_weights, S, "topk_weights"))) return rc;
+  if ((rc = check_tensor(reverse_indices, S, "reverse_indices"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if (d_y_or_null && (rc = check_tensor(d_y_or_null, S * H, "d_y"))) return rc;
+  if (d_weights_or_null && (rc = check_tensor(d_weights_or_null, S, "d_weights"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_ep_combine_backward_workspace_size(T, k)))) return rc;
+  if (S == 0 || (!d_y_or_null && !d_weights_or_null)) return MOE_OK;
+  return launch_sum_sorted_rows_backward(SortedRows{reverse_indices, offsets, dtype, T, k, E, H, ws, status}, topk_weights, d_out,
+                                         y_sorted, d_y_or_null, d_weights_or_null, (cudaStream_t)stream);
+}
+
+namespace moe {
+namespace {
+
+int check_fp8_dims(int M, int N, int K, int block_rows) {
+  REQUIRE(M >= 0 && N >= 0, "M and N must be >= 0 (got M=%d, N=%d)", M, N);
+  REQUIRE(K >= 0 && K % 16 == 0, "K must be a multiple of 16 (got %d)", K);
+  REQUIRE(block_rows == 1 || block_rows == fp8::BLOCK, "block_rows must be 1 or %d (got %d)", fp8::BLOCK, block_rows);
+  REQUIRE((long)M * N < 1L << 31, "M * N must be below 2^31 (got M=%d, N=%d)", M, N);
+  REQUIRE(K <= (1L << 31) - 1024 && N <= (1L << 31) - 1024, "N and K must be at most 2^31 - 1024");
+  if (block_rows > 1)
+    REQUIRE((double)M * fp8::blocks(N) * fp8::blocks(K) < 2147483648.0, "M=%d, N=%d, K=%d are too large together", M, N, K);
+  return MOE_OK;
+}
+
+long fp8_scale_count(int M, int N, int K, int block_rows) {
+  return (long)M * (block_rows > 1 ? fp8::blocks(N) : N) * fp8::blocks(K);
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API int moe_fp8_quantize(const void* x, int dtype, int M, int N, int K, int block_rows, uint8_t* codes, float* scales,
+                             void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  if ((rc = check_fp8_dims(M, N, K, block_rows))) return rc;
+  const long count = (long)M * N * K;
+  if ((rc = check_tensor(x, count, "x"))) return rc;
+  if ((rc = check_tensor(codes, count, "codes"))) return rc;
+  if ((rc = check_tensor(scales, fp8_scale_count(M, N, K, block_rows), "scales"))) return rc;
+  if (count == 0) return MOE_OK;
+  return launch_fp8_quantize(x, dtype, M, N, K, block_rows > 1, codes, scales, (cudaStream_t)stream);
+}
+
+MOE_API int moe_fp8_dequantize(const uint8_t* codes, const float* scales, int M, int N, int K, int block_rows, int dtype, void* out,
+                               void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  if ((rc = check_fp8_dims(M, N, K, block_rows))) return rc;
+  const long count = (long)M * N * K;
+  if ((rc = check_tensor(codes, count, "codes"))) return rc;
+  if ((rc = check_tensor(scales, fp8_scale_count(M, N, K, block_rows), "scales"))) return rc;
+  if ((rc = check_tensor(out, count, "out"))) return rc;
+  if (count == 0) return MOE_OK;
+  return launch_fp8_dequantize(codes, scales, M, N, K, block_rows > 1, dtype, out, (cudaStream_t)stream);
+}
+
+MOE_API int moe_rms_norm_fp8(const void* x, const void* residual_or_null, const void* weight, int dtype, int T, int H, float eps,
+                             uint8_t* codes, float* scales, void* residual_out_or_null, void* normed_or_null, void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(dtype))) return rc;
+  REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
+  REQUIRE(H >= 0 && H % 16 == 0, "H must be a multiple of 16 (got %d)", H);
+  REQUIRE(H <= (1L << 31) - 4096, "H must be at most 2^31 - 4096");
+  REQUIRE(eps >= 0.0f, "eps must be >= 0");
+  REQUIRE((residual_or_null == nullptr) == (residual_out_or_null == nullptr) || (long)T * H == 0,
+          "residual and residual_out come together");
+  const long count = (long)T * H;
+  if ((rc = check_tensor(x, count, "x"))) return rc;
+  if ((rc = check_tensor(weight, count ? H : 0, "weight"))) return rc;
+  if (residual_or_null && (rc = check_tensor(residual_or_null, count, "residual"))) return rc;
+  if (residual_out_or_null && (rc = check_tensor(residual_out_or_null, count, "residual_out"))) return rc;
+  if (normed_or_null && (rc = check_tensor(normed_or_null, count, "normed"))) return rc;
+  if ((rc = check_tensor(codes, count, "codes"))) return rc;
+  if ((rc = check_tensor(scales, count, "scales"))) return rc;
+  if (count == 0) return MOE_OK;
+  return launch_rms_norm_fp8(x, residual_or_null, weight, dtype, T, H, eps, codes, scales, residual_out_or_null, normed_or_null,
+                             (cudaStream_t)stream);
+}
+
+MOE_API int moe_fp8_gather_rows(const uint8_t* codes, const float* scales, const int32_t* sorted_token_ids, const int32_t* offsets,
+                                int T, int H, int E, int S, uint8_t* codes_sorted, float* scales_sorted, int32_t* status,
+                                void* stream) {
+  g_err[0] = 0;
+  int rc;
+  REQUIRE(T >= 0 && S >= 0, "T and S must be >= 0 (got T=%d, S=%d)", T, S);
+  REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "E must be in [1, %d] (got %d)", MOE_MAX_EXPERTS, E);
+  REQUIRE(H >= 0 && H % 16 == 0, "H must be a multiple of 16 (got %d)", H);
+  REQUIRE(H <= (1L << 31) - 1024, "H must be at most 2^31 - 1024");
+  if ((rc = check_tensor(codes, (long)T * H, "codes"))) return rc;
+  if ((rc = check_tensor(scales, (long)T * H, "scales"))) return rc;
+  if ((rc = check_tensor(sorted_token_ids, S, "sorted_token_ids"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if ((rc = check_tensor(codes_sorted, (long)S * H, "codes_sorted"))) return rc;
+  if ((rc = check_tensor(scales_sorted, (long)S * H, "scales_sorted"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if (S == 0 || H == 0) return MOE_OK;
+  return launch_fp8_gather_rows(codes, scales, sorted_token_ids, offsets, T, H, E, S, codes_sorted, scales_sorted, status,
+                                (cudaStream_t)stream);
+}
+
+MOE_API int moe_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes, const float* w_scales, int S,
+                                 int K, int N, int E, const int32_t* offsets, int activation, int out_dtype, void* y,
+                                 int32_t* status, void* stream) {
+  g_err[0] = 0;
+  int rc;
+  if ((rc = check_any_dtype(out_dtype))) return rc;
+  if ((rc = check_grouped_dims(S, K, N, E))) return rc;
+  REQUIRE(K % 16 == 0, "K must be a multiple of 16 (got %d)", K);
+  REQUIRE(activation == MOE_ACT_NONE || activation == MOE_ACT_SILU_AND_MUL, "unknown activation %d", activation);
+  REQUIRE(activation == MOE_ACT_NONE || N % 32 == 0, "silu_and_mul needs N / 2 to be a multiple of 16 (got N=%d)", N);
+  if ((rc = check_tensor(x_codes, (long)S * K, "x_codes"))) return rc;
+  if ((rc = check_tensor(x_scales, (long)S * K, "x_scales"))) return rc;
+  if ((rc = check_tensor(w_codes, (long)E * N * K, "w_codes"))) return rc;
+  if ((rc = check_tensor(w_scales, (long)E * N * K, "w_scales"))) return rc;
+  if ((rc = check_tensor(offsets, E + 1, "offsets"))) return rc;
+  if ((rc = check_tensor(y, (long)S * N, "y"))) return rc;
+  if (status && (rc = check_tensor(status, 1, "status"))) return rc;
+  if (S == 0 || N == 0) return MOE_OK;
+  if (K == 0)
+    return zero_out(y, (size_t)S * (activation == MOE_ACT_NONE ? N : N / 2) * dsize(out_dtype), (cudaStream_t)stream);
+  Fp8Args a{x_codes, x_scales, w_codes, w_scales, S, K, N, E, offsets, activation == MOE_ACT_SILU_AND_MUL, out_dtype, y, status};
+  return launch_fp8_grouped(a, (cudaStream_t)stream);
 }
 
 MOE_API uint64_t moe_set_wait_limit_ns(uint64_t ns) {

@@ -274,6 +274,9 @@ inline bool grouped_few_rows(int S, int E) { return S <= (long)kFewRows * E; }
 // Few rows per expert (grouped_few.cu): x, w with rows of `cols` elements (a multiple of 8).
 int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s);
 
+// Columns per unit of the weight-streaming kernels, a multiple of 16 up to `most`, for `heads` groups of rows.
+int grouped_few_columns(long heads, int cols, int most);
+
 // 4-bit microscaled values (mxfp4.cu): codes [rows, K / 2], scales [rows, K / 32].
 size_t mxfp4_quantize_workspace(int T, int K, bool with_rows, int R);
 int launch_mxfp4_quantize(const void* x, int dtype, int T, int K, const int32_t* rows, int R, uint8_t* codes,
@@ -296,6 +299,46 @@ struct Mxfp4Args {
 size_t mxfp4_grouped_workspace(int S, int K, int N, int E, bool silu);
 int launch_mxfp4_few(const Mxfp4Args& a, cudaStream_t s);
 int launch_mxfp4_grouped(const Mxfp4Args& a, cudaStream_t s);
+
+// 8-bit values with a float32 scale per block (fp8.cu): codes [M, N, K]; scales [M, N, ceil(K / 128)], or with
+// `blocks` [M, ceil(N / 128), ceil(K / 128)].
+int launch_fp8_quantize(const void* x, int dtype, int M, int N, int K, bool blocks, uint8_t* codes, float* scales, cudaStream_t s);
+int launch_fp8_dequantize(const uint8_t* codes, const float* scales, int M, int N, int K, bool blocks, int dtype, void* out,
+                          cudaStream_t s);
+int launch_rms_norm_fp8(const void* x, const void* residual, const void* weight, int dtype, int T, int H, float eps, uint8_t* codes,
+                        float* scales, void* sum, void* normed, cudaStream_t s);
+int launch_fp8_gather_rows(const uint8_t* codes, const float* scales, const int32_t* ids, const int32_t* offsets, int T, int H, int E,
+                           int S, uint8_t* out, float* out_scales, int32_t* status, cudaStream_t s);
+struct Fp8Args {
+  const uint8_t* x;
+  const float* x_scales;
+  const uint8_t* w;
+  const float* w_scales;
+  int S, K, N, E;
+  const int32_t* offsets;
+  int silu;          // y = silu(gate half) * up half: [S, N / 2]
+  int out_dtype;
+  void* y;
+  int32_t* status;
+};
+int launch_fp8_few(const Fp8Args& a, cudaStream_t s);
+int launch_fp8_grouped(const Fp8Args& a, cudaStream_t s);
+
+// Sums over a token's sorted rows and their gradients (sorted_rows.cu), rows of any width; ws: sorted_rows_workspace bytes.
+struct SortedRows {
+  const int32_t* reverse;
+  const int32_t* offsets;
+  int dtype, T, k, E, H;
+  void* ws;
+  int32_t* status;
+};
+size_t sorted_rows_workspace(int T, int k);
+// out[t] = sum_j weights[t, j] src[pos(t, j)]; null weights: 1
+int launch_sum_sorted_rows(const SortedRows& r, const float* weights, const void* src, void* out, const char* name, cudaStream_t s);
+int launch_sum_sorted_rows_backward(const SortedRows& r, const float* weights, const void* d_out, const void* y, void* d_y,
+                                    float* d_weights, cudaStream_t s);
+int launch_gather_any_rows(const void* src, const int32_t* ids, const int32_t* offsets, int elem_bytes, int T, int H, int E, int S,
+                           void* out, cudaStream_t s);
 
 // Launch with programmatic stream serialization (PDL): the kernel may start while
 // the previous kernel on the stream is still running; it must execute

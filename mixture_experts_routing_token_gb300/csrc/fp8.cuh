@@ -1,0 +1,80 @@
+// 8-bit values (e4m3: four bits of exponent, three of mantissa, no infinities, 448 the largest) with a
+// float32 scale per block, and the tensor-core product of two of them.
+#pragma once
+#include "common.cuh"
+
+namespace moe {
+namespace fp8 {
+
+constexpr int BLOCK = 128;       // values along a row (and rows of a weight matrix) that share a scale
+
+__host__ __device__ constexpr int blocks(int n) { return (n + BLOCK - 1) / BLOCK; }
+
+// Four float32 values to four codes, the first one low (nearest, ties to even, above 448 to 448).
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Four codes to the values they stand for before scaling (every one is exact in float16).
+__device__ __forceinline__ float4 decode4(uint32_t codes) {
+  uint32_t l, h;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(l), "=r"(h)
+      : "r"(codes));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&l)), y = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// Instruction descriptor, kind::f8f6f4: D float32, A and B e4m3 (format 0), both K-major, M x N.
+__host__ __device__ constexpr uint32_t idesc(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T over K = 32.
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two float32 multiply-adds in one instruction: acc += v * s, two sums and two values to a register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
+  asm("{\n\t.reg .b64 v;\n\t"
+      "mov.b64 v, {%1, %2};\n\t"
+      "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(v0), "r"(v1), "l"(s));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& a, uint32_t& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+
+}  // namespace fp8
+}  // namespace moe

@@ -1,0 +1,345 @@
+// Products of 8-bit rows grouped by expert on SM pairs (tcgen05.mma.cta_group::2, kind::f8f6f4, M = 256 x N = 256 x
+// K = 32, float32 accumulators in TMEM), with a scale for every 128 values of a row and 128 x 128 of a matrix:
+//
+//   y[p, n] = sum over blocks b of sx[p, b] sw[e, n / 128, b] sum over k in b of cx[p, k] cw[e, n, k]
+//   (with the gate, silu(y[p, n]) y[p, N/2 + n])
+//
+// The scales are any float32, so the tensor cores cannot apply them. An accumulator holds one block (K = 128, four
+// MMAs); the epilogue warps read it, multiply by sx sw and add in registers (two sums an instruction), while the
+// next block goes into the other accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside
+// a block see the tensor cores' truncating additions.
+//
+// Each SM of the pair loads its own 128 of a tile's 256 rows of x and half of its 256 rows of w per block (128 bytes
+// a row, the layout 128-byte swizzled TMA writes); with the gate SM 0 holds 128 gate rows and SM 1 the matching up
+// rows, so a TMEM lane has both.
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "grouped.cuh"
+#include "mxfp4_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace pair;
+
+constexpr int BM = 128;                 // rows of x per SM (256 per pair)
+constexpr int BN = 256;                 // rows of w per tile
+constexpr int HALF = BN / 2;            // per SM
+constexpr int KB = fp8::BLOCK;          // bytes of a row per step
+constexpr int NSTAGE = 6;
+constexpr int A_BYTES = BM * KB;
+constexpr int STAGE = A_BYTES + HALF * KB;
+constexpr int DSMEM = NSTAGE * STAGE + 1024;
+constexpr int PARTS = 2;                // epilogue warps per TMEM lane quarter
+constexpr int EPI_WARPS = 4 * PARTS;
+constexpr int W = BN / PARTS;           // columns of an epilogue warp
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+
+struct Params {
+  const int32_t* offsets;
+  const float* x_scales;
+  const float* w_scales;
+  int S, E, N;
+  int kb, nb;       // blocks along K and N
+  int cols;         // of y
+  int NT;
+  void* y;
+  int vec;
+  int32_t* status;
+  uint64_t wait_ns;
+};
+
+struct Tile {
+  int e, m, n;
+  grouped::Span g;
+};
+
+__device__ __forceinline__ int mtiles(int rows) { return (rows + 2 * BM - 1) / (2 * BM); }
+
+// Tiles of an expert that run together share the operand with fewer tiles, which stays in L2, while the other one is
+// walked once.
+__device__ __forceinline__ Tile tile_at(int t, int& e, const grouped::Groups& G, const Params& P) {
+  Tile d;
+  e = grouped::find_from(G.start, e, t);
+  d.e = e;
+  d.g = G.span(e);
+  const int local = t - G.start[e], mt = mtiles(d.g.rows());
+  if (mt > P.NT) {
+    d.m = grouped::quick_div(local, P.NT);
+    d.n = local - d.m * P.NT;
+  } else {
+    d.n = grouped::quick_div(local, mt);
+    d.m = local - d.n * mt;
+  }
+  return d;
+}
+
+// A thread's scales of one block.
+template <bool SILU>
+struct Scales {
+  float x, g, u0, u1;       // the row's; the columns': all of them, or the gate's, and of the up columns before and after `edge`
+};
+
+template <bool SILU, class T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params P) {
+  __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ grouped::Groups G;
+  extern __shared__ uint8_t dsmem_raw[];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const uint32_t dsmem = (ptx::smem_u32(dsmem_raw) + 1023u) & ~1023u;
+  auto st = [&](int s) { return dsmem + (uint32_t)(s * STAGE); };
+  volatile int* abort_p = &abort_flag;
+
+  if (tid == 0) {
+    for (int s = 0; s < NSTAGE; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_u32(&tfull_bar[b]), 1);
+      ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), 2 * EPI_WARPS);
+    }
+    ptx::mbar_init(ptx::smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmX);
+    ptx::prefetch_tmap(&tmW);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     ptx::smem_u32(&tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();          // the offsets and operands may be the previous kernel's output
+  pdl_trigger();
+  if (warp == 2)
+    grouped::group_list(P.offsets, P.E, P.S, [&](int rows) { return mtiles(rows) * P.NT; }, G);
+  ptx::tc_fence_before();
+  __syncthreads();
+  cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  const int total = G.start[P.E];
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (ptx::elect_one()) {
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = cluster_id, e = 0; t < total && ok; t += nclusters) {
+        const Tile ti = tile_at(t, e, G, P);
+        const int a_row = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM;
+        const int b_row = SILU ? ti.n * HALF + (int)rank * P.cols : ti.n * BN + (int)rank * HALF;
+        for (int k = 0; k < P.kb; ++k) {
+          if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
+          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
+          const uint32_t fb = map_to_rank(fb_local, 0);
+          tma_load_3d_pair(st(stage), &tmX, k * KB, a_row, 0, fb);
+          tma_load_3d_pair(st(stage) + A_BYTES, &tmW, k * KB, b_row, ti.e, fb);
+          if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader CTA)
+    if (leader && ptx::elect_one()) {
+      constexpr uint32_t IDESC = fp8::idesc(2 * BM, BN);
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int t = cluster_id; t < total && ok; t += nclusters) {
+        for (int k = 0; k < P.kb; ++k) {
+          ok = ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns) &&
+               ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+          const uint64_t ad = ptx::sdesc_k128(st(stage)), bd = ptx::sdesc_k128(st(stage) + A_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < KB / 32; ++kk) fp8::mma<2>(d_tmem, ad + kk * 2, bd + kk * 2, IDESC, kk != 0);
+          commit_pair(ptx::smem_u32(&empty_bar[stage]), 0x3);
+          commit_pair(ptx::smem_u32(&tfull_bar[acc]), 0x3);
+          if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
+          if (++acc == 2) { acc = 0; aph ^= 1u; }
+        }
+      }
+      commit_pair(ptx::smem_u32(&drain_bar), 0x1);
+      int dummy = 0;
+      ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, &dummy, DRAIN_NS);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;              // TMEM lane quarter this warp may read
+    const int part = (warp - 2) >> 2;    // its columns
+    const int row = q * 32 + lane;
+    T* y = static_cast<T*>(P.y);
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int t = cluster_id, e = 0; t < total; t += nclusters) {
+      const Tile ti = tile_at(t, e, G, P);
+      const int m = ti.m * (2 * BM) + (int)rank * BM + row;
+      const int nrows = ti.g.rows() - (m - lane);      // of this warp's 32 (from lane 0 on)
+      // first columns (rows of w) of this thread's sums: W of them, or W / 2 of the gate and as many up ones
+      const int c0 = SILU ? ti.n * HALF + part * (W / 2) : ti.n * BN + part * W;
+      const float* xs = P.x_scales + (long)min(ti.g.lo + m, P.S - 1) * P.kb;
+      const float* ws = P.w_scales + (long)ti.e * P.nb * P.kb;
+      const float* wg = ws + (long)min(c0 / KB, P.nb - 1) * P.kb;
+      // up columns: the half need not start where a block does
+      const int up = P.cols + c0;
+      const int edge = KB - up % KB;                   // up columns before the next block
+      const float* wu0 = ws + (long)min(up / KB, P.nb - 1) * P.kb;
+      const float* wu1 = ws + (long)min(up / KB + 1, P.nb - 1) * P.kb;
+      auto load = [&](int k) {
+        Scales<SILU> s;
+        s.x = __ldg(xs + k);
+        s.g = __ldg(wg + k);
+        s.u0 = SILU ? __ldg(wu0 + k) : 0.0f;
+        s.u1 = SILU ? __ldg(wu1 + k) : 0.0f;
+        return s;
+      };
+      uint64_t sum[W / 2];
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) sum[j] = 0;
+      Scales<SILU> next = load(0);
+      for (int k = 0; k < P.kb; ++k) {
+        const Scales<SILU> s = next;
+        if (k + 1 < P.kb) next = load(k + 1);
+        const float g = s.x * s.g, u0 = s.x * s.u0, u1 = s.x * s.u1;
+        // whole warps go on or stop
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+auto column = [&](int c) {          // where sums c .. c + 15 lie
+          return !SILU ? part * W + c : c < W / 2 ? part * (W / 2) + c : HALF + part * (W / 2) + c - W / 2;
+        };
+        uint32_t v[2][16];
+        ptx::tmem_ld16(taddr + column(0), v[0]);
+#pragma unroll
+        for (int c = 0; c < W; c += 16) {
+          uint32_t(&x)[16] = v[(c / 16) & 1];
+          ptx::tmem_ld_wait16(x);
+          if (c + 16 < W) {
+            ptx::tmem_ld16(taddr + column(c + 16), v[(c / 16 + 1) & 1]);
+          } else {                          // all read: the accumulator goes back
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
+          }
+          // a block's edge lies at a multiple of 16 columns
+          const float f = !SILU || c < W / 2 ? g : c - W / 2 < edge ? u0 : u1;
+          const uint64_t ff = fp8::pack2(f, f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fp8::fma2(sum[c / 2 + j], x[2 * j], x[2 * j + 1], ff);
+        }
+        if (++acc == 2) { acc = 0; aph ^= 1u; }
+      }
+      if (!ok) break;
+      T* dst = y + ((long)ti.g.lo + m) * P.cols;
+#pragma unroll
+      for (int c = 0; c < (SILU ? W / 2 : W); c += 32) {
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          fp8::unpack2(sum[c / 2 + j], v[2 * j], v[2 * j + 1]);
+          if (SILU) {
+            uint32_t u[2];
+            fp8::unpack2(sum[W / 4 + c / 2 + j], u[0], u[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              v[2 * j + h] = __float_as_uint(mx::silu_fast(__uint_as_float(v[2 * j + h])) * __uint_as_float(u[h]));
+          }
+        }
+        if (P.vec > 0) {
+          if (lane < nrows && c0 + c < P.cols) grouped::store_cols(dst, c0 + c, P.cols, P.vec, v);
+        } else if (nrows > 0 && c0 + c < P.cols) {
+          grouped::store_turned(v, dst - (long)lane * P.cols, nrows, c0 + c, P.cols);
+        }
+      }
+    }
+    if (!*abort_p)
+      grouped::zero_unowned(y, G, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
+                            (long)gridDim.x * EPI_WARPS * 32);
+  }
+
+  if (*abort_p) {   // after a timeout, let copies in flight land before the shared memory is released
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 1000000ull) {
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
+  if (tid == 0 && P.status) {
+    if (abort_flag) atomicOr(P.status, MOE_STATUS_TIMEOUT);
+    if (G.bad && blockIdx.x == 0) atomicOr(P.status, MOE_STATUS_BAD_INDEX);
+  }
+}
+
+template <bool SILU, class T>
+int launch(const Fp8Args& a, cudaStream_t s) {
+  const char* name = "fp8_grouped_gemm";
+  if (int rc = ensure_smem_limit(fp8_pair_kernel<SILU, T>, DSMEM, name)) return rc;
+  CUtensorMap tx, tw;
+  int rc;
+  if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;
+  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, HALF))) return rc;
+  Params p{};
+  p.offsets = a.offsets;
+  p.x_scales = a.x_scales;
+  p.w_scales = a.w_scales;
+  p.S = a.S;
+  p.E = a.E;
+  p.N = a.N;
+  p.kb = fp8::blocks(a.K);
+  p.nb = fp8::blocks(a.N);
+  p.cols = SILU ? a.N / 2 : a.N;
+  p.NT = SILU ? (p.cols + HALF - 1) / HALF : (p.cols + BN - 1) / BN;
+  p.y = a.y;
+  p.vec = grouped::store_width(a.y, p.cols, sizeof(T));
+  p.status = a.status;
+  p.wait_ns = wait_limit_ns();
+  const long tiles = ((long)(a.S + 2 * BM - 1) / (2 * BM) + a.E) * p.NT;
+  const int grid = 2 * (int)std::max(1L, std::min(tiles, (long)(num_sms() / 2)));
+  ProfScope ps(name, s);
+  const cudaError_t e = launch_pdl(fp8_pair_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, p);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+  return check_launch(name);
+}
+
+}  // namespace
+
+int launch_fp8_grouped(const Fp8Args& a, cudaStream_t s) {
+  if (grouped_few_rows(a.S, a.E)) return launch_fp8_few(a, s);
+  if (a.out_dtype == MOE_F32) return a.silu ? launch<true, float>(a, s) : launch<false, float>(a, s);
+  if (a.out_dtype == MOE_BF16) return a.silu ? launch<true, __nv_bfloat16>(a, s) : launch<false, __nv_bfloat16>(a, s);
+  return a.silu ? launch<true, __half>(a, s) : launch<false, __half>(a, s);
+}
+
+}  // namespace moe

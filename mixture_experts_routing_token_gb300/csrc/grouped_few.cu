@@ -367,22 +367,6 @@ __global__ void __launch_bounds__(Cfg<MX>::THREADS, 1)
   }
 }
 
-// Columns per unit: the largest number of rounds times (columns + the cost of a unit, about that of
-// 8 columns) is smallest; of equals the larger.
-int unit_columns(long heads, int cols, int most) {
-  int best = most;
-  long cost = 1L << 62;
-  for (int f = most; f >= BOX; f -= BOX) {
-    const long units = heads * ((cols + f - 1) / f), ctas = num_sms();
-    const long c = (units + ctas - 1) / ctas * (f + 8);
-    if (c < cost) {
-      cost = c;
-      best = f;
-    }
-  }
-  return best;
-}
-
 template <bool MX, bool SILU, class T>
 int launch(const CUtensorMap& w, const CUtensorMap& x, const Params& p, cudaStream_t s, const char* name) {
   if (int rc = ensure_smem_limit(grouped_few_kernel<MX, SILU, T>, Cfg<MX>::DSMEM, name)) return rc;
@@ -402,10 +386,26 @@ int launch_mx(int dtype, const CUtensorMap& w, const CUtensorMap& x, const Param
 
 }  // namespace
 
+// Columns per unit: the largest number of rounds times (columns + the cost of a unit, about that of
+// 8 columns) is smallest; of equals the larger.
+int grouped_few_columns(long heads, int cols, int most) {
+  int best = most;
+  long cost = 1L << 62;
+  for (int f = most; f >= BOX; f -= BOX) {
+    const long units = heads * ((cols + f - 1) / f), ctas = num_sms();
+    const long c = (units + ctas - 1) / ctas * (f + 8);
+    if (c < cost) {
+      cost = c;
+      best = f;
+    }
+  }
+  return best;
+}
+
 int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int cols, cudaStream_t s) {
   CUtensorMap tw, tx;
   int rc;
-  const int f = unit_columns(std::min(a.S, a.E), a.N, MAXF);
+  const int f = grouped_few_columns(std::min(a.S, a.E), a.N, MAXF);
   if ((rc = make_tmap_3d(&tw, w, 2, (uint64_t)cols, (uint64_t)a.N, (uint64_t)a.E, ROWB / 2, f))) return rc;
   if ((rc = make_tmap_3d(&tx, x, 2, (uint64_t)cols, (uint64_t)a.S, 1, ROWB / 2, BOX))) return rc;
   Params p{};
@@ -427,7 +427,7 @@ int launch_grouped_few(const GroupedArgs& a, const void* x, const void* w, int c
 int launch_mxfp4_few(const Mxfp4Args& a, cudaStream_t s) {
   CUtensorMap tw, tx;
   int rc;
-  const int f = unit_columns(std::min(a.S, a.E), a.silu ? a.N / 2 : a.N, a.silu ? MAXF / 2 : MAXF);
+  const int f = grouped_few_columns(std::min(a.S, a.E), a.silu ? a.N / 2 : a.N, a.silu ? MAXF / 2 : MAXF);
   if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.E, ROWB, f))) return rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K / 2, (uint64_t)a.S, 1, ROWB, BOX))) return rc;
   Params p{};

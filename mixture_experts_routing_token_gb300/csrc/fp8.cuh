@@ -59,22 +59,5 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// Two float32 multiply-adds in one instruction: acc += v * s, two sums and two values to a register pair.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
-  asm("{\n\t.reg .b64 v;\n\t"
-      "mov.b64 v, {%1, %2};\n\t"
-      "fma.rn.f32x2 %0, v, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(v0), "r"(v1), "l"(s));
-}
-__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& a, uint32_t& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-}
-
 }  // namespace fp8
 }  // namespace moe

@@ -5,8 +5,8 @@
 //   (with the gate, silu(y[p, n]) y[p, N/2 + n])
 //
 // The scales are any float32, so the tensor cores cannot apply them. An accumulator holds one block (K = 128, four
-// MMAs); the epilogue warps read it, multiply by sx sw and add in registers (two sums an instruction), while the
-// next block goes into the other accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside
+// MMAs); the epilogue warps read it, multiply by sx sw and add in registers, while the next block goes into the other
+// accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside
 // a block see the tensor cores' truncating additions.
 //
 // Each SM of the pair loads its own 128 of a tile's 256 rows of x and half of its 256 rows of w per block (128 bytes
@@ -34,7 +34,11 @@ constexpr int DSMEM = NSTAGE * STAGE + 1024;
 constexpr int PARTS = 2;                // epilogue warps per TMEM lane quarter
 constexpr int EPI_WARPS = 4 * PARTS;
 constexpr int W = BN / PARTS;           // columns of an epilogue warp
-constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr int EPI0 = 4;                 // the first of them
+constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;
+// 168 registers a thread at launch (12 warps); the epilogue's eight take what the other four give back
+constexpr int LOW_REGS = 72, HIGH_REGS = 216;
+static_assert(EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS <= (EPI0 + EPI_WARPS) * 168, "registers");
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
@@ -136,6 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = tmem_slot;
   const int total = G.start[P.E];
 
+  if (warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOW_REGS));
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     if (ptx::elect_one()) {
@@ -187,10 +192,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int dummy = 0;
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, &dummy, DRAIN_NS);
     }
-  } else {
+  } else if (warp >= EPI0) {
     // ------------------------------------------------------------ epilogue (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(HIGH_REGS));
     const int q = warp & 3;              // TMEM lane quarter this warp may read
-    const int part = (warp - 2) >> 2;    // its columns
+    const int part = (warp - EPI0) >> 2;    // its columns
     const int row = q * 32 + lane;
     T* y = static_cast<T*>(P.y);
     int acc = 0;
@@ -218,9 +224,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         s.u1 = SILU ? __ldg(wu1 + k) : 0.0f;
         return s;
       };
-      uint64_t sum[W / 2];
+      float sum[W];
 #pragma unroll
-      for (int j = 0; j < W / 2; ++j) sum[j] = 0;
+      for (int j = 0; j < W; ++j) sum[j] = 0.0f;
       Scales<SILU> next = load(0);
       for (int k = 0; k < P.kb; ++k) {
         const Scales<SILU> s = next;
@@ -231,27 +237,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-auto column = [&](int c) {          // where sums c .. c + 15 lie
-          return !SILU ? part * W + c : c < W / 2 ? part * (W / 2) + c : HALF + part * (W / 2) + c - W / 2;
-        };
-        uint32_t v[2][16];
-        ptx::tmem_ld16(taddr + column(0), v[0]);
 #pragma unroll
         for (int c = 0; c < W; c += 16) {
-          uint32_t(&x)[16] = v[(c / 16) & 1];
-          ptx::tmem_ld_wait16(x);
-          if (c + 16 < W) {
-            ptx::tmem_ld16(taddr + column(c + 16), v[(c / 16 + 1) & 1]);
-          } else {                          // all read: the accumulator goes back
+          uint32_t v[16];
+          ptx::tmem_ld16(taddr + (!SILU ? part * W + c : c < W / 2 ? part * (W / 2) + c : HALF + part * (W / 2) + c - W / 2), v);
+          ptx::tmem_ld_wait16(v);
+          if (c + 16 == W) {                // all read: the accumulator goes back
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
           }
           // a block's edge lies at a multiple of 16 columns
           const float f = !SILU || c < W / 2 ? g : c - W / 2 < edge ? u0 : u1;
-          const uint64_t ff = fp8::pack2(f, f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) fp8::fma2(sum[c / 2 + j], x[2 * j], x[2 * j + 1], ff);
+          for (int j = 0; j < 16; ++j) sum[c + j] = fmaf(__uint_as_float(v[j]), f, sum[c + j]);
         }
         if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
@@ -261,16 +260,8 @@ auto column = [&](int c) {          // where sums c .. c + 15 lie
       for (int c = 0; c < (SILU ? W / 2 : W); c += 32) {
         uint32_t v[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          fp8::unpack2(sum[c / 2 + j], v[2 * j], v[2 * j + 1]);
-          if (SILU) {
-            uint32_t u[2];
-            fp8::unpack2(sum[W / 4 + c / 2 + j], u[0], u[1]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              v[2 * j + h] = __float_as_uint(mx::silu_fast(__uint_as_float(v[2 * j + h])) * __uint_as_float(u[h]));
-          }
-        }
+        for (int j = 0; j < 32; ++j)
+          v[j] = __float_as_uint(SILU ? mx::silu_fast(sum[c + j]) * sum[W / 2 + c + j] : sum[c + j]);
         if (P.vec > 0) {
           if (lane < nrows && c0 + c < P.cols) grouped::store_cols(dst, c0 + c, P.cols, P.vec, v);
         } else if (nrows > 0 && c0 + c < P.cols) {
@@ -279,7 +270,7 @@ auto column = [&](int c) {          // where sums c .. c + 15 lie
       }
     }
     if (!*abort_p)
-      grouped::zero_unowned(y, G, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - 2) * 32 + lane,
+      grouped::zero_unowned(y, G, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - EPI0) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
   }
 

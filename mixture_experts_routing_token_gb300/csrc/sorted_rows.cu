@@ -15,6 +15,7 @@
 // dropped) and p is a routed row, so that whatever else the buffer holds, no index leaves the arrays. With few slots
 // each CTA of the one launch looks through reverse_indices itself instead.
 #include <algorithm>
+#include <type_traits>
 
 #include "values.cuh"
 
@@ -22,30 +23,59 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 8;               // slots of a token whose rows are under way together
+constexpr int kFlight = 8;              // loads of sorted rows that a thread has under way
 constexpr int kScanSlots = 2048;        // up to this many slots a CTA finds its own (see above)
-constexpr int kSlotsPerCta = kThreads / 32 * MOE_MAX_TOPK;
+constexpr int kMinGroup = 4;            // threads of a token at least
+constexpr int kSlotsPerCta = kThreads / kMinGroup * MOE_MAX_TOPK;
 
-// V neighbouring values: 16 bytes, or one where rows are not a multiple of that.
-template <class T, bool VEC>
+// B bytes of neighbouring values as they lie in memory: 16, or 4 or 2 where rows are not a multiple of more.
+template <int B>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = uint16_t; };
+
+template <class T, int B>
 struct Piece {
-  static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
-  float v[V];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (!VEC) {
-      v[0] = to_float(__ldg(p));
-    } else if constexpr (sizeof(T) == 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  static constexpr int V = B / (int)sizeof(T);
+  using W = typename Word<B>::type;
+  W w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const W*>(p)); }
+  __device__ __forceinline__ void values(float (&v)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (B == 16) {
+        v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+      } else {
+        v[0] = __uint_as_float(w);
+      }
+    } else if constexpr (B == 2) {
+      v[0] = to_float(*reinterpret_cast<const T*>(&w));
     } else {
-      load8(p, v);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        } else {
+          v[2 * i] = __uint_as_float(q[i] << 16);
+          v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+        }
+      }
     }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (!VEC) {
+  static __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (B == 16) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      else *p = v[0];
+    } else if constexpr (B == 2) {
       *p = from_float<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (B == 4) {
+      *reinterpret_cast<uint32_t*>(p) = grouped::pack_pair<T>(v[0], v[1]);
     } else {
       store8(p, v);
     }
@@ -102,10 +132,11 @@ __device__ __forceinline__ void take_positions(const Args& a, int s0, int count,
   __syncthreads();
 }
 
-// out[t] = sum_j w[t, j] src[pos(t, j)]. G threads take a token.
-template <class T, bool VEC>
+// out[t] = sum_j w[t, j] src[pos(t, j)]. G threads take a token, K of its slots and kFlight / K pieces at a time.
+template <class T, int B, int K>
 __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const Args a, const T* __restrict__ src, T* __restrict__ out, int G) {
-  using P = Piece<T, VEC>;
+  using P = Piece<T, B>;
+  constexpr int U = kFlight / K;
   __shared__ int pos[kSlotsPerCta];
   pdl_wait();
   pdl_trigger();
@@ -116,89 +147,117 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const Args a, const 
   const int* at = pos + local * a.k;
   const float* w = a.weights ? a.weights + (long)t * a.k : nullptr;
   const int pieces = a.H / P::V;
-  for (int c = threadIdx.x % G; c < pieces; c += G) {
-    P sum;
+  for (int c0 = threadIdx.x % G; c0 < pieces; c0 += U * G) {
+    float sum[U][P::V];
 #pragma unroll
-    for (int q = 0; q < P::V; ++q) sum.v[q] = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-      P y[kGroup];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (j0 + j < a.k && at[j0 + j] >= 0) y[j].load(src + (long)at[j0 + j] * a.H + c * P::V);
+      for (int q = 0; q < P::V; ++q) sum[u][q] = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += K) {
+      P y[K][U];
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces)
+            y[j][u].load(src + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V);
+#pragma unroll
+      for (int j = 0; j < K; ++j)
         if (j0 + j < a.k && at[j0 + j] >= 0) {
           const float wj = w ? __ldg(w + j0 + j) : 1.0f;
 #pragma unroll
-          for (int q = 0; q < P::V; ++q) sum.v[q] += wj * y[j].v[q];
+          for (int u = 0; u < U; ++u) {
+            float v[P::V];
+            y[j][u].values(v);
+#pragma unroll
+            for (int q = 0; q < P::V; ++q) sum[u][q] += wj * v[q];
+          }
         }
     }
-    sum.store(out + (long)t * a.H + c * P::V);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * G < pieces) P::store(out + (long)t * a.H + (c0 + u * G) * P::V, sum[u]);
   }
 }
 
 // d_y[pos(t, j)] = w[t, j] d_out[t] and d_w[t, j] = <d_out[t], y[pos(t, j)]>; either may be null.
-template <class T, bool VEC>
+template <class T, int B, int K>
 __global__ void __launch_bounds__(kThreads)
     sum_rows_backward_kernel(const Args a, const T* __restrict__ d_out, const T* __restrict__ y, T* __restrict__ d_y,
                              float* __restrict__ d_w, int G) {
-  using P = Piece<T, VEC>;
+  using P = Piece<T, B>;
+  constexpr int U = kFlight / K;
   __shared__ int pos[kSlotsPerCta];
-  __shared__ float part[kThreads / 32][kGroup];
+  __shared__ float part[kThreads / 32][K];
   pdl_wait();
   pdl_trigger();
   const int tokens = kThreads / G, t0 = blockIdx.x * tokens;
   take_positions(a, t0 * a.k, min(tokens, a.T - t0) * a.k, pos);
-  const int local = threadIdx.x / G, t = t0 + local;
+  const int local = threadIdx.x / G, me = threadIdx.x % G, t = t0 + local;
   const bool in = t < a.T;
   const int* at = pos + (in ? local : 0) * a.k;
   const float* w = a.weights + (long)(in ? t : 0) * a.k;
   const int pieces = a.H / P::V;
-  for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-    float dot[kGroup];
+  for (int j0 = 0; j0 < a.k; j0 += K) {
+    float dot[K];
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) dot[j] = 0.0f;
-    for (int c = threadIdx.x % G; in && c < pieces; c += G) {
-      P d, r[kGroup];
-      d.load(d_out + (long)t * a.H + c * P::V);
+    for (int j = 0; j < K; ++j) dot[j] = 0.0f;
+    for (int c0 = me; in && c0 < pieces; c0 += U * G) {
+      P d[U], r[K][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * G < pieces) d[u].load(d_out + (long)t * a.H + (c0 + u * G) * P::V);
       if (d_w != nullptr) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (j0 + j < a.k && at[j0 + j] >= 0) r[j].load(y + (long)at[j0 + j] * a.H + c * P::V);
+        for (int j = 0; j < K; ++j)
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (j0 + j < a.k && at[j0 + j] >= 0) {
-#pragma unroll
-            for (int q = 0; q < P::V; ++q) dot[j] += d.v[q] * r[j].v[q];
-          }
+          for (int u = 0; u < U; ++u)
+            if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces)
+              r[j][u].load(y + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V);
       }
-      if (d_y != nullptr) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (j0 + j < a.k && at[j0 + j] >= 0) {
-            const float wj = __ldg(w + j0 + j);
-            P o;
+      for (int u = 0; u < U; ++u) {
+        if (c0 + u * G >= pieces) continue;
+        float dv[P::V];
+        d[u].values(dv);
 #pragma unroll
-            for (int q = 0; q < P::V; ++q) o.v[q] = wj * d.v[q];
-            o.store(d_y + (long)at[j0 + j] * a.H + c * P::V);
+        for (int j = 0; j < K; ++j) {
+          if (j0 + j >= a.k || at[j0 + j] < 0) continue;
+          if (d_w != nullptr) {
+            float v[P::V];
+            r[j][u].values(v);
+#pragma unroll
+            for (int q = 0; q < P::V; ++q) dot[j] += dv[q] * v[q];
           }
+          if (d_y != nullptr) {
+            const float wj = __ldg(w + j0 + j);
+            float o[P::V];
+#pragma unroll
+            for (int q = 0; q < P::V; ++q) o[q] = wj * dv[q];
+            P::store(d_y + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V, o);
+          }
+        }
       }
     }
     if (d_w == nullptr) continue;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
+    for (int j = 0; j < K; ++j) {
+      for (int s = min(G, 32) / 2; s; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+      if (G > 32 && lane == 0) part[warp][j] = dot[j];
+    }
+    if (G > 32) __syncthreads();
 #pragma unroll
-      for (int s = 16; s; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
-      if (lane == 0) part[warp][j] = dot[j];
+    for (int j = 0; j < K; ++j) {
+      if (!in || me != j % G || j0 + j >= a.k) continue;
+      float sum = dot[j];
+      if (G > 32) {
+        sum = 0.0f;
+        for (int i = 0; i < G / 32; ++i) sum += part[warp + i][j];
+      }
+      d_w[(long)t * a.k + j0 + j] = sum;
     }
-    __syncthreads();
-    if (in && threadIdx.x % G < kGroup && j0 + threadIdx.x % G < a.k) {
-      float sum = 0.0f;
-      for (int i = 0; i < G / 32; ++i) sum += part[warp + i][lane];
-      d_w[(long)t * a.k + j0 + lane] = sum;
-    }
-    __syncthreads();
+    if (G > 32) __syncthreads();
   }
 }
 
@@ -237,47 +296,57 @@ int positions(Args& a, cudaStream_t s) {
   return done(launch_pdl(slot_positions_kernel, grid, kThreads, 0, s, a), "slot_positions");
 }
 
-// Threads of a token: as many as it has pieces, a power of two between a warp and the CTA.
-int threads_per_token(int pieces) {
-  int g = 32;
-  while (g < kThreads && g < pieces) g *= 2;
+// Threads of a token, a power of two: no more than it has pieces, and no more than give every SM five CTAs.
+int threads_per_token(int pieces, int T) {
+  int g = kMinGroup;
+  while (g < kThreads && g < pieces && (g < 32 || (long)T * g < 5L * kThreads * num_sms())) g *= 2;
   return g;
 }
 
-template <class T>
-bool by_16_bytes(int H, std::initializer_list<const void*> rows) {
-  if ((long)H * (int)sizeof(T) % 16 != 0) return false;
-  for (const void* p : rows)
-    if (!aligned(p, 16)) return false;
-  return true;
-}
+// Bytes of a row that are read at a time.
+int piece_bytes(long row_bytes) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : 2; }
 
-template <class T, bool VEC>
+template <class T, int B, int K>
 int sum_as(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  const int G = threads_per_token(a.H / Piece<T, VEC>::V), tokens = kThreads / G;
+  const int G = threads_per_token(a.H / Piece<T, B>::V, a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_kernel<T, VEC>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a, static_cast<const T*>(src),
+  return done(launch_pdl(sum_rows_kernel<T, B, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a, static_cast<const T*>(src),
                          static_cast<T*>(out), G),
               name);
 }
+template <class T, int B>
+int sum_of(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
+  return a.k <= 2 ? sum_as<T, B, 2>(a, src, out, name, s) : sum_as<T, B, kFlight>(a, src, out, name, s);
+}
 template <class T>
 int sum(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  return by_16_bytes<T>(a.H, {src, out}) ? sum_as<T, true>(a, src, out, name, s) : sum_as<T, false>(a, src, out, name, s);
+  const int b = piece_bytes((long)a.H * (int)sizeof(T));
+  if (b == 16) return sum_of<T, 16>(a, src, out, name, s);
+  if constexpr (sizeof(T) == 2)
+    if (b == 2) return sum_of<T, 2>(a, src, out, name, s);
+  return sum_of<T, 4>(a, src, out, name, s);
 }
 
-template <class T, bool VEC>
+template <class T, int B, int K>
 int sum_backward_as(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
   const char* name = "ep_combine_backward";
-  const int G = threads_per_token(a.H / Piece<T, VEC>::V), tokens = kThreads / G;
+  const int G = threads_per_token(a.H / Piece<T, B>::V, a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_backward_kernel<T, VEC>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
+  return done(launch_pdl(sum_rows_backward_kernel<T, B, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
                          static_cast<const T*>(d_out), static_cast<const T*>(y), static_cast<T*>(d_y), d_w, G),
               name);
 }
+template <class T, int B>
+int sum_backward_of(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
+  return a.k <= 2 ? sum_backward_as<T, B, 2>(a, d_out, y, d_y, d_w, s) : sum_backward_as<T, B, kFlight>(a, d_out, y, d_y, d_w, s);
+}
 template <class T>
 int sum_backward(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
-  return by_16_bytes<T>(a.H, {d_out, y, d_y}) ? sum_backward_as<T, true>(a, d_out, y, d_y, d_w, s)
-                                              : sum_backward_as<T, false>(a, d_out, y, d_y, d_w, s);
+  const int b = piece_bytes((long)a.H * (int)sizeof(T));
+  if (b == 16) return sum_backward_of<T, 16>(a, d_out, y, d_y, d_w, s);
+  if constexpr (sizeof(T) == 2)
+    if (b == 2) return sum_backward_of<T, 2>(a, d_out, y, d_y, d_w, s);
+  return sum_backward_of<T, 4>(a, d_out, y, d_y, d_w, s);
 }
 
 Args args(const SortedRows& r, const float* weights) {

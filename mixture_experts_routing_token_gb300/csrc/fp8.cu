@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(256) rms_norm_fp8_wide_kernel(const NormArgs a
 
 // ---- 8-bit rows into expert order ---------------------------------------------------------------
 
-// 16 bytes of codes per thread, and the scale of the block that starts there.
+// 16 bytes of codes per thread, and the scale of the block that starts there. A CTA takes 1024 neighbouring pieces a turn,
+// whose loads are under way together, and what it writes is one stretch of memory: 131072 rows of 2048, 284 MB, 61 us (4.6
+// TB/s written; filling the same memory takes 75); with pieces a grid apart 90, with a CTA for each turn 74.
 __global__ void __launch_bounds__(256)
     fp8_gather_kernel(const uint4* __restrict__ src, const float* __restrict__ src_scales, int T, int units, int sh, int kb,
                       const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, int E, int S,
@@ -323,8 +325,8 @@ __global__ void __launch_bounds__(256)
   const int rows = __ldg(offsets + E);
   if (blockIdx.x == 0 && threadIdx.x == 0 && (rows < 0 || rows > S) && status != nullptr) atomicOr(status, MOE_STATUS_BAD_INDEX);
   const long n = (long)min(max(rows, 0), S) * units;
-  const long stride = (long)gridDim.x * blockDim.x;
-  for (long i0 = (long)blockIdx.x * blockDim.x + threadIdx.x; i0 < n; i0 += U * stride) {
+  const long stride = blockDim.x;
+  for (long i0 = (long)blockIdx.x * blockDim.x * U + threadIdx.x; i0 < n; i0 += (long)U * gridDim.x * blockDim.x) {
     uint4 c[U];
     float s[U];
     long r[U];
@@ -349,8 +351,8 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < U; ++u) {
       const long i = i0 + u * stride;
       if (i >= n) break;
-      out[i] = c[u];
-      if ((b[u] & 7) == 0) scales[r[u] * kb + (b[u] >> 3)] = s[u];
+      __stcs(out + i, c[u]);
+      if ((b[u] & 7) == 0) __stcs(scales + r[u] * kb + (b[u] >> 3), s[u]);
     }
   }
 }
@@ -439,7 +441,7 @@ int launch_fp8_gather_rows(const uint8_t* codes, const float* scales, const int3
                            int S, uint8_t* out, float* out_scales, int32_t* status, cudaStream_t s) {
   const char* name = "fp8_gather_rows";
   const int units = H / 16;
-  const unsigned grid = std::min(blocks_for((long)S * units, 4), (unsigned)num_sms() * 8);
+  const unsigned grid = std::min(blocks_for((long)S * units, 4), (unsigned)num_sms() * 4);
   ProfScope ps(name, s);
   return done(launch_pdl(fp8_gather_kernel, grid, 256, 0, s, reinterpret_cast<const uint4*>(codes), scales, T, units,
                          pow2_shift(units), fp8::blocks(H), ids, offsets, E, S, reinterpret_cast<uint4*>(out), out_scales, status),

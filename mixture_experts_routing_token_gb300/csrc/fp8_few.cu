@@ -9,10 +9,11 @@
 // x, f columns of y) by turns:
 //   warp 0     TMA producer: per block of 128 of the reduction one box of f rows of w (two with the gate), boxes of 16
 //              rows of x, through a ring whose stages are as large as the launch's units need;
-//   warp 1     MMA issuer (M = 128, N = 16 .. 64, four K = 32 a block) into accumulators of one block each, eight of
-//              them in turn, so that neither side waits for the other's latency;
-//   warps 2-5  epilogue: multiply an accumulator by sx sw and add it in registers, block by block; at the end of a
-//              unit a warp stores 32 neighbouring columns of a row at a time.
+//   warp 1     MMA issuer (M = 128, N = 16 .. 64, four K = 32 a block), a block to an accumulator;
+//   warps 2-5  epilogue: multiply an accumulator by sx sw and add it in registers; at the end of a unit a warp stores
+//              32 neighbouring columns of a row at a time.
+// Blocks go to the epilogue four at a time (2 x 4 x 64 columns of tensor memory): a hand-over takes the epilogue some
+// 500 cycles beside the sums, and one per block, 16 KB of weights, held the whole kernel at 4.8 TB/s.
 // f is chosen on the host as for the 16-bit products (grouped_few.cu).
 #include <algorithm>
 
@@ -35,9 +36,8 @@ constexpr int MAXSTAGE = 20;
 constexpr int RING = 208 * 1024;
 constexpr int DSMEM = RING + 1024;
 constexpr int THREADS = 6 * 32;
-constexpr int NACC = 8;
-constexpr uint32_t TMEM_COLS = NACC * MAXR;
-constexpr int AHEAD = 4;                 // blocks whose scales are loaded together
+constexpr int CHUNK = 4;                 // blocks that are handed to the epilogue together, each in columns of its own
+constexpr uint32_t ACC_COLS = CHUNK * MAXR, TMEM_COLS = 2 * ACC_COLS;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
 struct Params {
@@ -87,7 +87,7 @@ template <bool SILU, class T>
 __global__ void __launch_bounds__(THREADS, 1)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params P) {
   __shared__ __align__(8) uint64_t full_bar[MAXSTAGE], empty_bar[MAXSTAGE];
-  __shared__ __align__(8) uint64_t tfull_bar[NACC], tempty_bar[NACC], drain_bar;
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int s_most;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
     }
-    for (int b = 0; b < NACC; ++b) {
+    for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&tfull_bar[b]), 1);
       ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), 4);
     }
@@ -174,18 +174,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Unit u = unit_at(t, G, expert_of, P, tiles);
         const uint32_t idesc = fp8::idesc(MAXF, (u.rows + BOX - 1) / BOX * BOX);
         for (int k = 0; k < P.kb; ++k) {
-          ok = ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns) &&
-               ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
+          if (k % CHUNK == 0) {
+            ok = ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns);
+            if (!ok) break;
+          }
+          ok = ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * MAXR);
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS + k % CHUNK * MAXR);
           const uint64_t ad = ptx::sdesc_k128(st(stage)), bd = ptx::sdesc_k128(st(stage) + a_bytes);
 #pragma unroll
           for (int kk = 0; kk < KB / 32; ++kk) fp8::mma<1>(d_tmem, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
           ptx::mma_commit(ptx::smem_u32(&empty_bar[stage]));
-          ptx::mma_commit(ptx::smem_u32(&tfull_bar[acc]));
           if (++stage == nstage) { stage = 0; ph ^= 1u; }
-          if (++acc == NACC) { acc = 0; aph ^= 1u; }
+          if (k % CHUNK == CHUNK - 1 || k == P.kb - 1) {
+            ptx::mma_commit(ptx::smem_u32(&tfull_bar[acc]));
+            if (++acc == 2) { acc = 0; aph ^= 1u; }
+          }
         }
       }
       ptx::mma_commit(ptx::smem_u32(&drain_bar));
@@ -206,10 +211,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float* ws = P.w_scales + ((long)u.e * P.nb + min(wrow / KB, P.nb - 1)) * P.kb;
       const float* xs0 = P.x_scales + (long)(u.row + min(lane, u.rows - 1)) * P.kb;
       const float* xs1 = P.x_scales + (long)(u.row + min(lane + 32, u.rows - 1)) * P.kb;
-      float w[AHEAD], x0[AHEAD], x1[AHEAD];
+      float w[CHUNK], x0[CHUNK], x1[CHUNK];
       auto load = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+        for (int i = 0; i < CHUNK; ++i) {
           const int k = min(k0 + i, P.kb - 1);
           w[i] = __ldg(ws + k);
           x0[i] = __ldg(xs0 + k);
@@ -221,40 +226,42 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < MAXR; ++j) sum[j] = 0.0f;
       load(0);
       bool ok = true;
-      for (int k0 = 0; k0 < P.kb && ok; k0 += AHEAD) {
-        float cw[AHEAD], c0[AHEAD], c1[AHEAD];
+      for (int k0 = 0; k0 < P.kb && ok; k0 += CHUNK) {
+        float cw[CHUNK], c0[CHUNK], c1[CHUNK];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+        for (int i = 0; i < CHUNK; ++i) {
           cw[i] = w[i];
           c0[i] = x0[i];
           c1[i] = x1[i];
         }
-        if (k0 + AHEAD < P.kb) load(k0 + AHEAD);
+        if (k0 + CHUNK < P.kb) load(k0 + CHUNK);
+        // whole warps go on or stop (the shuffles below)
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          if (k0 + i >= P.kb || !ok) continue;
-          // whole warps go on or stop (the shuffles below)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns));
-          if (!ok) continue;
-          ptx::tc_fence_after();
-          const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * MAXR);
+        for (int c = 0; c < MAXR; c += 16) {
+          if (c >= u.rows) continue;
+          uint32_t v[CHUNK][16];
 #pragma unroll
-          for (int c = 0; c < MAXR; c += 16) {
-            if (c >= u.rows) continue;
-            uint32_t v[16];
-            ptx::tmem_ld16(taddr + c, v);
-            ptx::tmem_ld_wait();
+          for (int i = 0; i < CHUNK; ++i)
+            if (k0 + i < P.kb) ptx::tmem_ld16(taddr + i * MAXR + c, v[i]);
+#pragma unroll
+          for (int i = 0; i < CHUNK; ++i) {
+            if (k0 + i >= P.kb) continue;
+            ptx::tmem_ld_wait16(v[i]);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float s = __shfl_sync(0xffffffffu, c < 32 ? c0[i] : c1[i], (c + j) & 31) * cw[i];
-              sum[c + j] = fmaf(__uint_as_float(v[j]), s, sum[c + j]);
+              sum[c + j] = fmaf(__uint_as_float(v[i][j]), s, sum[c + j]);
             }
           }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[acc]));
-          if (++acc == NACC) { acc = 0; aph ^= 1u; }
         }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[acc]));
+        if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       // every epilogue warp sees the same outcome: the gate's exchange needs all four
       if (SILU) ok = !named_bar_or(1, 128, !ok);

@@ -33,7 +33,7 @@ constexpr int MAXHEADS = MOE_MAX_EXPERTS + kFewRows * MOE_MAX_EXPERTS / MAXR;   
 constexpr int A_READ = MAXF * KB;        // what an MMA reads of its A operand, whatever was loaded
 constexpr int UP = A_READ / 2;           // with the gate: the up rows, after 64 rows of room for the gate's
 constexpr int MAXSTAGE = 20;
-constexpr int RING = 208 * 1024;
+constexpr int RING = 204 * 1024;
 constexpr int DSMEM = RING + 1024;
 constexpr int THREADS = 6 * 32;
 constexpr int CHUNK = 4;                 // blocks that are handed to the epilogue together, each in columns of its own
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ grouped::Groups G;
   __shared__ uint16_t expert_of[MAXHEADS];
   __shared__ float up_part[SILU ? 64 : 1][17];      // up columns of 16 rows, on their way to the gate's warps
+  __shared__ __align__(16) float x_part[4][CHUNK][MAXR];      // a chunk's scales of the rows, of each warp's own
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -227,15 +228,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       load(0);
       bool ok = true;
       for (int k0 = 0; k0 < P.kb && ok; k0 += CHUNK) {
-        float cw[CHUNK], c0[CHUNK], c1[CHUNK];
+        float cw[CHUNK];
+        __syncwarp();                      // the last chunk's have been read
 #pragma unroll
         for (int i = 0; i < CHUNK; ++i) {
           cw[i] = w[i];
-          c0[i] = x0[i];
-          c1[i] = x1[i];
+          x_part[q][i][lane] = x0[i];
+          if (u.rows > 32) x_part[q][i][lane + 32] = x1[i];
         }
+        __syncwarp();
         if (k0 + CHUNK < P.kb) load(k0 + CHUNK);
-        // whole warps go on or stop (the shuffles below)
+        // whole warps go on or stop
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&tfull_bar[acc]), aph, abort_p, P.wait_ns));
         if (!ok) break;
         ptx::tc_fence_after();
@@ -252,9 +255,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (k0 + i >= P.kb) continue;
             ptx::tmem_ld_wait16(v[i]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float s = __shfl_sync(0xffffffffu, c < 32 ? c0[i] : c1[i], (c + j) & 31) * cw[i];
-              sum[c + j] = fmaf(__uint_as_float(v[i][j]), s, sum[c + j]);
+            for (int j = 0; j < 16; j += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(&x_part[q][i][c + j]);
+              sum[c + j] = fmaf(__uint_as_float(v[i][j]), x.x * cw[i], sum[c + j]);
+              sum[c + j + 1] = fmaf(__uint_as_float(v[i][j + 1]), x.y * cw[i], sum[c + j + 1]);
+              sum[c + j + 2] = fmaf(__uint_as_float(v[i][j + 2]), x.z * cw[i], sum[c + j + 2]);
+              sum[c + j + 3] = fmaf(__uint_as_float(v[i][j + 3]), x.w * cw[i], sum[c + j + 3]);
             }
           }
         }

@@ -82,7 +82,6 @@ __device__ __forceinline__ Tile tile_at(int t, int& e, const grouped::Groups& G,
 }
 
 // A thread's scales of one block.
-template <bool SILU>
 struct Scales {
   float x, g, u0, u1;       // the row's; the columns': all of them, or the gate's, and of the up columns before and after `edge`
 };
@@ -202,34 +201,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int acc = 0;
     uint32_t aph = 0;
     bool ok = true;
-    for (int t = cluster_id, e = 0; t < total; t += nclusters) {
-      const Tile ti = tile_at(t, e, G, P);
-      const int m = ti.m * (2 * BM) + (int)rank * BM + row;
-      const int nrows = ti.g.rows() - (m - lane);      // of this warp's 32 (from lane 0 on)
+    // where a tile's scales are; `next` is loaded a block ahead, a tile's first one before the last tile's results are
+    // stored
+    const float *xs, *wg, *wu0, *wu1;
+    int c0, edge;
+    auto locate = [&](const Tile& ti) {
+      const int r = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM + row;
       // first columns (rows of w) of this thread's sums: W of them, or W / 2 of the gate and as many up ones
-      const int c0 = SILU ? ti.n * HALF + part * (W / 2) : ti.n * BN + part * W;
-      const float* xs = P.x_scales + (long)min(ti.g.lo + m, P.S - 1) * P.kb;
+      c0 = SILU ? ti.n * HALF + part * (W / 2) : ti.n * BN + part * W;
       const float* ws = P.w_scales + (long)ti.e * P.nb * P.kb;
-      const float* wg = ws + (long)min(c0 / KB, P.nb - 1) * P.kb;
+      xs = P.x_scales + (long)min(r, P.S - 1) * P.kb;
+      wg = ws + (long)min(c0 / KB, P.nb - 1) * P.kb;
       // up columns: the half need not start where a block does
-      const int up = P.cols + c0;
-      const int edge = KB - up % KB;                   // up columns before the next block
-      const float* wu0 = ws + (long)min(up / KB, P.nb - 1) * P.kb;
-      const float* wu1 = ws + (long)min(up / KB + 1, P.nb - 1) * P.kb;
-      auto load = [&](int k) {
-        Scales<SILU> s;
-        s.x = __ldg(xs + k);
-        s.g = __ldg(wg + k);
-        s.u0 = SILU ? __ldg(wu0 + k) : 0.0f;
-        s.u1 = SILU ? __ldg(wu1 + k) : 0.0f;
-        return s;
-      };
+      const int up = SILU ? P.cols + c0 : 0;
+      edge = KB - up % KB;                             // up columns before the next block
+      wu0 = ws + (long)min(up / KB, P.nb - 1) * P.kb;
+      wu1 = ws + (long)min(up / KB + 1, P.nb - 1) * P.kb;
+    };
+    auto load = [&](int k) {
+      Scales s;
+      s.x = __ldg(xs + k);
+      s.g = __ldg(wg + k);
+      s.u0 = SILU ? __ldg(wu0 + k) : 0.0f;
+      s.u1 = SILU ? __ldg(wu1 + k) : 0.0f;
+      return s;
+    };
+    Scales next{};
+    int e = 0;
+    Tile ti{};
+    if (cluster_id < total) {
+      ti = tile_at(cluster_id, e, G, P);
+      locate(ti);
+      next = load(0);
+    }
+    for (int t = cluster_id; t < total; t += nclusters) {
       float sum[W];
 #pragma unroll
       for (int j = 0; j < W; ++j) sum[j] = 0.0f;
-      Scales<SILU> next = load(0);
       for (int k = 0; k < P.kb; ++k) {
-        const Scales<SILU> s = next;
+        const Scales s = next;
         if (k + 1 < P.kb) next = load(k + 1);
         const float g = s.x * s.g, u0 = s.x * s.u0, u1 = s.x * s.u1;
         // whole warps go on or stop
@@ -255,7 +265,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       if (!ok) break;
+      const int m = ti.m * (2 * BM) + (int)rank * BM + row, col = c0;
+      const int nrows = ti.g.rows() - (m - lane);      // of this warp's 32 (from lane 0 on)
       T* dst = y + ((long)ti.g.lo + m) * P.cols;
+      if (t + nclusters < total) {
+        ti = tile_at(t + nclusters, e, G, P);
+        locate(ti);
+        next = load(0);
+      }
 #pragma unroll
       for (int c = 0; c < (SILU ? W / 2 : W); c += 32) {
         uint32_t v[32];
@@ -263,9 +280,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 32; ++j)
           v[j] = __float_as_uint(SILU ? mx::silu_fast(sum[c + j]) * sum[W / 2 + c + j] : sum[c + j]);
         if (P.vec > 0) {
-          if (lane < nrows && c0 + c < P.cols) grouped::store_cols(dst, c0 + c, P.cols, P.vec, v);
-        } else if (nrows > 0 && c0 + c < P.cols) {
-          grouped::store_turned(v, dst - (long)lane * P.cols, nrows, c0 + c, P.cols);
+          if (lane < nrows && col + c < P.cols) grouped::store_cols(dst, col + c, P.cols, P.vec, v);
+        } else if (nrows > 0 && col + c < P.cols) {
+          grouped::store_turned(v, dst - (long)lane * P.cols, nrows, col + c, P.cols);
         }
       }
     }

@@ -458,9 +458,12 @@ def _first(t, name):
 
 def _take(t, name, dtype, index):
     """Address of an input after its checks."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
-        _refuse(t, name, dtype, index)
-    return t.data_ptr()
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:      # not a tensor
+        pass
+    _refuse(t, name, dtype, index)
 
 
 def _give(t, name, shape, dtype, index, stream):
@@ -494,6 +497,10 @@ def _raw(stream, index):
 # of 0.8): a 4-bit product that makes its workspace takes the host 13.7 us, and 20.1 where the library is called once to
 # say that it needs one.
 _sizes = functools.lru_cache(maxsize=4096)
+
+
+# What follows from the shapes of a call alone is worked out once for each (1 us less a call).
+_shapes = functools.lru_cache(maxsize=4096)
 
 
 def _fits(*sizes):
@@ -734,6 +741,16 @@ def moe_gather_rows_backward_workspace_size(T, k) -> int:
     return int(lib().moe_gather_rows_backward_workspace_size(T, k))
 
 
+@_shapes
+def _gather_backward_shape(x, reverse, offsets, k):
+    """(T, H, E, shape of d_hidden)"""
+    if len(x) != 2 or k < 1 or x[0] % k or reverse != x[:1] or len(offsets) != 1 or offsets[0] < 2:
+        raise ValueError("shapes must be d_x_sorted [T * k, H], reverse_indices [T * k], offsets [E + 1]")
+    T, H, E = x[0] // k, x[1], offsets[0] - 1
+    _fits(x[0], H, E)
+    return T, H, E, torch.Size((T, H))
+
+
 def moe_gather_rows_backward(d_x_sorted, reverse_indices, offsets, k, d_hidden=None, workspace=None, status=None, stream=None):
     """Gradient of :func:`moe_gather_rows`: d_hidden[t] = sum_j d_x_sorted[pos(t, j)] -> [T, H] in d_x_sorted's dtype.
 
@@ -743,12 +760,9 @@ def moe_gather_rows_backward(d_x_sorted, reverse_indices, offsets, k, d_hidden=N
     rp = _take(reverse_indices, "reverse_indices", _I32, d)
     op = _take(offsets, "offsets", _I32, d)
     dt = _code(dtype)
-    xs, k = d_x_sorted.shape, int(k)
-    if len(xs) != 2 or k < 1 or xs[0] % k or reverse_indices.shape != xs[:1] or len(offsets.shape) != 1 or offsets.shape[0] < 2:
-        raise ValueError("shapes must be d_x_sorted [T * k, H], reverse_indices [T * k], offsets [E + 1]")
-    T, H, E = xs[0] // k, xs[1], offsets.shape[0] - 1
-    _fits(xs[0], H, E)
-    d_hidden, hp = _give(d_hidden, "d_hidden", (T, H), dtype, d, stream)
+    k = int(k)
+    T, H, E, shape = _gather_backward_shape(d_x_sorted.shape, reverse_indices.shape, offsets.shape, k)
+    d_hidden, hp = _give(d_hidden, "d_hidden", shape, dtype, d, stream)
     space, ws, nb = _space(workspace, moe_gather_rows_backward_workspace_size(T, k), d, stream)
     rc = lib().moe_gather_rows_backward(xp, rp, op, dt, T, H, E, k, hp, ws, nb, _status_ptr(status, d), _raw(stream, d))
     if rc:
@@ -760,6 +774,18 @@ def moe_gather_rows_backward(d_x_sorted, reverse_indices, offsets, k, d_hidden=N
 def moe_ep_combine_backward_workspace_size(T, k) -> int:
     _fits(T, k)
     return int(lib().moe_ep_combine_backward_workspace_size(T, k))
+
+
+@_shapes
+def _combine_backward_shape(d_out, y, weights, reverse, offsets):
+    """(T, k, H, E, shape of the sorted rows)"""
+    if (len(d_out) != 2 or len(weights) != 2 or weights[0] != d_out[0] or reverse != (weights[0] * weights[1],) or len(offsets) != 1
+            or offsets[0] < 2 or (y is not None and y != (weights[0] * weights[1], d_out[1]))):
+        raise ValueError("shapes must be d_out [T, H], y_sorted [T * k, H], topk_weights [T, k], reverse_indices [T * k], "
+                         "offsets [E + 1]")
+    (T, H), k, E = d_out, weights[1], offsets[0] - 1
+    _fits(T * k, H, E)
+    return T, k, H, E, torch.Size((T * k, H))
 
 
 def moe_ep_combine_backward(d_out, y_sorted, topk_weights, reverse_indices, offsets, d_y=None, d_weights=None, workspace=None,
@@ -774,15 +800,10 @@ def moe_ep_combine_backward(d_out, y_sorted, topk_weights, reverse_indices, offs
     rp = _take(reverse_indices, "reverse_indices", _I32, d)
     op = _take(offsets, "offsets", _I32, d)
     dt = _code(dtype)
-    gs, ws_ = d_out.shape, topk_weights.shape
-    if (len(gs) != 2 or len(ws_) != 2 or ws_[0] != gs[0] or reverse_indices.shape != (ws_[0] * ws_[1],) or len(offsets.shape) != 1
-            or offsets.shape[0] < 2 or (y_sorted is not None and y_sorted.shape != (ws_[0] * ws_[1], gs[1]))):
-        raise ValueError("shapes must be d_out [T, H], y_sorted [T * k, H], topk_weights [T, k], reverse_indices [T * k], "
-                         "offsets [E + 1]")
-    (T, H), k, E = gs, ws_[1], offsets.shape[0] - 1
-    _fits(T * k, H, E)
-    d_y, dyp = _give(d_y, "d_y", (T * k, H), dtype, d, stream) if want_d_y else (None, None)
-    d_weights, dwp = _give(d_weights, "d_weights", (T, k), torch.float32, d, stream) if want_d_weights else (None, None)
+    T, k, H, E, rows = _combine_backward_shape(d_out.shape, None if y_sorted is None else y_sorted.shape, topk_weights.shape,
+                                               reverse_indices.shape, offsets.shape)
+    d_y, dyp = _give(d_y, "d_y", rows, dtype, d, stream) if want_d_y else (None, None)
+    d_weights, dwp = _give(d_weights, "d_weights", topk_weights.shape, torch.float32, d, stream) if want_d_weights else (None, None)
     space, ws, nb = _space(workspace, moe_ep_combine_backward_workspace_size(T, k), d, stream)
     rc = lib().moe_ep_combine_backward(gp, yp, wp, rp, op, dt, T, k, H, E, dyp, dwp, ws, nb, _status_ptr(status, d), _raw(stream, d))
     if rc:
@@ -799,6 +820,7 @@ def _pieces(n):
     return -(-n // FP8_BLOCK)
 
 
+@_shapes
 def _fp8_shape(shape, block_rows, name):
     """(matrices, rows, columns, shape of the scales) of values [..., K], or of matrices [..., N, K] with 128 x 128 blocks."""
     if block_rows not in (1, FP8_BLOCK):
@@ -807,10 +829,10 @@ def _fp8_shape(shape, block_rows, name):
         raise ValueError(f"{name} must be [..., K] ([..., N, K] with block_rows {FP8_BLOCK}) with K a multiple of 16")
     K = shape[-1]
     if block_rows == 1:
-        M, N, scales = 1, shape[:-1].numel(), (*shape[:-1], _pieces(K))
+        M, N, scales = 1, shape[:-1].numel(), torch.Size((*shape[:-1], _pieces(K)))
     else:
         M, N = shape[:-2].numel(), shape[-2]
-        scales = (*shape[:-2], _pieces(N), _pieces(K))
+        scales = torch.Size((*shape[:-2], _pieces(N), _pieces(K)))
     _fits(M, N, K, M * N)
     return M, N, K, scales
 
@@ -863,7 +885,7 @@ def moe_rms_norm_fp8(x, weight, residual=None, eps=1e-6, want_normed=False, code
     dt = _code(dtype)
     xs = x.shape
     _, T, H, ss = _fp8_shape(xs, 1, "x")
-    if weight.shape != (H,) or (residual is not None and residual.shape != xs):
+    if weight.shape != xs[-1:] or (residual is not None and residual.shape != xs):
         raise ValueError("shapes must be x [..., H], weight [H], residual as x")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
@@ -877,6 +899,18 @@ def moe_rms_norm_fp8(x, weight, residual=None, eps=1e-6, want_normed=False, code
     return codes, scales, residual_out, normed
 
 
+@_shapes
+def _fp8_gather_shape(codes, scales, ids, offsets):
+    """(T, H, S, E, shapes of the outputs)"""
+    if (len(codes) != 2 or codes[1] % 16 or scales != (codes[0], _pieces(codes[1])) or len(ids) != 1 or len(offsets) != 1
+            or offsets[0] < 2):
+        raise ValueError("shapes must be codes [T, H], scales [T, ceil(H / 128)], sorted_token_ids [S], offsets [E + 1] with H a "
+                         "multiple of 16")
+    (T, H), S, E = codes, ids[0], offsets[0] - 1
+    _fits(T, H, S, E)
+    return T, H, S, E, torch.Size((S, H)), torch.Size((S, _pieces(H)))
+
+
 def moe_fp8_gather_rows(codes, scales, sorted_token_ids, offsets, out=None, out_scales=None, status=None, stream=None):
     """Expert-sorted copies of 8-bit rows -> (codes [S, H], scales [S, ceil(H/128)]), rows p < offsets[E].
 
@@ -888,19 +922,29 @@ def moe_fp8_gather_rows(codes, scales, sorted_token_ids, offsets, out=None, out_
     sp = _take(scales, "scales", _F32, d)
     ip = _take(sorted_token_ids, "sorted_token_ids", _I32, d)
     op = _take(offsets, "offsets", _I32, d)
-    cs, ids = codes.shape, sorted_token_ids.shape
-    if len(cs) != 2 or cs[1] % 16 or scales.shape != (cs[0], _pieces(cs[1])) or len(ids) != 1 or len(offsets.shape) != 1 \
-            or offsets.shape[0] < 2:
-        raise ValueError("shapes must be codes [T, H], scales [T, ceil(H / 128)], sorted_token_ids [S], offsets [E + 1] with H a "
-                         "multiple of 16")
-    (T, H), S, E = cs, ids[0], offsets.shape[0] - 1
-    _fits(T, H, S, E)
-    out, xp = _give(out, "out", (S, H), _F8, d, stream)
-    out_scales, xsp = _give(out_scales, "out_scales", (S, _pieces(H)), _F32, d, stream)
+    T, H, S, E, rows, row_scales = _fp8_gather_shape(codes.shape, scales.shape, sorted_token_ids.shape, offsets.shape)
+    out, xp = _give(out, "out", rows, _F8, d, stream)
+    out_scales, xsp = _give(out_scales, "out_scales", row_scales, _F32, d, stream)
     rc = lib().moe_fp8_gather_rows(cp, sp, ip, op, T, H, E, S, xp, xsp, _status_ptr(status, d), _raw(stream, d))
     if rc:
         _check("moe_fp8_gather_rows", rc)
     return out, out_scales
+
+
+@_shapes
+def _fp8_product_shape(x, x_scales, w, w_scales, offsets, activation):
+    """(S, K, N, E, the activation's code, shape of y)"""
+    if (len(x) != 2 or len(w) != 3 or w[2] != x[1] or x[1] % 16 or x_scales != (x[0], _pieces(x[1]))
+            or w_scales != (w[0], _pieces(w[1]), _pieces(w[2])) or offsets != (w[0] + 1,)):
+        raise ValueError("shapes must be x_codes [S, K], x_scales [S, ceil(K / 128)], w_codes [E, N, K], "
+                         "w_scales [E, ceil(N / 128), ceil(K / 128)], offsets [E + 1] with K a multiple of 16")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
+    (S, K), (E, N, _), act = x, w, _ACTIVATIONS[activation]
+    if act and N % 32:
+        raise ValueError("silu_and_mul needs N to be a multiple of 32")
+    _fits(S, K, N, E)
+    return S, K, N, E, act, torch.Size((S, N // 2 if act else N))
 
 
 def moe_fp8_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activation=None, out_dtype=torch.bfloat16, out=None,
@@ -919,24 +963,8 @@ def moe_fp8_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activati
     wsp = _take(w_scales, "w_scales", _F32, d)
     op = _take(offsets, "offsets", _I32, d)
     dt = _code(out_dtype)
-    xs, wsh = x_codes.shape, w_codes.shape
-    if len(xs) != 2 or len(wsh) != 3:
-        raise ValueError("shapes must be x_codes [S, K], w_codes [E, N, K]")
-    S, K = xs
-    E, N, same = wsh
-    if (same != K or K % 16 or x_scales.shape != (S, _pieces(K)) or w_scales.shape != (E, _pieces(N), _pieces(K))
-            or offsets.shape != (E + 1,)):
-        raise ValueError("shapes must be x_codes [S, K], x_scales [S, ceil(K / 128)], w_codes [E, N, K], "
-                         "w_scales [E, ceil(N / 128), ceil(K / 128)], offsets [E + 1] with K a multiple of 16")
-    if activation not in _ACTIVATIONS:
-        raise ValueError(f"activation must be None or 'silu_and_mul' (got {activation!r})")
-    cols, act = N, _ACTIVATIONS[activation]
-    if act:
-        if N % 32:
-            raise ValueError("silu_and_mul needs N to be a multiple of 32")
-        cols = N // 2
-    _fits(S, K, N, E)
-    out, yp = _give(out, "out", (S, cols), out_dtype, d, stream)
+    S, K, N, E, act, shape = _fp8_product_shape(x_codes.shape, x_scales.shape, w_codes.shape, w_scales.shape, offsets.shape, activation)
+    out, yp = _give(out, "out", shape, out_dtype, d, stream)
     rc = lib().moe_fp8_grouped_gemm(xp, xsp, wp, wsp, S, K, N, E, op, act, dt, yp, _status_ptr(status, d), _raw(stream, d))
     if rc:
         _check("moe_fp8_grouped_gemm", rc)

@@ -29,7 +29,7 @@ constexpr int BOX = 16;                  // rows of x per TMA box
 constexpr int BOX_BYTES = BOX * KB;
 constexpr int MAXF = 128;                // MMA M
 constexpr int MAXR = 64;                 // rows of x per unit (MMA N at most)
-constexpr int MAXHEADS = MOE_MAX_EXPERTS + kFewRows * MOE_MAX_EXPERTS / MAXR;   // (expert, 64 rows) of a launch
+constexpr int MAXHEADS = MOE_MAX_EXPERTS + fp8::kFewRows * MOE_MAX_EXPERTS / MAXR;   // (expert, 64 rows) of a launch
 constexpr int A_READ = MAXF * KB;        // what an MMA reads of its A operand, whatever was loaded
 constexpr int UP = A_READ / 2;           // with the gate: the up rows, after 64 rows of room for the gate's
 constexpr int MAXSTAGE = 20;

@@ -344,7 +344,7 @@ int launch(const Fp8Args& a, cudaStream_t s) {
 }  // namespace
 
 int launch_fp8_grouped(const Fp8Args& a, cudaStream_t s) {
-  if (grouped_few_rows(a.S, a.E)) return launch_fp8_few(a, s);
+  if (fp8::few_rows(a.S, a.E)) return launch_fp8_few(a, s);
   if (a.out_dtype == MOE_F32) return a.silu ? launch<true, float>(a, s) : launch<false, float>(a, s);
   if (a.out_dtype == MOE_BF16) return a.silu ? launch<true, __nv_bfloat16>(a, s) : launch<false, __nv_bfloat16>(a, s);
   return a.silu ? launch<true, __half>(a, s) : launch<false, __half>(a, s);

@@ -111,9 +111,13 @@ __device__ __forceinline__ void take_positions(const Args& a, int s0, int count,
   if (a.pos == nullptr) {
     for (int i = threadIdx.x; i < count; i += kThreads) pos[i] = -1;
     __syncthreads();
-    for (int p = threadIdx.x; p < n; p += kThreads) {
-      const int i = __ldg(a.reverse + p) - s0;
-      if (i >= 0 && i < count) pos[i] = p;
+    for (int p0 = threadIdx.x; p0 < n; p0 += 8 * kThreads) {
+      int s[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = p0 + i * kThreads < n ? __ldg(a.reverse + p0 + i * kThreads) : -1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s[i] >= s0 && s[i] - s0 < count) pos[s[i] - s0] = p0 + i * kThreads;
     }
   } else {
     for (int i = threadIdx.x; i < count; i += kThreads) {

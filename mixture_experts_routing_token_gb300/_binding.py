@@ -452,7 +452,8 @@ def _first(t, name):
     index = t.get_device()
     if index < 0 or not t.is_contiguous():
         _refuse(t, name, None, index)
-    _on_current(index, name)
+    if index != _current_device():
+        _on_current(index, name)
     return t.data_ptr(), t.dtype, index
 
 
@@ -471,10 +472,13 @@ def _give(t, name, shape, dtype, index, stream):
     if t is None:
         t = _new(shape, dtype, index, stream)
         return t, t.data_ptr()
-    p = _take(t, name, dtype, index)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    return t, p
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.is_contiguous() and t.shape == shape:
+            return t, t.data_ptr()
+    except AttributeError:      # not a tensor
+        pass
+    _take(t, name, dtype, index)
+    raise ValueError(f"{name} must have shape {tuple(shape)}")
 
 
 def _status_ptr(status, index):

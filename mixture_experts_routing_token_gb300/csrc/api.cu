@@ -162,10 +162,19 @@ int g_nranges = 0, g_next_range = 0;
 
 bool is_device_ptr(const void* p) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  // this thread's last answers in front of the shared list: a call asks for up to ten pointers, mostly of a few ranges
+  static thread_local DevRange last[8] = {};
+  static thread_local int next_last = 0;
+  for (const DevRange& r : last)
+    if (a >= r.lo && a < r.hi) return true;
   {
     std::lock_guard<std::mutex> lk(g_range_mu);
     for (int i = 0; i < g_nranges; ++i)
-      if (a >= g_ranges[i].lo && a < g_ranges[i].hi) return true;
+      if (a >= g_ranges[i].lo && a < g_ranges[i].hi) {
+        last[next_last] = g_ranges[i];
+        next_last = (next_last + 1) % 8;
+        return true;
+      }
   }
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {

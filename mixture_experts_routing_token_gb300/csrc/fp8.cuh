@@ -8,11 +8,10 @@ namespace fp8 {
 
 constexpr int BLOCK = 128;       // values along a row (and rows of a weight matrix) that share a scale
 
-// Whether a product takes the weight-streaming kernel: up to 44 rows per expert on average. Measured, us, that kernel /
-// the SM-pair kernel, 64 experts [2816, 2048]: with the gate 68 / 96 at 16 rows, 84 / 97 at 32, 93 / 97 at 40, 104 / 98
-// at 48; without 62 / 90, 73 / 91, 79 / 92, 87 / 93, and 124 / 94 at 64; 8 experts [14336, 4096] 79 / 104 at 32, 92 / 107
-// at 48, 136 / 109 at 64.
-constexpr int kFewRows = 44;
+// Whether a product takes the weight-streaming kernel: up to 48 rows per expert on average. Measured, us, that kernel /
+// the SM-pair kernel, 64 experts [2816, 2048]: with the gate 65 / 95 at 16 rows, 72 / 96 at 32, 85 / 97 at 48, 118 / 97
+// at 64; without 61 / 89, 71 / 92, 85 / 93, 122 / 95; 8 experts [14336, 4096] 78 / 102 at 32, 91 / 106 at 48, 136 / 107 at 64.
+constexpr int kFewRows = 48;
 inline bool few_rows(int S, int E) { return S <= (long)kFewRows * E; }
 
 __host__ __device__ constexpr int blocks(int n) { return (n + BLOCK - 1) / BLOCK; }

@@ -41,7 +41,8 @@ def f64(t):
 
 
 SIZES = [(1, 1, 8, 0), (1, 4, 1, 1), (3, 2, 64, 0), (77, 2, 1001, 9), (40, 4, 2048, 0), (300, 3, 136, 100), (9, 4, 4096, 0),
-         (1100, 2, 24, 5), (600, 4, 33, 0), (2000, 4, 16, 7999), (513, 4, 8200, 3), (5, 4, 20000, 2), (700, 3, 7, 11)]
+         (1100, 2, 24, 5), (600, 4, 33, 0), (2000, 4, 16, 7999), (513, 4, 8200, 3), (5, 4, 20000, 2), (700, 3, 7, 11),
+         (2500, 4, 24, 5), (2500, 4, 33, 9999), (9000, 1, 40, 100), (2100, 1, 72, 0)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -155,7 +156,7 @@ def test_bad_routing_is_reported_and_stays_in_bounds(T):
         assert int(status) == moe.MOE_STATUS_BAD_INDEX
 
 
-@pytest.mark.parametrize("T", [40, 1500])
+@pytest.mark.parametrize("T", [40, 1500, 2600])
 def test_in_a_graph(T):
     moe = need_gpu()
     k, H = 4, 256
@@ -181,9 +182,9 @@ def test_in_a_graph(T):
 def test_a_workspace_that_holds_other_positions():
     """What an earlier call left in the workspace names no rows."""
     moe = need_gpu()
-    T, k, H = 1500, 4, 64
+    T, k, H = 2600, 4, 64
     ws = torch.zeros(moe.moe_gather_rows_backward_workspace_size(T, k), dtype=torch.uint8, device=DEV)
-    for seed, dropped in ((0, 0), (1, 3000), (2, 5999), (3, 0)):
+    for seed, dropped in ((0, 0), (1, 3000), (2, 10399), (3, 0)):
         reverse, off, n = routing(T, k, dropped, seed)
         d_x = torch.randn(T * k, H, device=DEV)
         rg, og = torch.from_numpy(reverse).to(DEV), torch.from_numpy(off).to(DEV)

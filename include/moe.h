@@ -425,8 +425,9 @@ MOE_API int moe_fp8_gather_rows(const uint8_t* codes, const float* scales, const
  *   of 16, as the next product's K): y [S, N / 2] = silu(columns 0 .. N/2 - 1) *
  *   (columns N/2 .. N - 1) (silu of arguments below -87 is 0). y is of out_dtype
  *   (any of the three), rounded once.
- * Within a block the tensor cores add with truncation; the blocks' sums are added
- * rounded to nearest. offsets, rows without an expert and status as
+ * Within a block the tensor cores add with truncation; the blocks' sums are scaled
+ * by the product of their two scales (formed first, in float32: it should be a
+ * normal number) and added rounded to nearest. offsets, rows without an expert and status as
  * moe_grouped_gemm. No workspace.
  */
 MOE_API int moe_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes,
@@ -502,7 +503,8 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
  * outside it sets MOE_STATUS_BAD_INDEX (the results of the slots concerned are
  * undefined). No atomics on the outputs: equal calls give equal bits.
  * ws / ws_bytes: at least the matching *_workspace_size(T, k) bytes (0 for small
- * calls: then ws may be null).
+ * calls: then ws may be null); calls that may run at the same time need separate
+ * workspaces.
  */
 MOE_API size_t moe_gather_rows_backward_workspace_size(int T, int k);
 MOE_API int moe_gather_rows_backward(const void* d_x_sorted, const int32_t* reverse_indices, const int32_t* offsets,

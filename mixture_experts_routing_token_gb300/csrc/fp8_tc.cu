@@ -5,13 +5,21 @@
 //   (with the gate, silu(y[p, n]) y[p, N/2 + n])
 //
 // The scales are any float32, so the tensor cores cannot apply them. An accumulator holds one block (K = 128, four
-// MMAs); the epilogue warps read it, multiply by sx sw and add in registers, while the next block goes into the other
-// accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside
-// a block see the tensor cores' truncating additions.
+// MMAs); the epilogue warps read it, multiply by sx sw (one float32 product) and add in registers, while the next block
+// goes into the other accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside a block see the
+// tensor cores' truncating additions.
 //
 // Each SM of the pair loads its own 128 of a tile's 256 rows of x and half of its 256 rows of w per block (128 bytes
 // a row, the layout 128-byte swizzled TMA writes); with the gate SM 0 holds 128 gate rows and SM 1 the matching up
-// rows, so a TMEM lane has both.
+// rows, so a TMEM lane has both. Eight epilogue warps keep 128 sums a thread, for which the other warps give up
+// registers.
+//
+// Bound at prompt sizes by the way of an accumulator: four MMAs (512 cycles), their commit, the read and the sums (356
+// cycles for both SMs' quarters at best), the hand-back, the next issue. Tensor memory holds two, so a block takes about
+// half of that round trip, 900 to 1000 cycles, where the tensor cores need 512 and the operands 490 (tensor pipe 46%
+// busy). 131072 rows, 64 experts of [2816, 2048] with the gate: 700 us on a cold GPU (2.16 PFLOP/s), 720 to 750 in a long
+// run. Of that the single multiply-adds were worth 4% (two values an instruction move them into pairs first), the
+// register split 5%, loading a tile's first scales before the last tile's stores 7%.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -46,7 +54,7 @@ struct Params {
   const int32_t* offsets;
   const float* x_scales;
   const float* w_scales;
-  int S, E, N;
+  int S, E;
   int kb, nb;       // blocks along K and N
   int cols;         // of y
   int NT;
@@ -310,10 +318,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
+// The epilogue's warps wait for the registers that they ask for, so a block has to start with as many as the split needs
+// in all: with the register limit of its launch bounds, which a kernel that moves registers is compiled for. Asked once.
+template <bool SILU, class T>
+bool enough_registers() {
+  static const bool enough = [] {
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, fp8_pair_kernel<SILU, T>) != cudaSuccess) return false;
+    return at.numRegs * (EPI0 + EPI_WARPS) >= EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS;
+  }();
+  return enough;
+}
+
 template <bool SILU, class T>
 int launch(const Fp8Args& a, cudaStream_t s) {
   const char* name = "fp8_grouped_gemm";
   if (int rc = ensure_smem_limit(fp8_pair_kernel<SILU, T>, DSMEM, name)) return rc;
+  if (!enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
   CUtensorMap tx, tw;
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;
@@ -324,7 +345,6 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   p.w_scales = a.w_scales;
   p.S = a.S;
   p.E = a.E;
-  p.N = a.N;
   p.kb = fp8::blocks(a.K);
   p.nb = fp8::blocks(a.N);
   p.cols = SILU ? a.N / 2 : a.N;

@@ -112,31 +112,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// The same for roles that wait often: the thread is parked until the phase completes, 20 us at most a time, instead of
-// coming back for another try at the hardware's own pace.
-__device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (limit_ns < kShortWaitNs) return mbar_wait(bar, parity, abort, limit_ns);
-  uint64_t t0 = 0;
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if (*abort) return false;
-    const uint64_t t = globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
 // ---- TMA -------------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {

@@ -395,3 +395,47 @@ def test_a_wait_that_runs_out_is_reported(silu, counts):
     finally:
         moe.set_wait_limit_ns(before)
     assert torch.equal(moe.moe_fp8_grouped_gemm(*args, activation=act), want)
+
+
+def test_rows_past_2_to_the_31():
+    """Codes, values, sorted rows and operands of more than 2^31 elements: the last rows as those of small calls."""
+    moe = need_gpu()
+    K, T = 2048, (1 << 20) + 5
+    g = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.empty(T, K, dtype=torch.bfloat16, device=DEV)
+    x[-300:] = torch.randn(300, K, generator=g, device=DEV)
+    codes, scales = moe.moe_fp8_quantize(x)
+    few = moe.moe_fp8_quantize(x[-300:].contiguous())
+    assert torch.equal(bits_t(codes[-300:]), bits_t(few[0])) and torch.equal(scales[-300:], few[1])
+    values = moe.moe_fp8_dequantize(codes, scales, out=x)
+    assert torch.equal(values[-300:], moe.moe_fp8_dequantize(*few))
+    w = moe.moe_fp8_quantize(torch.randn(2, 32, K, generator=g, device=DEV), block_rows=128)
+    for split in (T - 3, T - 290):          # the last expert has 3 rows or 290
+        off = torch.tensor([0, split, T], dtype=torch.int32, device=DEV)
+        y = moe.moe_fp8_grouped_gemm(codes, scales, *w, off)
+        n = T - split
+        # the same kernel on the last rows alone: a first expert with enough rows
+        head = 300 - n if n > 200 else 297
+        small = torch.tensor([0, head, head + n], dtype=torch.int32, device=DEV)
+        last = (codes[T - head - n:].contiguous(), scales[T - head - n:].contiguous())
+        assert torch.equal(y[-n:], moe.moe_fp8_grouped_gemm(*last, *w, small)[-n:])
+    ids = torch.arange(T, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    out, out_scales = moe.moe_fp8_gather_rows(codes, scales, ids, torch.tensor([0, T], dtype=torch.int32, device=DEV))
+    assert torch.equal(bits_t(out[:300]), bits_t(codes[-300:].flip(0))) and torch.equal(out_scales[:300], scales[-300:].flip(0))
+    assert torch.equal(bits_t(out[-300:]), bits_t(codes[:300].flip(0)))
+
+
+def test_calls_on_two_streams_at_once():
+    moe = need_gpu()
+    cases = [(operands(c, 1024, 320, seed=s), act) for s, (c, act) in enumerate((([300, 0, 120], None), ([5, 3, 9], None),
+                                                                              ([300, 90, 7], "silu_and_mul"), ([2, 8, 1], "silu_and_mul")))]
+    args = [((*to_gpu(x), *to_gpu(w), torch.from_numpy(off).to(DEV)), act) for (x, w, off), act in cases]
+    want = [moe.moe_fp8_grouped_gemm(*a, activation=act) for a, act in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = []
+    for _ in range(5):
+        for (a, act), s in zip(args, streams):
+            got.append(moe.moe_fp8_grouped_gemm(*a, activation=act, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i], want[i % 4]) for i in range(len(got)))

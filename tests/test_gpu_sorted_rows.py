@@ -198,3 +198,51 @@ def test_a_workspace_that_holds_other_positions():
     want = torch.zeros(T * k)
     want[torch.from_numpy(reverse[:n]).long()] = H
     assert torch.equal(d_w.cpu().reshape(-1), want)
+
+
+def test_rows_past_2_to_the_31():
+    moe = need_gpu()
+    T, k, H = (1 << 19) + 3, 2, 2048
+    S = T * k
+    rev = torch.arange(S, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    off = torch.tensor([0, 5, S], dtype=torch.int32, device=DEV)
+    y = torch.empty(S, H, dtype=torch.bfloat16, device=DEV)
+    y[:200], y[-200:] = torch.randn(200, H, device=DEV), torch.randn(200, H, device=DEV)
+    d_out = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+    d_out[:100], d_out[-100:] = torch.randn(100, H, device=DEV), torch.randn(100, H, device=DEV)
+    w = torch.rand(T, k, device=DEV)
+    d_y, d_w = moe.moe_ep_combine_backward(d_out, y, w, rev, off)
+    d_h = moe.moe_gather_rows_backward(y, rev, off, k)
+    # slot s lies in row S - 1 - s: the last tokens in the first rows and the other way round
+    for tokens, rows in ((slice(0, 100), slice(S - 200, S)), (slice(T - 100, T), slice(0, 200))):
+        d, v, p = d_out[tokens].double(), y[rows].double().flip(0).reshape(100, k, H), w[tokens].double()
+        got = d_y[rows].double().flip(0).reshape(100, k, H)
+        want = p[:, :, None] * d[:, None]
+        assert ((got - want).abs() <= (2.0 ** -24 + 1.01 * half(torch.bfloat16)) * want.abs() + least(torch.bfloat16)).all()
+        mag = (d[:, None].abs() * v.abs()).sum(2)
+        assert ((d_w[tokens].double() - (d[:, None] * v).sum(2)).abs() <= (H // 32 + 14) * 2.0 ** -24 * mag).all()
+        total, mag = v.sum(1), v.abs().sum(1)
+        assert ((d_h[tokens].double() - total).abs() <= k * 2.0 ** -24 * mag + 1.01 * half(torch.bfloat16) * mag).all()
+
+
+def test_calls_on_two_streams_at_once():
+    moe = need_gpu()
+    cases = []
+    for seed, (T, k, H) in enumerate(((40, 4, 256), (2600, 4, 256), (300, 2, 1001), (9000, 1, 64))):
+        reverse, off, n = routing(T, k, 7, seed)
+        d_out, y, d_x, w = (t.to(DEV) for t in tensors(T, k, H, torch.bfloat16, seed))
+        cases.append((d_out, y, d_x, w, torch.from_numpy(reverse).to(DEV), torch.from_numpy(off).to(DEV), k))
+
+    def run(d_out, y, d_x, w, rg, og, k, s):
+        return (*moe.moe_ep_combine_backward(d_out, y, w, rg, og, d_y=torch.zeros_like(y) if s is None else None, stream=s),
+                moe.moe_gather_rows_backward(d_x, rg, og, k, stream=s))
+
+    want = [run(*c, None) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [run(*c, s) for _ in range(5) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        c, w = cases[i % 4], want[i % 4]
+        n = int(c[5][-1])
+        assert torch.equal(g[0][:n], w[0][:n]) and torch.equal(g[1], w[1]) and torch.equal(g[2], w[2])

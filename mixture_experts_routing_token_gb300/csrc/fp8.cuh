@@ -8,10 +8,11 @@ namespace fp8 {
 
 constexpr int BLOCK = 128;       // values along a row (and rows of a weight matrix) that share a scale
 
-// Whether a product takes the weight-streaming kernel: up to 48 rows per expert on average. Measured, us, that kernel /
-// the SM-pair kernel, 64 experts [2816, 2048]: with the gate 65 / 95 at 16 rows, 72 / 96 at 32, 85 / 97 at 48, 118 / 97
-// at 64; without 61 / 89, 71 / 92, 85 / 93, 122 / 95; 8 experts [14336, 4096] 78 / 102 at 32, 91 / 106 at 48, 136 / 107 at 64.
-constexpr int kFewRows = 48;
+// Whether a product takes the weight-streaming kernel: up to 8 rows per expert on average. Measured, us, that kernel / the
+// tiled one: one row of 8 experts, 64 experts [2816, 2048] with the gate 15 / 19; 2 experts, [2816, 2048] 8.9 / 11.3,
+// [14336, 4096] 25 / 33; 4 rows an expert, 8 experts [2816, 2048] 15 / 17, 64 experts 62 / 62; 8 rows, 64 experts [2048, 1408]
+// 34 / 37; 16 rows, 64 experts [2816, 2048] 65 / 64, 8 experts 16 / 14; 32 rows 72 / 65 and 19 / 14.
+constexpr int kFewRows = 8;
 inline bool few_rows(int S, int E) { return S <= (long)kFewRows * E; }
 
 __host__ __device__ constexpr int blocks(int n) { return (n + BLOCK - 1) / BLOCK; }
@@ -47,22 +48,13 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T over K = 32.
-template <int CTAS>
 __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CTAS == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 }  // namespace fp8

@@ -10,8 +10,8 @@
 //   warp 0     TMA producer: per block of 128 of the reduction one box of f rows of w (two with the gate), boxes of 16
 //              rows of x, through a ring whose stages are as large as the launch's units need;
 //   warp 1     MMA issuer (M = 128, N = 16 .. 64, four K = 32 a block), a block to an accumulator;
-//   warps 2-   epilogue (four warps, with the gate eight): multiply an accumulator by sx sw and add it in registers; at
-//              the end of a unit a warp stores 32 neighbouring columns of a row at a time.
+//   warps 2-5  epilogue: multiply an accumulator by sx sw and add it in registers; at the end of a unit a warp stores 32
+//              neighbouring columns of a row at a time.
 // Blocks go to the epilogue four at a time (2 x 4 x 64 columns of tensor memory): a hand-over takes the epilogue some
 // 500 cycles beside the sums, and one per block, 16 KB of weights, held the whole kernel at 4.8 TB/s.
 // f is chosen on the host as for the 16-bit products (grouped_few.cu).
@@ -33,17 +33,9 @@ constexpr int MAXHEADS = MOE_MAX_EXPERTS + fp8::kFewRows * MOE_MAX_EXPERTS / MAX
 constexpr int A_READ = MAXF * KB;        // what an MMA reads of its A operand, whatever was loaded
 constexpr int UP = A_READ / 2;           // with the gate: the up rows, after 64 rows of room for the gate's
 constexpr int MAXSTAGE = 20;
-// Sets of four epilogue warps, 16 rows of x each by turns. Measured, us, one / two, 64 experts of [2816, 2048]: with the
-// gate 61 / 61 at 4 rows an expert, 70 / 65 at 24, 81 / 72 at 32, 90 / 82 at 40; without (at most 168 registers a thread
-// are too few for two) 62 / 64 at 24, 71 / 75 at 32, 77 / 80 at 40.
-template <bool SILU>
-constexpr int sets() { return SILU ? 2 : 1; }
-template <bool SILU>
-constexpr int threads() { return (2 + 4 * sets<SILU>()) * 32; }
-template <bool SILU>
-constexpr int ring() { return (SILU ? 200 : 208) * 1024; }
-template <bool SILU>
-constexpr int dsmem_bytes() { return ring<SILU>() + 1024; }
+constexpr int THREADS = 192;
+constexpr int RING = 204 * 1024;
+constexpr int DSMEM = RING + 1024;
 constexpr int CHUNK = 4;                 // blocks that are handed to the epilogue together, each in columns of its own
 constexpr uint32_t ACC_COLS = CHUNK * MAXR, TMEM_COLS = 2 * ACC_COLS;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
@@ -92,9 +84,8 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
 }
 
 template <bool SILU, class T>
-__global__ void __launch_bounds__(threads<SILU>(), 1)
+__global__ void __launch_bounds__(THREADS, 1)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params P) {
-  constexpr int SETS = sets<SILU>(), RING = ring<SILU>();
   __shared__ __align__(8) uint64_t full_bar[MAXSTAGE], empty_bar[MAXSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
@@ -102,8 +93,8 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
   __shared__ int s_most;
   __shared__ grouped::Groups G;
   __shared__ uint16_t expert_of[MAXHEADS];
-  __shared__ float up_part[SILU ? SETS : 1][SILU ? 64 : 1][17];      // up columns of 16 rows, on their way to the gate's warps
-  __shared__ __align__(16) float x_part[4 * SETS][CHUNK][MAXR / SETS];      // a chunk's scales of the rows, of each warp's own
+  __shared__ float up_part[SILU ? 64 : 1][17];      // up columns of 16 rows, on their way to the gate's warps
+  __shared__ __align__(16) float x_part[4][CHUNK][MAXR];      // a chunk's scales of the rows, of each warp's own
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -117,7 +108,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&tfull_bar[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), 4 * SETS);
+      ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), 4);
     }
     ptx::mbar_init(ptx::smem_u32(&drain_bar), 1);
     abort_flag = 0;
@@ -194,7 +185,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS + k % CHUNK * MAXR);
           const uint64_t ad = ptx::sdesc_k128(st(stage)), bd = ptx::sdesc_k128(st(stage) + a_bytes);
 #pragma unroll
-          for (int kk = 0; kk < KB / 32; ++kk) fp8::mma<1>(d_tmem, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
+          for (int kk = 0; kk < KB / 32; ++kk) fp8::mma(d_tmem, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
           ptx::mma_commit(ptx::smem_u32(&empty_bar[stage]));
           if (++stage == nstage) { stage = 0; ph ^= 1u; }
           if (k % CHUNK == CHUNK - 1 || k == P.kb - 1) {
@@ -211,24 +202,20 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int l = q * 32 + lane;         // row of the A operand
-    const int set = SETS == 1 ? 0 : (warp - 2) >> 2;     // 16 rows of x in 16 SETS
-    auto& xp = x_part[set * 4 + q];
+    auto& xp = x_part[q];
     T* y = static_cast<T*>(P.y);
     int acc = 0;
     uint32_t aph = 0;
     // A unit's scales: `load` fetches a chunk's while the last one is added, a unit's first ones before the last unit's
-    // results are stored (loaded where they are used: 24 rows an expert, 64 experts of [2816, 2048] with the gate, 75 us
-    // instead of 70).
+    // results are stored.
     const float *ws, *xs0, *xs1;             // of this lane's row of w, and of two rows of x
     bool more = false;                       // rows in the second 32
     float w[CHUNK], x0[CHUNK], x1[CHUNK];
     auto locate = [&](const Unit& u) {
       const int wrow = !SILU || l < 64 ? u.n0 + l : P.cols + u.n0 + l - 64;
       ws = P.w_scales + ((long)u.e * P.nb + min(wrow / KB, P.nb - 1)) * P.kb;
-      // entry i of a set's scales: row 32 (i / 16) + 16 set + i % 16 of two sets, row i of one
-      const int r = SETS == 2 ? set * 16 + (lane & 15) + 2 * (lane & 16) : lane;
-      xs0 = P.x_scales + (long)(u.row + min(r, u.rows - 1)) * P.kb;
-      xs1 = P.x_scales + (long)(u.row + min(r + 32, u.rows - 1)) * P.kb;
+      xs0 = P.x_scales + (long)(u.row + min(lane, u.rows - 1)) * P.kb;
+      xs1 = P.x_scales + (long)(u.row + min(lane + 32, u.rows - 1)) * P.kb;
       more = u.rows > 32;
     };
     auto load = [&](int k0) {
@@ -237,7 +224,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
         const int k = min(k0 + i, P.kb - 1);
         w[i] = __ldg(ws + k);
         x0[i] = __ldg(xs0 + k);
-        x1[i] = SETS == 1 && more ? __ldg(xs1 + k) : 0.0f;
+        x1[i] = more ? __ldg(xs1 + k) : 0.0f;
       }
     };
     Unit u{};
@@ -247,9 +234,9 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
       load(0);
     }
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      float sum[MAXR / SETS];
+      float sum[MAXR];
 #pragma unroll
-      for (int j = 0; j < MAXR / SETS; ++j) sum[j] = 0.0f;
+      for (int j = 0; j < MAXR; ++j) sum[j] = 0.0f;
       bool ok = true;
       for (int k0 = 0; k0 < P.kb && ok; k0 += CHUNK) {
         float cw[CHUNK];
@@ -258,7 +245,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
         for (int i = 0; i < CHUNK; ++i) {
           cw[i] = w[i];
           xp[i][lane] = x0[i];
-          if (SETS == 1 && more) xp[i][(lane + 32) % (MAXR / SETS)] = x1[i];
+          if (more) xp[i][lane + 32] = x1[i];
         }
         __syncwarp();
         if (k0 + CHUNK < P.kb) load(k0 + CHUNK);
@@ -268,12 +255,12 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
         ptx::tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
 #pragma unroll
-        for (int c = 0; c < MAXR / SETS; c += 16) {
-          if (c * SETS + set * 16 >= u.rows) continue;
+        for (int c = 0; c < MAXR; c += 16) {
+          if (c >= u.rows) continue;
           uint32_t v[CHUNK][16];
 #pragma unroll
           for (int i = 0; i < CHUNK; ++i)
-            if (k0 + i < P.kb) ptx::tmem_ld16(taddr + i * MAXR + c * SETS + set * 16, v[i]);
+            if (k0 + i < P.kb) ptx::tmem_ld16(taddr + i * MAXR + c, v[i]);
 #pragma unroll
           for (int i = 0; i < CHUNK; ++i) {
             if (k0 + i >= P.kb) continue;
@@ -294,7 +281,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
         if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       // every epilogue warp sees the same outcome: the gate's exchange needs all four
-      if (SILU) ok = !named_bar_or(1 + set, 128, !ok);
+      if (SILU) ok = !named_bar_or(1, 128, !ok);
       if (!ok) break;
       const int rows = u.rows, cols = u.cols;
       T* dst = y + (long)u.row * P.cols + u.n0;
@@ -304,27 +291,26 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
         load(0);
       }
 #pragma unroll
-      for (int c = 0; c < MAXR / SETS; c += 16) {
-        const int r0 = c * SETS + set * 16;      // 16 rows of x
-        if (r0 >= rows) continue;
+      for (int c = 0; c < MAXR; c += 16) {
+        if (c >= rows) continue;
         if (SILU) {
           if (l >= 64) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) up_part[set][l - 64][j] = sum[c + j];
+            for (int j = 0; j < 16; ++j) up_part[l - 64][j] = sum[c + j];
           }
-          ptx::named_bar_sync(1 + set, 128);
+          ptx::named_bar_sync(1, 128);
         }
         if (l < cols) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (r0 + j < rows)
-              dst[(long)(r0 + j) * P.cols + l] = from_float<T>(SILU ? mx::silu_fast(sum[c + j]) * up_part[set][l][j] : sum[c + j]);
+            if (c + j < rows)
+              dst[(long)(c + j) * P.cols + l] = from_float<T>(SILU ? mx::silu_fast(sum[c + j]) * up_part[l][j] : sum[c + j]);
         }
-        if (SILU) ptx::named_bar_sync(1 + set, 128);
+        if (SILU) ptx::named_bar_sync(1, 128);
       }
     }
     if (!*abort_p)
-      grouped::zero_unowned(y, G, P.E, P.S, P.cols, (long)blockIdx.x * (128 * SETS) + tid - 64, (long)gridDim.x * (128 * SETS));
+      grouped::zero_unowned(y, G, P.E, P.S, P.cols, (long)blockIdx.x * 128 + tid - 64, (long)gridDim.x * 128);
   }
 
   if (*abort_p) {   // after a timeout, let copies in flight land before the shared memory is released
@@ -347,7 +333,7 @@ __global__ void __launch_bounds__(threads<SILU>(), 1)
 template <bool SILU, class T>
 int launch(const Fp8Args& a, cudaStream_t s) {
   const char* name = "fp8_grouped_few";
-  if (int rc = ensure_smem_limit(fp8_few_kernel<SILU, T>, dsmem_bytes<SILU>(), name)) return rc;
+  if (int rc = ensure_smem_limit(fp8_few_kernel<SILU, T>, DSMEM, name)) return rc;
   CUtensorMap tw, tx;
   int rc;
   Params p{};
@@ -366,7 +352,7 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(fp8_few_kernel<SILU, T>, num_sms(), threads<SILU>(), dsmem_bytes<SILU>(), s, tw, tx, p);
+  const cudaError_t e = launch_pdl(fp8_few_kernel<SILU, T>, num_sms(), THREADS, DSMEM, s, tw, tx, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }

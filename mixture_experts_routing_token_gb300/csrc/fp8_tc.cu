@@ -1,5 +1,5 @@
-// Products of 8-bit rows grouped by expert on SM pairs (tcgen05.mma.cta_group::2, kind::f8f6f4, M = 256 x N = 256 x
-// K = 32, float32 accumulators in TMEM), with a scale for every 128 values of a row and 128 x 128 of a matrix:
+// Products of 8-bit rows grouped by expert (tcgen05.mma.kind::f8f6f4, M = 128 x N = 256 x K = 32, float32 accumulators in
+// TMEM), with a scale for every 128 values of a row and 128 x 128 of a matrix:
 //
 //   y[p, n] = sum over blocks b of sx[p, b] sw[e, n / 128, b] sum over k in b of cx[p, k] cw[e, n, k]
 //   (with the gate, silu(y[p, n]) y[p, N/2 + n])
@@ -9,17 +9,16 @@
 // goes into the other accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside a block see the
 // tensor cores' truncating additions.
 //
-// Each SM of the pair loads its own 128 of a tile's 256 rows of x and half of its 256 rows of w per block (128 bytes
-// a row, the layout 128-byte swizzled TMA writes); with the gate SM 0 holds 128 gate rows and SM 1 the matching up
-// rows, so a TMEM lane has both. Eight epilogue warps keep 128 sums a thread, for which the other warps give up
-// registers.
+// One CTA per SM takes tiles of 128 rows of x and 256 of w by turns; with the gate these are 128 gate rows and the
+// matching up rows, so a TMEM lane has both. Eight epilogue warps keep 128 sums a thread, for which the other warps give
+// up registers. Tiles of 256 rows on SM pairs load a third less and were no faster, for a pair's accumulator takes longer to
+// come and go and an expert's last rows fill more of a tile: us, SM pairs / this, 131072 rows of 64 experts, [2816, 2048]
+// with the gate 731 / 707, [2048, 1408] without 394 / 397 to 412; 64 rows an expert 96 / 65.
 //
 // Bound at prompt sizes by the way of an accumulator: four MMAs (512 cycles), their commit, the read and the sums (356
-// cycles for both SMs' quarters at best), the hand-back, the next issue. Tensor memory holds two, so a block takes about
-// half of that round trip, 900 to 1000 cycles, where the tensor cores need 512 and the operands 490 (tensor pipe 46%
-// busy). 131072 rows, 64 experts of [2816, 2048] with the gate: 700 us on a cold GPU (2.16 PFLOP/s), 720 to 750 in a long
-// run. Of that the single multiply-adds were worth 4% (two values an instruction move them into pairs first), the
-// register split 5%, loading a tile's first scales before the last tile's stores 7%.
+// cycles), the hand-back, the next issue. Tensor memory holds two, so a block takes about half of that round trip, 1100
+// to 1200 cycles. 131072 rows, 64 experts of [2816, 2048] with the gate: 675 us on a cold GPU (2.24 PFLOP/s), 700 to 710
+// in a long run. At 64 rows an expert it is HBM: 65 us, 5.9 TB/s.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -29,15 +28,13 @@
 namespace moe {
 namespace {
 
-using namespace pair;
-
-constexpr int BM = 128;                 // rows of x per SM (256 per pair)
+constexpr int BM = 128;                 // rows of x per tile
 constexpr int BN = 256;                 // rows of w per tile
-constexpr int HALF = BN / 2;            // per SM
+constexpr int HALF = BN / 2;            // with the gate: gate rows, and as many up rows
 constexpr int KB = fp8::BLOCK;          // bytes of a row per step
-constexpr int NSTAGE = 6;
+constexpr int NSTAGE = 4;
 constexpr int A_BYTES = BM * KB;
-constexpr int STAGE = A_BYTES + HALF * KB;
+constexpr int STAGE = A_BYTES + BN * KB;
 constexpr int DSMEM = NSTAGE * STAGE + 1024;
 constexpr int PARTS = 2;                // epilogue warps per TMEM lane quarter
 constexpr int EPI_WARPS = 4 * PARTS;
@@ -69,7 +66,7 @@ struct Tile {
   grouped::Span g;
 };
 
-__device__ __forceinline__ int mtiles(int rows) { return (rows + 2 * BM - 1) / (2 * BM); }
+__device__ __forceinline__ int mtiles(int rows) { return (rows + BM - 1) / BM; }
 
 // Tiles of an expert that run together share the operand with fewer tiles, which stays in L2, while the other one is
 // walked once.
@@ -95,8 +92,8 @@ struct Scales {
 };
 
 template <bool SILU, class T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params P) {
+__global__ void __launch_bounds__(THREADS, 1)
+    fp8_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params P) {
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
@@ -105,9 +102,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t dsmem_raw[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
-  const bool leader = rank == 0;
-  const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   const uint32_t dsmem = (ptx::smem_u32(dsmem_raw) + 1023u) & ~1023u;
   auto st = [&](int s) { return dsmem + (uint32_t)(s * STAGE); };
   volatile int* abort_p = &abort_flag;
@@ -119,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(ptx::smem_u32(&tfull_bar[b]), 1);
-      ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), 2 * EPI_WARPS);
+      ptx::mbar_init(ptx::smem_u32(&tempty_bar[b]), EPI_WARPS);
     }
     ptx::mbar_init(ptx::smem_u32(&drain_bar), 1);
     abort_flag = 0;
@@ -129,57 +123,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ptx::prefetch_tmap(&tmX);
     ptx::prefetch_tmap(&tmW);
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     ptx::smem_u32(&tmem_slot)),
-                 "r"(TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), TMEM_COLS);
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2)
     grouped::group_list(P.offsets, P.E, P.S, [&](int rows) { return mtiles(rows) * P.NT; }, G);
   ptx::tc_fence_before();
   __syncthreads();
-  cluster_sync();      // barriers of both CTAs initialised before any cross-CTA signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const int total = G.start[P.E];
 
   if (warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOW_REGS));
   if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+    // ------------------------------------------------------------ producer
     if (ptx::elect_one()) {
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = cluster_id, e = 0; t < total && ok; t += nclusters) {
+      for (int t = (int)blockIdx.x, e = 0; t < total && ok; t += (int)gridDim.x) {
         const Tile ti = tile_at(t, e, G, P);
-        const int a_row = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM;
-        const int b_row = SILU ? ti.n * HALF + (int)rank * P.cols : ti.n * BN + (int)rank * HALF;
+        const int a_row = ti.g.lo + ti.m * BM;
+        const int b_row = SILU ? ti.n * HALF : ti.n * BN;
         for (int k = 0; k < P.kb; ++k) {
           if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[stage]), ph ^ 1u, abort_p, P.wait_ns)) {
             ok = false;
             break;
           }
-          const uint32_t fb_local = ptx::smem_u32(&full_bar[stage]);
-          if (leader) ptx::mbar_arrive_expect_tx(fb_local, 2 * STAGE);
-          const uint32_t fb = map_to_rank(fb_local, 0);
-          tma_load_3d_pair(st(stage), &tmX, k * KB, a_row, 0, fb);
-          tma_load_3d_pair(st(stage) + A_BYTES, &tmW, k * KB, b_row, ti.e, fb);
+          const uint32_t fb = ptx::smem_u32(&full_bar[stage]);
+          ptx::mbar_arrive_expect_tx(fb, STAGE);
+          ptx::tma_load_3d(st(stage), &tmX, k * KB, a_row, 0, fb);
+          ptx::tma_load_3d(st(stage) + A_BYTES, &tmW, k * KB, b_row, ti.e, fb);
+          if (SILU) ptx::tma_load_3d(st(stage) + A_BYTES + HALF * KB, &tmW, k * KB, P.cols + b_row, ti.e, fb);
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
         }
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader CTA)
-    if (leader && ptx::elect_one()) {
-      constexpr uint32_t IDESC = fp8::idesc(2 * BM, BN);
+    // ------------------------------------------------------------ MMA issuer
+    if (ptx::elect_one()) {
+      constexpr uint32_t IDESC = fp8::idesc(BM, BN);
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int t = cluster_id; t < total && ok; t += nclusters) {
+      for (int t = (int)blockIdx.x; t < total && ok; t += (int)gridDim.x) {
         for (int k = 0; k < P.kb; ++k) {
           ok = ptx::mbar_wait(ptx::smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_p, P.wait_ns) &&
                ptx::mbar_wait(ptx::smem_u32(&full_bar[stage]), ph, abort_p, P.wait_ns);
@@ -188,19 +175,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
           const uint64_t ad = ptx::sdesc_k128(st(stage)), bd = ptx::sdesc_k128(st(stage) + A_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < KB / 32; ++kk) fp8::mma<2>(d_tmem, ad + kk * 2, bd + kk * 2, IDESC, kk != 0);
-          commit_pair(ptx::smem_u32(&empty_bar[stage]), 0x3);
-          commit_pair(ptx::smem_u32(&tfull_bar[acc]), 0x3);
+          for (int kk = 0; kk < KB / 32; ++kk) fp8::mma(d_tmem, ad + kk * 2, bd + kk * 2, IDESC, kk != 0);
+          ptx::mma_commit(ptx::smem_u32(&tfull_bar[acc]));
+          ptx::mma_commit(ptx::smem_u32(&empty_bar[stage]));
           if (++stage == NSTAGE) { stage = 0; ph ^= 1u; }
           if (++acc == 2) { acc = 0; aph ^= 1u; }
         }
       }
-      commit_pair(ptx::smem_u32(&drain_bar), 0x1);
+      ptx::mma_commit(ptx::smem_u32(&drain_bar));
       int dummy = 0;
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, &dummy, DRAIN_NS);
     }
   } else if (warp >= EPI0) {
-    // ------------------------------------------------------------ epilogue (both CTAs)
+    // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(HIGH_REGS));
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int part = (warp - EPI0) >> 2;    // its columns
@@ -214,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const float *xs, *wg, *wu0, *wu1;
     int c0, edge;
     auto locate = [&](const Tile& ti) {
-      const int r = ti.g.lo + ti.m * (2 * BM) + (int)rank * BM + row;
+      const int r = ti.g.lo + ti.m * BM + row;
       // first columns (rows of w) of this thread's sums: W of them, or W / 2 of the gate and as many up ones
       c0 = SILU ? ti.n * HALF + part * (W / 2) : ti.n * BN + part * W;
       const float* ws = P.w_scales + (long)ti.e * P.nb * P.kb;
@@ -237,12 +224,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Scales next{};
     int e = 0;
     Tile ti{};
-    if (cluster_id < total) {
-      ti = tile_at(cluster_id, e, G, P);
+    if ((int)blockIdx.x < total) {
+      ti = tile_at((int)blockIdx.x, e, G, P);
       locate(ti);
       next = load(0);
     }
-    for (int t = cluster_id; t < total; t += nclusters) {
+    for (int t = (int)blockIdx.x; t < total; t += (int)gridDim.x) {
       float sum[W];
 #pragma unroll
       for (int j = 0; j < W; ++j) sum[j] = 0.0f;
@@ -263,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (c + 16 == W) {                // all read: the accumulator goes back
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_remote(map_to_rank(ptx::smem_u32(&tempty_bar[acc]), 0));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tempty_bar[acc]));
           }
           // a block's edge lies at a multiple of 16 columns
           const float f = !SILU || c < W / 2 ? g : c - W / 2 < edge ? u0 : u1;
@@ -273,11 +260,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       if (!ok) break;
-      const int m = ti.m * (2 * BM) + (int)rank * BM + row, col = c0;
+      const int m = ti.m * BM + row, col = c0;
       const int nrows = ti.g.rows() - (m - lane);      // of this warp's 32 (from lane 0 on)
       T* dst = y + ((long)ti.g.lo + m) * P.cols;
-      if (t + nclusters < total) {
-        ti = tile_at(t + nclusters, e, G, P);
+      if (t + (int)gridDim.x < total) {
+        ti = tile_at(t + (int)gridDim.x, e, G, P);
         locate(ti);
         next = load(0);
       }
@@ -306,11 +293,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
-                 : "memory");
+    ptx::tmem_dealloc(tmem_base, TMEM_COLS);
   }
   if (tid == 0 && P.status) {
     if (abort_flag) atomicOr(P.status, MOE_STATUS_TIMEOUT);
@@ -324,7 +309,7 @@ template <bool SILU, class T>
 bool enough_registers() {
   static const bool enough = [] {
     cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, fp8_pair_kernel<SILU, T>) != cudaSuccess) return false;
+    if (cudaFuncGetAttributes(&at, fp8_tc_kernel<SILU, T>) != cudaSuccess) return false;
     return at.numRegs * (EPI0 + EPI_WARPS) >= EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS;
   }();
   return enough;
@@ -333,12 +318,12 @@ bool enough_registers() {
 template <bool SILU, class T>
 int launch(const Fp8Args& a, cudaStream_t s) {
   const char* name = "fp8_grouped_gemm";
-  if (int rc = ensure_smem_limit(fp8_pair_kernel<SILU, T>, DSMEM, name)) return rc;
+  if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T>, DSMEM, name)) return rc;
   if (!enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
   CUtensorMap tx, tw;
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;
-  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, HALF))) return rc;
+  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, SILU ? HALF : BN))) return rc;
   Params p{};
   p.offsets = a.offsets;
   p.x_scales = a.x_scales;
@@ -353,10 +338,10 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   p.vec = grouped::store_width(a.y, p.cols, sizeof(T));
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
-  const long tiles = ((long)(a.S + 2 * BM - 1) / (2 * BM) + a.E) * p.NT;
-  const int grid = 2 * (int)std::max(1L, std::min(tiles, (long)(num_sms() / 2)));
+  const long tiles = ((long)(a.S + BM - 1) / BM + a.E) * p.NT;
+  const int grid = (int)std::max(1L, std::min(tiles, (long)num_sms()));
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(fp8_pair_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, p);
+  const cudaError_t e = launch_pdl(fp8_tc_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }

@@ -287,6 +287,18 @@ def test_product_with_the_gate(dtype, counts, K, N):
     check_product(moe, *operands(counts, K, N, seed=K + N), dtype, True)
 
 
+# few rows an expert on average, many of one of them
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("counts,K,N", [
+    ([0] * 15 + [128], 400, 352), ([0, 130, 1, 0] + [0] * 15, 2048, 96), ([70, 2] + [1] * 20 + [33], 640, 1030),
+    ([3, 0, 17, 0, 0, 0, 49, 0, 0], 144, 160), ([63] + [0] * 6 + [1], 528, 258)])
+def test_product_of_uneven_groups(dtype, silu, counts, K, N):
+    moe = need_gpu()
+    N -= N % 32 if silu else 0          # what the gate takes
+    check_product(moe, *operands(counts, K, N, seed=K + N), dtype, silu)
+
+
 @pytest.mark.parametrize("silu", [False, True])
 @pytest.mark.parametrize("counts", [[5, 0, 7], [300, 0, 90]])
 def test_rows_without_an_expert_are_zero(silu, counts):

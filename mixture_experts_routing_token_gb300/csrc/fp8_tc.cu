@@ -13,12 +13,12 @@
 // matching up rows, so a TMEM lane has both. Eight epilogue warps keep 128 sums a thread, for which the other warps give
 // up registers. Tiles of 256 rows on SM pairs load a third less and were no faster, for a pair's accumulator takes longer to
 // come and go and an expert's last rows fill more of a tile: us, SM pairs / this, 131072 rows of 64 experts, [2816, 2048]
-// with the gate 731 / 707, [2048, 1408] without 394 / 397 to 412; 64 rows an expert 96 / 65.
+// with the gate 731 / 712, [2048, 1408] without 394 / 380; 64 rows an expert 96 / 66.
 //
 // Bound at prompt sizes by the way of an accumulator: four MMAs (512 cycles), their commit, the read and the sums (356
 // cycles), the hand-back, the next issue. Tensor memory holds two, so a block takes about half of that round trip, 1100
-// to 1200 cycles. 131072 rows, 64 experts of [2816, 2048] with the gate: 675 us on a cold GPU (2.24 PFLOP/s), 700 to 710
-// in a long run. At 64 rows an expert it is HBM: 65 us, 5.9 TB/s.
+// to 1200 cycles. 131072 rows, 64 experts of [2816, 2048] with the gate: 670 us on a cold GPU (2.26 PFLOP/s), 700 to 715
+// in a long run. At 64 rows an expert it is HBM: 66 us, 5.8 TB/s.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -32,10 +32,8 @@ constexpr int BM = 128;                 // rows of x per tile
 constexpr int BN = 256;                 // rows of w per tile
 constexpr int HALF = BN / 2;            // with the gate: gate rows, and as many up rows
 constexpr int KB = fp8::BLOCK;          // bytes of a row per step
-constexpr int NSTAGE = 4;
 constexpr int A_BYTES = BM * KB;
 constexpr int STAGE = A_BYTES + BN * KB;
-constexpr int DSMEM = NSTAGE * STAGE + 1024;
 constexpr int PARTS = 2;                // epilogue warps per TMEM lane quarter
 constexpr int EPI_WARPS = 4 * PARTS;
 constexpr int W = BN / PARTS;           // columns of an epilogue warp
@@ -44,6 +42,14 @@ constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;
 // 168 registers a thread at launch (12 warps); the epilogue's eight take what the other four give back
 constexpr int LOW_REGS = 72, HIGH_REGS = 216;
 static_assert(EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS <= (EPI0 + EPI_WARPS) * 168, "registers");
+// 16-bit results leave through shared memory (store_rows), for which the ring has a stage less. Measured, us, single rows
+// from registers and four stages / this: 131072 rows of 64 experts, [2816, 2048] with the gate 724 / 713, [2048, 1408] without
+// 402 / 385; 64 rows an expert of the first 65.6 / 66.5. float32 results, twice as many bytes, stay with four stages.
+constexpr int OUT_BYTES = 4096;         // of a warp
+template <class T>
+constexpr int stages() { return sizeof(T) == 2 ? 3 : 4; }
+template <class T>
+constexpr int dsmem_bytes() { return stages<T>() * STAGE + (sizeof(T) == 2 ? EPI_WARPS * OUT_BYTES : 0) + 1024; }
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
@@ -93,7 +99,9 @@ struct Scales {
 
 template <bool SILU, class T>
 __global__ void __launch_bounds__(THREADS, 1)
-    fp8_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params P) {
+    fp8_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                  const __grid_constant__ CUtensorMap tmY, const Params P) {
+  constexpr int NSTAGE = stages<T>();
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
@@ -260,27 +268,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++acc == 2) { acc = 0; aph ^= 1u; }
       }
       if (!ok) break;
-      const int m = ti.m * BM + row, col = c0;
-      const int nrows = ti.g.rows() - (m - lane);      // of this warp's 32 (from lane 0 on)
-      T* dst = y + ((long)ti.g.lo + m) * P.cols;
+      const int col = c0;
+      const int row_y = ti.g.lo + ti.m * BM + q * 32;      // this warp's first row, and how many it has
+      const int nrows = ti.g.hi - row_y;
       if (t + (int)gridDim.x < total) {
         ti = tile_at(t + (int)gridDim.x, e, G, P);
         locate(ti);
         next = load(0);
       }
+      T* row0 = y + (long)row_y * P.cols;
+      auto result = [&](int i) { return SILU ? mx::silu_fast(sum[i]) * sum[(W / 2 + i) % W] : sum[i]; };
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t buf = dsmem + NSTAGE * STAGE + (warp - EPI0) * OUT_BYTES;
 #pragma unroll
-      for (int c = 0; c < (SILU ? W / 2 : W); c += 32) {
-        uint32_t v[32];
+        for (int c = 0; c < (SILU ? W / 2 : W); c += 64) {
+          uint32_t v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = __float_as_uint(SILU ? mx::silu_fast(sum[c + j]) * sum[W / 2 + c + j] : sum[c + j]);
-        if (P.vec > 0) {
-          if (lane < nrows && col + c < P.cols) grouped::store_cols(dst, col + c, P.cols, P.vec, v);
-        } else if (nrows > 0 && col + c < P.cols) {
-          grouped::store_turned(v, dst - (long)lane * P.cols, nrows, col + c, P.cols);
+          for (int j = 0; j < 32; ++j) v[j] = grouped::pack_pair<T>(result(c + 2 * j), result(c + 2 * j + 1));
+          if (nrows <= 0 || col + c >= P.cols) continue;
+          if (P.vec > 0)
+            grouped::store_rows(buf, v, &tmY, col + c, row_y, 0, nrows >= 32, row0, nrows, P.cols);
+          else
+            grouped::store_ragged(buf, v, row0, nrows, col + c, P.cols);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < (SILU ? W / 2 : W); c += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(result(c + j));
+          if (nrows <= 0 || col + c >= P.cols) continue;
+          if (P.vec == 0)
+            grouped::store_turned(v, row0, nrows, col + c, P.cols);
+          else if (lane < nrows)
+            grouped::store_cols(row0 + (long)lane * P.cols, col + c, P.cols, P.vec, v);
         }
       }
     }
+    if (sizeof(T) == 2 && lane == 0) ptx::tma_store_wait();      // the last rows have left
     if (!*abort_p)
       grouped::zero_unowned(y, G, P.E, P.S, P.cols, ((long)blockIdx.x * EPI_WARPS + warp - EPI0) * 32 + lane,
                             (long)gridDim.x * EPI_WARPS * 32);
@@ -318,9 +343,9 @@ bool enough_registers() {
 template <bool SILU, class T>
 int launch(const Fp8Args& a, cudaStream_t s) {
   const char* name = "fp8_grouped_gemm";
-  if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T>, DSMEM, name)) return rc;
+  if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T>, dsmem_bytes<T>(), name)) return rc;
   if (!enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
-  CUtensorMap tx, tw;
+  CUtensorMap tx, tw, ty{};
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;
   if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, SILU ? HALF : BN))) return rc;
@@ -336,12 +361,13 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   p.NT = SILU ? (p.cols + HALF - 1) / HALF : (p.cols + BN - 1) / BN;
   p.y = a.y;
   p.vec = grouped::store_width(a.y, p.cols, sizeof(T));
+  if (sizeof(T) == 2 && p.vec > 0 && (rc = make_tmap_3d(&ty, a.y, 2, (uint64_t)p.cols, (uint64_t)a.S, 1, 64, 32))) return rc;
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
   const long tiles = ((long)(a.S + BM - 1) / BM + a.E) * p.NT;
   const int grid = (int)std::max(1L, std::min(tiles, (long)num_sms()));
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(fp8_tc_kernel<SILU, T>, grid, THREADS, DSMEM, s, tx, tw, p);
+  const cudaError_t e = launch_pdl(fp8_tc_kernel<SILU, T>, grid, THREADS, dsmem_bytes<T>(), s, tx, tw, ty, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
 }

@@ -1,4 +1,5 @@
 // C ABI: argument checks, workspace layout, launch sequencing, timing hooks.
+#include <limits.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -846,7 +847,7 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
   int rc;
   if ((rc = check_routing_dims(T, E, k))) return rc;
   if ((rc = check_any_dtype(dtype))) return rc;
-  REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
+  REQUIRE(H >= 1 && H <= INT_MAX - 64, "H must be in [1, 2^31 - 65] (got %d)", H);
   const long S = (long)T * k;
   if ((rc = check_tensor(y_sorted, S * H, "y_sorted"))) return rc;
   if ((rc = check_tensor(topk_weights, S, "topk_weights"))) return rc;
@@ -874,7 +875,7 @@ MOE_API int moe_gather_rows_backward(const void* d_x_sorted, const int32_t* reve
   int rc;
   if ((rc = check_routing_dims(T, E, k))) return rc;
   if ((rc = check_any_dtype(dtype))) return rc;
-  REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
+  REQUIRE(H >= 1 && H <= INT_MAX - 64, "H must be in [1, 2^31 - 65] (got %d)", H);
   const long S = (long)T * k;
   if ((rc = check_tensor(d_x_sorted, S * H, "d_x_sorted"))) return rc;
   if ((rc = check_tensor(reverse_indices, S, "reverse_indices"))) return rc;
@@ -900,7 +901,7 @@ MOE_API int moe_ep_combine_backward(const void* d_out, const void* y_sorted, con
   int rc;
   if ((rc = check_routing_dims(T, E, k))) return rc;
   if ((rc = check_any_dtype(dtype))) return rc;
-  REQUIRE(H >= 1, "H must be >= 1 (got %d)", H);
+  REQUIRE(H >= 1 && H <= INT_MAX - 64, "H must be in [1, 2^31 - 65] (got %d)", H);
   const long S = (long)T * k;
   if ((rc = check_tensor(d_out, (long)T * H, "d_out"))) return rc;
   if (d_weights_or_null && (rc = check_tensor(y_sorted, S * H, "y_sorted"))) return rc;

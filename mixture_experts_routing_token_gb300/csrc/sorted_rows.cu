@@ -28,62 +28,104 @@ constexpr int kFlight = 8;              // loads of sorted rows that a thread ha
 // graph, with the first kernel and its workspace, and without: 4000 slots of 500 tokens 26.5 / 11.7 and 13.5 / 10.7, 8000
 // slots of 1000 tokens 27.5 / 12.4 and 14.3 / 14.8, of 8000 tokens 27.2 / 22.2 and 30.5 / 31.2.
 bool each_looks(int T, int k) { return (long)T * k <= 2048 || ((long)T * k <= 8192 && T <= 2048); }
+// Rows in windows: two slots at a time, a piece each, in registers for four CTAs an SM. Measured, us, 8192 tokens x 8 of 2047
+// bf16 values, combine backward / gather backward: 151 / 83; with five CTAs 222 / 93, four slots and three CTAs 167 / 90,
+// as many registers as it likes 202 / 109; single values instead of windows 244 / 199. At 2046 values 148 / 82, in words of 4
+// bytes together 259.
+constexpr int kCtas = 4;
 constexpr int kMinGroup = 4;            // threads of a token at least
 constexpr int kSlotsPerCta = kThreads / kMinGroup * MOE_MAX_TOPK;
 
-// B bytes of neighbouring values as they lie in memory: 16, or 4 or 2 where rows are not a multiple of more.
-template <int B>
-struct Word;
-template <>
-struct Word<16> { using type = uint4; };
-template <>
-struct Word<4> { using type = uint32_t; };
-template <>
-struct Word<2> { using type = uint16_t; };
-
-template <class T, int B>
+// 16 bytes of neighbouring values as they lie in memory.
+template <class T>
 struct Piece {
-  static constexpr int V = B / (int)sizeof(T);
-  using W = typename Word<B>::type;
-  W w;
-  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const W*>(p)); }
+  static constexpr int V = 16 / (int)sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void values(float (&v)[V]) const {
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (B == 16) {
-        v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
-      } else {
-        v[0] = __uint_as_float(w);
-      }
-    } else if constexpr (B == 2) {
-      v[0] = to_float(*reinterpret_cast<const T*>(&w));
-    } else {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(&w);
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        if constexpr (std::is_same<T, __half>::value) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i));
-          v[2 * i] = f.x;
-          v[2 * i + 1] = f.y;
-        } else {
-          v[2 * i] = __uint_as_float(q[i] << 16);
-          v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-        }
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(q[i]);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(q + i));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      } else {
+        v[2 * i] = __uint_as_float(q[i] << 16);
+        v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
       }
     }
   }
   static __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (B == 16) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      else *p = v[0];
-    } else if constexpr (B == 2) {
-      *p = from_float<T>(v[0]);
-    } else if constexpr (B == 4) {
-      *reinterpret_cast<uint32_t*>(p) = grouped::pack_pair<T>(v[0], v[1]);
-    } else {
-      store8(p, v);
-    }
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else store8(p, v);
   }
 };
+
+// Rows that are not a multiple of 16 bytes start anywhere between two pieces of memory, each at a place of its own. The row
+// that is written sets the pieces: the first may begin up to V - 1 values before the row, the last end after it. A row
+// that is read is shifted against them and comes as the two pieces that hold the values (the second one is the next
+// thread's first and comes out of L1).
+template <class T>
+__device__ __forceinline__ int values_before(const T* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T); }
+
+// A piece of the array from `first` (which is at the start of one) to `last`; zeros outside.
+template <class T>
+__device__ __forceinline__ Piece<T> piece_inside(const T* p, const T* first, const T* last) {
+  constexpr int V = Piece<T>::V;
+  Piece<T> r;
+  if (p >= first && p + V <= last) {
+    r.load(p);
+  } else {
+    __align__(16) T v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p >= first && p + i < last ? p[i] : from_float<T>(0.0f);
+    r.w = *reinterpret_cast<const uint4*>(v);
+  }
+  return r;
+}
+
+template <class T>
+struct Window {
+  Piece<T> lo, hi;
+  uint32_t shift;          // bytes
+  __device__ __forceinline__ void load(const T* p, const T* first, const T* last) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    shift = (uint32_t)(at & 15);
+    const T* q = reinterpret_cast<const T*>(at - shift);
+    lo = piece_inside(q, first, last);
+    if (shift) hi = piece_inside(q + Piece<T>::V, first, last);
+  }
+  __device__ __forceinline__ Piece<T> get() const {
+    uint32_t w[8] = {lo.w.x, lo.w.y, lo.w.z, lo.w.w, hi.w.x, hi.w.y, hi.w.z, hi.w.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+    }
+    Piece<T> r;
+    r.w = make_uint4(w[0], w[1], w[2], w[3]);
+    return r;
+  }
+};
+
+// Values i .. i + V - 1 of a row of H, those that there are.
+template <class T>
+__device__ __forceinline__ void store_inside(T* row, int i, int H, const float (&v)[Piece<T>::V]) {
+  constexpr int V = Piece<T>::V;
+  if (i >= 0 && i + V <= H) {
+    Piece<T>::store(row + i, v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+      if (i + q >= 0 && i + q < H) row[i + q] = from_float<T>(v[q]);
+  }
+}
 
 struct Args {
   const int32_t* reverse;
@@ -140,10 +182,11 @@ __device__ __forceinline__ void take_positions(const Args& a, int s0, int count,
 }
 
 // out[t] = sum_j w[t, j] src[pos(t, j)]. G threads take a token, K of its slots and kFlight / K pieces at a time.
-template <class T, int B, int K>
-__global__ void __launch_bounds__(kThreads) sum_rows_kernel(const Args a, const T* __restrict__ src, T* __restrict__ out, int G) {
-  using P = Piece<T, B>;
-  constexpr int U = kFlight / K;
+// WHOLE: rows are a multiple of 16 bytes and begin at one.
+template <class T, bool WHOLE, int K>
+__global__ void __launch_bounds__(kThreads, WHOLE ? 0 : kCtas)
+    sum_rows_kernel(const Args a, const T* __restrict__ src, T* __restrict__ out, int G) {
+  constexpr int V = Piece<T>::V, U = WHOLE ? kFlight / K : 1;
   __shared__ int pos[kSlotsPerCta];
   pdl_wait();
   pdl_trigger();
@@ -153,47 +196,55 @@ __global__ void __launch_bounds__(kThreads) sum_rows_kernel(const Args a, const 
   if (t >= a.T) return;
   const int* at = pos + local * a.k;
   const float* w = a.weights ? a.weights + (long)t * a.k : nullptr;
-  const int pieces = a.H / P::V;
+  T* row = out + (long)t * a.H;
+  const int before = WHOLE ? 0 : values_before(row);
+  const int pieces = (a.H + before + V - 1) / V;
   for (int c0 = threadIdx.x % G; c0 < pieces; c0 += U * G) {
-    float sum[U][P::V];
+    float sum[U][V];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int q = 0; q < P::V; ++q) sum[u][q] = 0.0f;
+      for (int q = 0; q < V; ++q) sum[u][q] = 0.0f;
     for (int j0 = 0; j0 < a.k; j0 += K) {
-      P y[K][U];
+      std::conditional_t<WHOLE, Piece<T>, Window<T>> y[K][U];
 #pragma unroll
       for (int j = 0; j < K; ++j)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces)
-            y[j][u].load(src + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V);
+          if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces) {
+            const T* p = src + (long)at[j0 + j] * a.H + (c0 + u * G) * V - before;
+            if constexpr (WHOLE) y[j][u].load(p);
+            else y[j][u].load(p, src, src + (long)a.T * a.k * a.H);
+          }
 #pragma unroll
       for (int j = 0; j < K; ++j)
         if (j0 + j < a.k && at[j0 + j] >= 0) {
           const float wj = w ? __ldg(w + j0 + j) : 1.0f;
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            float v[P::V];
-            y[j][u].values(v);
+            float v[V];
+            if constexpr (WHOLE) y[j][u].values(v);
+            else y[j][u].get().values(v);
 #pragma unroll
-            for (int q = 0; q < P::V; ++q) sum[u][q] += wj * v[q];
+            for (int q = 0; q < V; ++q) sum[u][q] += wj * v[q];
           }
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + u * G < pieces) P::store(out + (long)t * a.H + (c0 + u * G) * P::V, sum[u]);
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u * G >= pieces) continue;
+      if constexpr (WHOLE) Piece<T>::store(row + (c0 + u * G) * V, sum[u]);
+      else store_inside(row, (c0 + u * G) * V - before, a.H, sum[u]);
+    }
   }
 }
 
 // d_y[pos(t, j)] = w[t, j] d_out[t] and d_w[t, j] = <d_out[t], y[pos(t, j)]>; either may be null.
-template <class T, int B, int K>
-__global__ void __launch_bounds__(kThreads)
+template <class T, bool WHOLE, int K>
+__global__ void __launch_bounds__(kThreads, WHOLE ? 0 : kCtas)
     sum_rows_backward_kernel(const Args a, const T* __restrict__ d_out, const T* __restrict__ y, T* __restrict__ d_y,
                              float* __restrict__ d_w, int G) {
-  using P = Piece<T, B>;
-  constexpr int U = kFlight / K;
+  constexpr int V = Piece<T>::V, U = WHOLE ? kFlight / K : 1;
   __shared__ int pos[kSlotsPerCta];
   __shared__ float part[kThreads / 32][K];
   pdl_wait();
@@ -204,44 +255,92 @@ __global__ void __launch_bounds__(kThreads)
   const bool in = t < a.T;
   const int* at = pos + (in ? local : 0) * a.k;
   const float* w = a.weights + (long)(in ? t : 0) * a.k;
-  const int pieces = a.H / P::V;
   for (int j0 = 0; j0 < a.k; j0 += K) {
     float dot[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) dot[j] = 0.0f;
-    for (int c0 = me; in && c0 < pieces; c0 += U * G) {
-      P d[U], r[K][U];
+    if constexpr (WHOLE) {
+      const int pieces = a.H / V;
+      for (int c0 = me; in && c0 < pieces; c0 += U * G) {
+        Piece<T> d[U], r[K][U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (c0 + u * G < pieces) d[u].load(d_out + (long)t * a.H + (c0 + u * G) * P::V);
-      if (d_w != nullptr) {
+        for (int u = 0; u < U; ++u)
+          if (c0 + u * G < pieces) d[u].load(d_out + (long)t * a.H + (c0 + u * G) * V);
+        if (d_w != nullptr) {
 #pragma unroll
-        for (int j = 0; j < K; ++j)
+          for (int j = 0; j < K; ++j)
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces)
-              r[j][u].load(y + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V);
+            for (int u = 0; u < U; ++u)
+              if (j0 + j < a.k && at[j0 + j] >= 0 && c0 + u * G < pieces)
+                r[j][u].load(y + (long)at[j0 + j] * a.H + (c0 + u * G) * V);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c0 + u * G >= pieces) continue;
+          float dv[V];
+          d[u].values(dv);
+#pragma unroll
+          for (int j = 0; j < K; ++j) {
+            if (j0 + j >= a.k || at[j0 + j] < 0) continue;
+            if (d_w != nullptr) {
+              float v[V];
+              r[j][u].values(v);
+#pragma unroll
+              for (int q = 0; q < V; ++q) dot[j] += dv[q] * v[q];
+            }
+            if (d_y != nullptr) {
+              const float wj = __ldg(w + j0 + j);
+              float o[V];
+#pragma unroll
+              for (int q = 0; q < V; ++q) o[q] = wj * dv[q];
+              Piece<T>::store(d_y + (long)at[j0 + j] * a.H + (c0 + u * G) * V, o);
+            }
+          }
+        }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (c0 + u * G >= pieces) continue;
-        float dv[P::V];
-        d[u].values(dv);
+    } else {
+      // the sorted row sets the pieces; d_out comes shifted to each, out of L1 after the first
+      const T* const d_row = d_out + (long)(in ? t : 0) * a.H;
+      const int pieces = (a.H - 1) / V + 2;
+      for (int c = me; in && c < pieces; c += G) {
+        Window<T> d[K];
+        Piece<T> r[K];
+        int x[K];              // first value, H: nothing to do
 #pragma unroll
         for (int j = 0; j < K; ++j) {
+          x[j] = a.H;
           if (j0 + j >= a.k || at[j0 + j] < 0) continue;
-          if (d_w != nullptr) {
-            float v[P::V];
-            r[j][u].values(v);
+          const long row = (long)at[j0 + j] * a.H;
+          const int i = c * V - (int)(row & (V - 1));
+          if (i >= a.H) continue;
+          x[j] = i;
+          if (d_w != nullptr) r[j] = piece_inside(y + row + i, y, y + (long)a.T * a.k * a.H);
+          d[j].load(d_row + i, d_out, d_out + (long)a.T * a.H);
+        }
 #pragma unroll
-            for (int q = 0; q < P::V; ++q) dot[j] += dv[q] * v[q];
+        for (int j = 0; j < K; ++j) {
+          const int i = x[j];
+          if (i >= a.H) continue;
+          float dv[V];
+          d[j].get().values(dv);
+          if (d_w != nullptr) {
+            float v[V];
+            r[j].values(v);
+            if (i >= 0 && i + V <= a.H) {
+#pragma unroll
+              for (int q = 0; q < V; ++q) dot[j] += dv[q] * v[q];
+            } else {           // what lies beside the row may be anything
+#pragma unroll
+              for (int q = 0; q < V; ++q)
+                if (i + q >= 0 && i + q < a.H) dot[j] += dv[q] * v[q];
+            }
           }
           if (d_y != nullptr) {
             const float wj = __ldg(w + j0 + j);
-            float o[P::V];
+            float o[V];
 #pragma unroll
-            for (int q = 0; q < P::V; ++q) o[q] = wj * dv[q];
-            P::store(d_y + (long)at[j0 + j] * a.H + (c0 + u * G) * P::V, o);
+            for (int q = 0; q < V; ++q) o[q] = wj * dv[q];
+            store_inside(d_y + (long)at[j0 + j] * a.H, i, a.H, o);
           }
         }
       }
@@ -268,20 +367,40 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// out[p] = src[ids[p]] for the routed rows, rows of any width: 2 or 4 bytes at a time.
-template <class W>
+// out[p] = src[ids[p]] for the routed rows, rows of any width.
+template <class T>
 __global__ void __launch_bounds__(kThreads)
-    gather_any_rows_kernel(const W* __restrict__ src, const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, int E,
-                           int T, int S, int H, W* __restrict__ out) {
+    gather_any_rows_kernel(const T* __restrict__ src, const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, int E,
+                           int rows, int S, int H, T* __restrict__ out) {
+  constexpr int V = Piece<T>::V, U = 4;
   pdl_wait();
   pdl_trigger();
   const int n = min(max(__ldg(offsets + E), 0), S), lane = threadIdx.x & 31;
   for (long p = (long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; p < n; p += (long)gridDim.x * (kThreads / 32)) {
     const int t = __ldg(ids + p);
-    if (t < 0 || t >= T) continue;
-    const W* from = src + (long)t * H;
-    W* to = out + p * H;
-    for (int c = lane; c < H; c += 32) to[c] = __ldg(from + c);
+    if (t < 0 || t >= rows) continue;
+    const T* from = src + (long)t * H;
+    T* to = out + p * H;
+    for (long i = lane * V - values_before(to); i < H; i += U * 32 * V) {
+      Window<T> w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * 32 * V < H) w[u].load(from + i + u * 32 * V, src, src + (long)rows * H);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long x = i + u * 32 * V;
+        if (x >= H) continue;
+        __align__(16) T v[V];
+        *reinterpret_cast<uint4*>(v) = w[u].get().w;
+        if (x >= 0 && x + V <= H) {
+          *reinterpret_cast<uint4*>(to + x) = *reinterpret_cast<const uint4*>(v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < V; ++q)
+            if (x + q >= 0 && x + q < H) to[x + q] = v[q];
+        }
+      }
+    }
   }
 }
 
@@ -310,50 +429,37 @@ int threads_per_token(int pieces, int T) {
   return g;
 }
 
-// Bytes of a row that are read at a time.
-int piece_bytes(long row_bytes) { return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : 2; }
+// Whether rows are whole pieces of 16 bytes (arrays start at one).
+template <class T>
+bool whole(const Args& a) { return a.H % Piece<T>::V == 0; }
 
-template <class T, int B, int K>
+template <class T, bool WHOLE, int K>
 int sum_as(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  const int G = threads_per_token(a.H / Piece<T, B>::V, a.T), tokens = kThreads / G;
+  const int G = threads_per_token(a.H / Piece<T>::V, a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_kernel<T, B, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a, static_cast<const T*>(src),
-                         static_cast<T*>(out), G),
+  return done(launch_pdl(sum_rows_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
+                         static_cast<const T*>(src), static_cast<T*>(out), G),
               name);
-}
-template <class T, int B>
-int sum_of(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  return a.k <= 2 ? sum_as<T, B, 2>(a, src, out, name, s) : sum_as<T, B, kFlight>(a, src, out, name, s);
 }
 template <class T>
 int sum(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  const int b = piece_bytes((long)a.H * (int)sizeof(T));
-  if (b == 16) return sum_of<T, 16>(a, src, out, name, s);
-  if constexpr (sizeof(T) == 2)
-    if (b == 2) return sum_of<T, 2>(a, src, out, name, s);
-  return sum_of<T, 4>(a, src, out, name, s);
+  if (!whole<T>(a)) return sum_as<T, false, 2>(a, src, out, name, s);
+  return a.k <= 2 ? sum_as<T, true, 2>(a, src, out, name, s) : sum_as<T, true, kFlight>(a, src, out, name, s);
 }
 
-template <class T, int B, int K>
+template <class T, bool WHOLE, int K>
 int sum_backward_as(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
   const char* name = "ep_combine_backward";
-  const int G = threads_per_token(a.H / Piece<T, B>::V, a.T), tokens = kThreads / G;
+  const int G = threads_per_token(a.H / Piece<T>::V, a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_backward_kernel<T, B, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
+  return done(launch_pdl(sum_rows_backward_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
                          static_cast<const T*>(d_out), static_cast<const T*>(y), static_cast<T*>(d_y), d_w, G),
               name);
 }
-template <class T, int B>
-int sum_backward_of(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
-  return a.k <= 2 ? sum_backward_as<T, B, 2>(a, d_out, y, d_y, d_w, s) : sum_backward_as<T, B, kFlight>(a, d_out, y, d_y, d_w, s);
-}
 template <class T>
 int sum_backward(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
-  const int b = piece_bytes((long)a.H * (int)sizeof(T));
-  if (b == 16) return sum_backward_of<T, 16>(a, d_out, y, d_y, d_w, s);
-  if constexpr (sizeof(T) == 2)
-    if (b == 2) return sum_backward_of<T, 2>(a, d_out, y, d_y, d_w, s);
-  return sum_backward_of<T, 4>(a, d_out, y, d_y, d_w, s);
+  if (!whole<T>(a)) return sum_backward_as<T, false, 2>(a, d_out, y, d_y, d_w, s);
+  return a.k <= 2 ? sum_backward_as<T, true, 2>(a, d_out, y, d_y, d_w, s) : sum_backward_as<T, true, kFlight>(a, d_out, y, d_y, d_w, s);
 }
 
 Args args(const SortedRows& r, const float* weights) {
@@ -387,11 +493,11 @@ int launch_gather_any_rows(const void* src, const int32_t* ids, const int32_t* o
   const int grid = (int)std::max(1L, std::min((long)num_sms() * 8, ((long)S + 7) / 8));
   ProfScope ps(name, s);
   if (elem_bytes == 4)
-    return done(launch_pdl(gather_any_rows_kernel<uint32_t>, grid, kThreads, 0, s, static_cast<const uint32_t*>(src), ids, offsets, E,
-                           T, S, H, static_cast<uint32_t*>(out)),
+    return done(launch_pdl(gather_any_rows_kernel<float>, grid, kThreads, 0, s, static_cast<const float*>(src), ids, offsets, E, T, S, H,
+                           static_cast<float*>(out)),
                 name);
-  return done(launch_pdl(gather_any_rows_kernel<uint16_t>, grid, kThreads, 0, s, static_cast<const uint16_t*>(src), ids, offsets, E, T,
-                         S, H, static_cast<uint16_t*>(out)),
+  return done(launch_pdl(gather_any_rows_kernel<__half>, grid, kThreads, 0, s, static_cast<const __half*>(src), ids, offsets, E, T, S, H,
+                         static_cast<__half*>(out)),
               name);
 }
 

@@ -214,11 +214,13 @@ def test_c_gradients(moe):
     call = lambda dt=1, T=4, H=8, E=4, k=2, x=one, ws=None, nb=0: f(x, one, one, dt, T, H, E, k, one, ws, nb, None, None)  # noqa: E731
     assert call(dt=7) == BAD and call(H=0) == BAD and call(k=5) == BAD and call(T=-1) == BAD and call(k=33, E=64) == BAD
     assert call(x=None) == BAD and "d_x_sorted is null" in err(moe)
+    assert call(H=2 ** 31 - 64) == BAD and "H must be" in err(moe)
     assert f(None, None, one, 1, 0, 8, 4, 2, None, None, 0, None, None) == BAD      # offsets: not device memory
     g = L.moe_ep_combine_backward
     call = lambda dt=1, T=4, H=8, E=4, k=2, d=one: g(d, one, one, one, one, dt, T, k, H, E, one, one, None, 0, None, None)  # noqa: E731
     assert call(dt=7) == BAD and call(H=0) == BAD and call(k=5) == BAD and call(T=-1) == BAD
     assert call(d=None) == BAD and "d_out is null" in err(moe)
+    assert call(H=2 ** 31 - 1) == BAD and "H must be" in err(moe)
 
 
 def test_workspace_sizes(moe):

@@ -94,6 +94,47 @@ def test_forward(dtype, T, k, H, dropped):
     assert (np.abs(got - want) <= 2 * k * 2.0 ** -24 * mag + 1.01 * half(dt) * (np.abs(want) + mag * k * 2.0 ** -23) + least(dt)).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(5, 1, 1), (9, 3, 3), (40, 2, 7), (40, 4, 9), (3, 2, 1001), (300, 3, 130), (1500, 4, 31), (2100, 1, 4098), (7, 4, 2044)])
+def test_rows_of_any_width_keep_to_themselves(dtype, T, k, H):
+    """NaN in one row stays in what that row has a part in, wherever the rows lie against 16 bytes."""
+    moe = need_gpu()
+    dt = TYPES[dtype]
+    reverse, off, n = routing(T, k, 0, T)
+    d_out, y, d_x, w = (t.to(DEV) for t in tensors(T, k, H, dt))
+    rg, og = torch.from_numpy(reverse).to(DEV), torch.from_numpy(off).to(DEV)
+    pos = torch.empty(T * k, dtype=torch.long, device=DEV)
+    pos[rg.long()] = torch.arange(T * k, device=DEV)
+    run = lambda: (*moe.moe_ep_combine_backward(d_out, y, w, rg, og), moe.moe_gather_rows_backward(d_x, rg, og, k),  # noqa: E731
+                   moe.moe_ep_combine(y, w, rg, og), moe.moe_gather_rows(d_out, rg // k, og, k))
+    clean = run()
+    for row in sorted({0, 1, n // 2, n - 2, n - 1} & set(range(n))):
+        kept = y[row].clone(), d_x[row].clone()
+        y[row], d_x[row] = float("nan"), float("inf")
+        d_y, d_w, d_h, out, rows = run()
+        slot = int(reverse[row])
+        t = slot // k
+        others = torch.arange(T, device=DEV) != t
+        assert torch.equal(d_y, clean[0]) and torch.equal(rows, clean[4])
+        assert torch.isnan(d_w.view(-1)[slot]) and int(torch.isnan(d_w).sum()) == 1
+        assert torch.equal(d_w.view(-1)[torch.arange(T * k, device=DEV) != slot], clean[1].view(-1)[torch.arange(T * k, device=DEV) != slot])
+        assert not torch.isfinite(d_h[t]).any() and torch.equal(d_h[others], clean[2][others])
+        assert torch.isnan(out[t]).all() and torch.equal(out[others], clean[3][others])
+        y[row], d_x[row] = kept
+    for t in sorted({0, T // 2, T - 1}):
+        kept = d_out[t].clone()
+        d_out[t] = float("nan")
+        d_y, d_w, d_h, out, rows = run()
+        mine = pos[t * k:(t + 1) * k]
+        others = torch.ones(T * k, dtype=torch.bool, device=DEV)
+        others[mine] = False
+        for got, was in ((d_y, clean[0]), (rows, clean[4])):
+            assert torch.isnan(got[mine]).all() and torch.equal(got[others], was[others])
+        assert int(torch.isnan(d_w).sum()) == k and torch.isnan(d_w[t]).all()
+        assert torch.equal(d_h, clean[2]) and torch.equal(out, clean[3])
+        d_out[t] = kept
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_gradients_are_the_transposes(dtype):
     """<combine(y), d> = <y, d_y> = <w, d_w> and <gather(x), d_x> = <x, d_hidden>, as the calls give them."""
@@ -200,9 +241,10 @@ def test_a_workspace_that_holds_other_positions():
     assert torch.equal(d_w.cpu().reshape(-1), want)
 
 
-def test_rows_past_2_to_the_31():
+@pytest.mark.parametrize("H", [2048, 2049])
+def test_rows_past_2_to_the_31(H):
     moe = need_gpu()
-    T, k, H = (1 << 19) + 3, 2, 2048
+    T, k = (1 << 19) + 3, 2
     S = T * k
     rev = torch.arange(S, dtype=torch.int32, device=DEV).flip(0).contiguous()
     off = torch.tensor([0, 5, S], dtype=torch.int32, device=DEV)

@@ -23,7 +23,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFlight = 8;              // loads of sorted rows that a thread has under way
+// Loads of sorted rows that a thread has under way: of 2, 4 or 8 slots (K), the least that are k or more. Measured, us, both
+// gradients with 8 / 4 / 2 slots at a time, bf16 rows of 2048: k = 8, 8192 tokens 158 / 160 / 162 (500 tokens of 512 values
+// 10.8 / 11.7 / 14.0), k = 4, 16384 tokens 185 / 153 / 161, k = 3, 8192 tokens 89 / 72 / 77.
+constexpr int kFlight = 8;
 // Whether the CTAs look for their slots themselves. Measured, us, both gradients of bf16 rows of 512, from Python / in a
 // graph, with the first kernel and its workspace, and without: 4000 slots of 500 tokens 26.5 / 11.7 and 13.5 / 10.7, 8000
 // slots of 1000 tokens 27.5 / 12.4 and 14.3 / 14.8, of 8000 tokens 27.2 / 22.2 and 30.5 / 31.2.
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, WHOLE ? 0 : kCtas)
     } else {
       // the sorted row sets the pieces; d_out comes shifted to each, out of L1 after the first
       const T* const d_row = d_out + (long)(in ? t : 0) * a.H;
-      const int pieces = (a.H - 1) / V + 2;
+      const int pieces = (a.H - 1) / V + 2;      // of a row, wherever it lies
       for (int c = me; in && c < pieces; c += G) {
         Window<T> d[K];
         Piece<T> r[K];
@@ -433,9 +436,13 @@ int threads_per_token(int pieces, int T) {
 template <class T>
 bool whole(const Args& a) { return a.H % Piece<T>::V == 0; }
 
+// Pieces of a row at most.
+template <class T, bool WHOLE>
+int pieces_of(int H) { return WHOLE ? H / Piece<T>::V : (H - 1) / Piece<T>::V + 2; }
+
 template <class T, bool WHOLE, int K>
 int sum_as(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
-  const int G = threads_per_token(a.H / Piece<T>::V, a.T), tokens = kThreads / G;
+  const int G = threads_per_token(pieces_of<T, WHOLE>(a.H), a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
   return done(launch_pdl(sum_rows_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
                          static_cast<const T*>(src), static_cast<T*>(out), G),
@@ -444,13 +451,14 @@ int sum_as(const Args& a, const void* src, void* out, const char* name, cudaStre
 template <class T>
 int sum(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
   if (!whole<T>(a)) return sum_as<T, false, 2>(a, src, out, name, s);
-  return a.k <= 2 ? sum_as<T, true, 2>(a, src, out, name, s) : sum_as<T, true, kFlight>(a, src, out, name, s);
+  if (a.k <= 2) return sum_as<T, true, 2>(a, src, out, name, s);
+  return a.k <= 4 ? sum_as<T, true, 4>(a, src, out, name, s) : sum_as<T, true, 8>(a, src, out, name, s);
 }
 
 template <class T, bool WHOLE, int K>
 int sum_backward_as(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
   const char* name = "ep_combine_backward";
-  const int G = threads_per_token(a.H / Piece<T>::V, a.T), tokens = kThreads / G;
+  const int G = threads_per_token(pieces_of<T, WHOLE>(a.H), a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
   return done(launch_pdl(sum_rows_backward_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
                          static_cast<const T*>(d_out), static_cast<const T*>(y), static_cast<T*>(d_y), d_w, G),
@@ -459,7 +467,8 @@ int sum_backward_as(const Args& a, const void* d_out, const void* y, void* d_y, 
 template <class T>
 int sum_backward(const Args& a, const void* d_out, const void* y, void* d_y, float* d_w, cudaStream_t s) {
   if (!whole<T>(a)) return sum_backward_as<T, false, 2>(a, d_out, y, d_y, d_w, s);
-  return a.k <= 2 ? sum_backward_as<T, true, 2>(a, d_out, y, d_y, d_w, s) : sum_backward_as<T, true, kFlight>(a, d_out, y, d_y, d_w, s);
+  if (a.k <= 2) return sum_backward_as<T, true, 2>(a, d_out, y, d_y, d_w, s);
+  return a.k <= 4 ? sum_backward_as<T, true, 4>(a, d_out, y, d_y, d_w, s) : sum_backward_as<T, true, 8>(a, d_out, y, d_y, d_w, s);
 }
 
 Args args(const SortedRows& r, const float* weights) {

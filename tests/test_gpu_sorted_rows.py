@@ -21,12 +21,13 @@ def least(dtype):
 
 
 def routing(T, k, dropped, seed=0):
-    """reverse [T k] in expert order (ascending slots within an expert), offsets of 4 experts, routed rows."""
+    """reverse [T k] in expert order (ascending slots within an expert), offsets of max(4, k) experts, routed rows."""
     rng = np.random.default_rng(seed)
-    expert = rng.integers(0, 4, T * k)
-    expert[rng.permutation(T * k)[:dropped]] = 4
+    E = max(4, k)
+    expert = rng.integers(0, E, T * k)
+    expert[rng.permutation(T * k)[:dropped]] = E
     reverse = np.argsort(expert, kind="stable").astype(np.int32)
-    off = np.concatenate([[0], np.cumsum(np.bincount(expert, minlength=5)[:4])]).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(np.bincount(expert, minlength=E + 1)[:E])]).astype(np.int32)
     return reverse, off, int(off[-1])
 
 
@@ -42,7 +43,8 @@ def f64(t):
 
 SIZES = [(1, 1, 8, 0), (1, 4, 1, 1), (3, 2, 64, 0), (77, 2, 1001, 9), (40, 4, 2048, 0), (300, 3, 136, 100), (9, 4, 4096, 0),
          (1100, 2, 24, 5), (600, 4, 33, 0), (2000, 4, 16, 7999), (513, 4, 8200, 3), (5, 4, 20000, 2), (700, 3, 7, 11),
-         (2500, 4, 24, 5), (2500, 4, 33, 9999), (9000, 1, 40, 100), (2100, 1, 72, 0)]
+         (2500, 4, 24, 5), (2500, 4, 33, 9999), (9000, 1, 40, 100), (2100, 1, 72, 0),
+         (50, 5, 264, 3), (700, 8, 1032, 60), (1300, 8, 257, 0), (40, 11, 520, 7), (9, 32, 72, 0), (300, 32, 35, 900)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)

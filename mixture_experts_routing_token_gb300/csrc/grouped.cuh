@@ -252,48 +252,80 @@ __device__ __forceinline__ void store_rows(uint32_t buf, const uint32_t (&q)[32]
   __syncwarp();
 }
 
-// The same for rows that are not a multiple of 16 bytes: each row is read back from the buffer by the
-// whole warp and leaves in 4-byte words (a row that starts between two words gives its first value
-// alone and shifts the others by one), 128 bytes an instruction, eight rows under way together. 16000
-// float16 rows, K = 136, 4093 columns: 109 us; 139 where the lanes exchanged the block by shuffles and
-// stored single values, 216 with one row at a time. `count` > 0 rows, columns from c0 on.
+// The same for rows that are not a multiple of 16 bytes, which start anywhere between two pieces of memory: eight lanes take
+// a row and store its whole pieces, each out of the two in the buffer that hold its values, shifted in registers; the up to
+// seven values before the first and behind the last of them leave in words and single values, a row a lane. 16000
+// float16 rows, K = 136, 4093 columns: 80 us; 109 where a whole warp read a row back and stored it in words of 4 bytes, 139
+// where the lanes exchanged the block by shuffles and stored single values. 22676 8-bit rows, K = 128, 8121 bf16 columns:
+// 177 us, with words 238 (39 instructions a row and 64 columns, of which the epilogue's warps are short).
+// `count` > 0 rows, columns from c0 on.
 template <class T>
 __device__ __forceinline__ void store_ragged(uint32_t buf, const uint32_t (&q)[32], T* row0, int count, int c0, int cols) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, p = lane & 7;
   __syncwarp();                                   // the last columns have been read
 #pragma unroll
-  for (int p = 0; p < 8; ++p)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((p ^ (lane & 7)) << 4)),
-                 "r"(q[4 * p]), "r"(q[4 * p + 1]), "r"(q[4 * p + 2]), "r"(q[4 * p + 3])
+  for (int i = 0; i < 8; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                 "r"(q[4 * i]), "r"(q[4 * i + 1]), "r"(q[4 * i + 2]), "r"(q[4 * i + 3])
                  : "memory");
   __syncwarp();
   const int left = min(64, cols - c0);            // values of a row
-  uint16_t* row = reinterpret_cast<uint16_t*>(row0) + c0;
-#pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += 8) {
+  uint16_t* const first = reinterpret_cast<uint16_t*>(row0) + c0;
+  auto before = [](const uint16_t* row) { return (int)(reinterpret_cast<uintptr_t>(row) >> 1) & 7; };
+#pragma unroll 2
+  for (int r0 = 0; r0 < 32; r0 += 4) {
     if (r0 >= count) break;
-    uint32_t w[8], next[8];
+    const int r = r0 + (lane >> 3);
+    uint16_t* row = first + (long)r * cols;
+    const int d = before(row), x = 8 * p - d;     // the values x .. x + 7, of the pieces p - 1 and p
+    uint32_t w[8];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(buf + r * 128 + ((((p - 1) & 7) ^ (r & 7)) << 4))
+                 : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "r"(buf + r * 128 + ((p ^ (r & 7)) << 4))
+                 : "memory");
+    const uint32_t shift = 16 - 2 * d;            // bytes
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(w[i])
-                   : "r"(buf + (r0 + i) * 128 + ((((lane >> 2) ^ i) << 4) | ((lane & 3) << 2)))
+    for (int i = 0; i < 4; ++i) w[i] = shift & 16 ? w[i + 4] : w[i];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+    if (r < count && x >= 0 && x + 8 <= left) *reinterpret_cast<uint4*>(row + x) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (lane < count) {
+    uint16_t* row = first + (long)lane * cols;
+    const int d = before(row);
+    const int head = min((8 - d) & 7, left);                   // values before the first whole piece
+    const int tail = max(head, ((left + d) & ~7) - d);         // the first one behind the last
+    auto value = [&](int v) {
+      uint32_t b;
+      asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                   : "=r"(b)
+                   : "r"(buf + lane * 128 + (((v >> 3) ^ (lane & 7)) << 4) + (v & 7) * 2)
                    : "memory");
+      return b;
+    };
+    auto some = [&](int v, int end) {                          // up to seven of them
+      if (v < end && (reinterpret_cast<uintptr_t>(row + v) & 2)) {
+        row[v] = (uint16_t)value(v);
+        ++v;
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) next[i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint16_t* p = row + (long)(r0 + i) * cols;
-      const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
-      const uint32_t v = __byte_perm(w[i], next[i], odd ? 0x5432 : 0x3210);
-      const int e = 2 * lane + odd;
-      const bool in = r0 + i < count;
-      if (in && e + 1 < left) *reinterpret_cast<uint32_t*>(p + e) = v;
-      // the values without a pair: a row's first, lane 0's; its last, of the lane that ends there
-      const bool head = odd && lane == 0;
-      if (in && (head || e + 1 == left)) p[head ? 0 : e] = (uint16_t)(head ? w[i] : v);
-      if (in && head && e + 1 == left) p[e] = (uint16_t)v;
-    }
+      for (int i = 0; i < 3; ++i)
+        if (v + 1 < end) {
+          *reinterpret_cast<uint32_t*>(row + v) = value(v) | value(v + 1) << 16;
+          v += 2;
+        }
+      if (v < end) row[v] = (uint16_t)value(v);
+    };
+    some(0, head);
+    some(tail, left);
   }
 }
 

@@ -9,9 +9,10 @@ namespace fp8 {
 constexpr int BLOCK = 128;       // values along a row (and rows of a weight matrix) that share a scale
 
 // Whether a product takes the weight-streaming kernel: up to 8 rows per expert on average. Measured, us, that kernel / the
-// tiled one: one row of 8 experts, 64 experts [2816, 2048] with the gate 15 / 19; 2 experts, [2816, 2048] 8.9 / 11.3,
-// [14336, 4096] 25 / 33; 4 rows an expert, 8 experts [2816, 2048] 15 / 17, 64 experts 62 / 62; 8 rows, 64 experts [2048, 1408]
-// 34 / 37; 16 rows, 64 experts [2816, 2048] 65 / 64, 8 experts 16 / 14; 32 rows 72 / 65 and 19 / 14.
+// tiled one: one row of 8 experts, 64 experts [2816, 2048] with the gate 15 / 19; of 2 experts, [14336, 4096] 25 / 33;
+// 8 rows of 4 experts, [2816, 1408] 7.4 / 9.3; 4 rows an expert, 8 experts [2816, 2048] 15 / 17, 64 experts 62 / 62; 8
+// rows, 64 experts [2048, 1408] 34 / 37; 16 rows, 64 experts [2816, 2048] 65 / 64, 8 experts 16 / 14; 32 rows 72 / 65 and
+// 19 / 14.
 constexpr int kFewRows = 8;
 inline bool few_rows(int S, int E) { return S <= (long)kFewRows * E; }
 

@@ -1,4 +1,4 @@
-// Products of 8-bit rows grouped by expert (tcgen05.mma.kind::f8f6f4, M = 128 x N = 256 x K = 32, float32 accumulators in
+// Products of 8-bit rows grouped by expert (tcgen05.mma.kind::f8f6f4, M = 128 x N = 256 or 128 x K = 32, float32 accumulators in
 // TMEM), with a scale for every 128 values of a row and 128 x 128 of a matrix:
 //
 //   y[p, n] = sum over blocks b of sx[p, b] sw[e, n / 128, b] sum over k in b of cx[p, k] cw[e, n, k]
@@ -9,11 +9,12 @@
 // goes into the other accumulator. Sums are rounded to nearest every 128 terms, and only the 128 inside a block see the
 // tensor cores' truncating additions.
 //
-// One CTA per SM takes tiles of 128 rows of x and 256 of w by turns; with the gate these are 128 gate rows and the
-// matching up rows, so a TMEM lane has both. Eight epilogue warps keep 128 sums a thread, for which the other warps give
-// up registers. Tiles of 256 rows on SM pairs load a third less and were no faster, for a pair's accumulator takes longer to
-// come and go and an expert's last rows fill more of a tile: us, SM pairs / this, 131072 rows of 64 experts, [2816, 2048]
-// with the gate 731 / 712, [2048, 1408] without 394 / 380; 64 rows an expert 96 / 66.
+// One CTA per SM takes tiles of 128 rows of x and 256 of w (128 where there are few, see launch) by turns; with the gate
+// half of these are gate rows and half the matching up rows, so a TMEM lane has both. Eight epilogue warps (four) keep 128
+// sums a thread, for which the other warps of the wide form give up registers. Tiles of 256 rows on SM pairs load a third
+// less and were no faster, for a pair's accumulator takes longer to come and go and an expert's last rows fill more of a
+// tile: us, SM pairs / this, 131072 rows of 64 experts, [2816, 2048] with the gate 731 / 712, [2048, 1408] without
+// 394 / 380; 64 rows an expert 96 / 66.
 //
 // Bound at prompt sizes by the way of an accumulator: four MMAs (512 cycles), their commit, the read and the sums (356
 // cycles), the hand-back, the next issue. Tensor memory holds two, so a block takes about half of that round trip, 1100
@@ -29,28 +30,31 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;                 // rows of x per tile
-constexpr int BN = 256;                 // rows of w per tile
-constexpr int HALF = BN / 2;            // with the gate: gate rows, and as many up rows
 constexpr int KB = fp8::BLOCK;          // bytes of a row per step
 constexpr int A_BYTES = BM * KB;
-constexpr int STAGE = A_BYTES + BN * KB;
-constexpr int PARTS = 2;                // epilogue warps per TMEM lane quarter
-constexpr int EPI_WARPS = 4 * PARTS;
-constexpr int W = BN / PARTS;           // columns of an epilogue warp
+constexpr int W = 128;                  // rows of w (columns) of an epilogue warp
 constexpr int EPI0 = 4;                 // the first of them
-constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;
-// 168 registers a thread at launch (12 warps); the epilogue's eight take what the other four give back
+// Wide form: 168 registers a thread at launch (12 warps); the epilogue's eight take what the other four give back.
 constexpr int LOW_REGS = 72, HIGH_REGS = 216;
-static_assert(EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS <= (EPI0 + EPI_WARPS) * 168, "registers");
-// 16-bit results leave through shared memory (store_rows), for which the ring has a stage less. Measured, us, single rows
-// from registers and four stages / this: 131072 rows of 64 experts, [2816, 2048] with the gate 724 / 713, [2048, 1408] without
-// 402 / 385; 64 rows an expert of the first 65.6 / 66.5. float32 results, twice as many bytes, stay with four stages.
-constexpr int OUT_BYTES = 4096;         // of a warp
-template <class T>
-constexpr int stages() { return sizeof(T) == 2 ? 3 : 4; }
-template <class T>
-constexpr int dsmem_bytes() { return stages<T>() * STAGE + (sizeof(T) == 2 ? EPI_WARPS * OUT_BYTES : 0) + 1024; }
-constexpr uint32_t TMEM_COLS = 2 * BN;
+
+// Tiles are 128 PARTS rows of w wide, with PARTS epilogue warps per TMEM lane quarter.
+// 16-bit results leave through shared memory (store_rows), for which the wide form's ring has a stage less. Measured, us,
+// single rows from registers and four stages / this: 131072 rows of 64 experts, [2816, 2048] with the gate 724 / 713,
+// [2048, 1408] without 402 / 385; 64 rows an expert of the first 65.6 / 66.5. float32 results, twice as many bytes, stay
+// with four stages.
+template <int PARTS, class T>
+struct Form {
+  static constexpr int BN = W * PARTS;
+  static constexpr int HALF = BN / 2;   // with the gate: gate rows, and as many up rows
+  static constexpr int STAGE = A_BYTES + BN * KB;
+  static constexpr int NSTAGE = PARTS == 1 ? 6 : sizeof(T) == 2 ? 3 : 4;
+  static constexpr int EPI_WARPS = 4 * PARTS;
+  static constexpr int THREADS = (EPI0 + EPI_WARPS) * 32;
+  static constexpr int OUT_BYTES = sizeof(T) == 2 ? 4096 : 0;      // of a warp
+  static constexpr int DSMEM = NSTAGE * STAGE + EPI_WARPS * OUT_BYTES + 1024;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+};
+static_assert(EPI0 * LOW_REGS + 8 * HIGH_REGS <= (EPI0 + 8) * 168, "registers");
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
 struct Params {
@@ -97,11 +101,12 @@ struct Scales {
   float x, g, u0, u1;       // the row's; the columns': all of them, or the gate's, and of the up columns before and after `edge`
 };
 
-template <bool SILU, class T>
-__global__ void __launch_bounds__(THREADS, 1)
+template <bool SILU, class T, int PARTS>
+__global__ void __launch_bounds__(Form<PARTS, T>::THREADS, 1)
     fp8_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmY, const Params P) {
-  constexpr int NSTAGE = stages<T>();
+  using F = Form<PARTS, T>;
+  constexpr int BN = F::BN, HALF = F::HALF, STAGE = F::STAGE, NSTAGE = F::NSTAGE, EPI_WARPS = F::EPI_WARPS;
   __shared__ __align__(8) uint64_t full_bar[NSTAGE], empty_bar[NSTAGE];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     ptx::prefetch_tmap(&tmX);
     ptx::prefetch_tmap(&tmW);
   }
-  if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), TMEM_COLS);
+  if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), F::TMEM_COLS);
   pdl_wait();          // the offsets and operands may be the previous kernel's output
   pdl_trigger();
   if (warp == 2)
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = tmem_slot;
   const int total = G.start[P.E];
 
-  if (warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOW_REGS));
+  if (PARTS == 2 && warp < EPI0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOW_REGS));
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (ptx::elect_one()) {
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= EPI0) {
     // ------------------------------------------------------------ epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(HIGH_REGS));
+    if (PARTS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(HIGH_REGS));
     const int q = warp & 3;              // TMEM lane quarter this warp may read
     const int part = (warp - EPI0) >> 2;    // its columns
     const int row = q * 32 + lane;
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       T* row0 = y + (long)row_y * P.cols;
       auto result = [&](int i) { return SILU ? mx::silu_fast(sum[i]) * sum[(W / 2 + i) % W] : sum[i]; };
       if constexpr (sizeof(T) == 2) {
-        const uint32_t buf = dsmem + NSTAGE * STAGE + (warp - EPI0) * OUT_BYTES;
+        const uint32_t buf = dsmem + NSTAGE * STAGE + (warp - EPI0) * F::OUT_BYTES;
 #pragma unroll
         for (int c = 0; c < (SILU ? W / 2 : W); c += 64) {
           uint32_t v[32];
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, TMEM_COLS);
+    ptx::tmem_dealloc(tmem_base, F::TMEM_COLS);
   }
   if (tid == 0 && P.status) {
     if (abort_flag) atomicOr(P.status, MOE_STATUS_TIMEOUT);
@@ -334,21 +339,22 @@ template <bool SILU, class T>
 bool enough_registers() {
   static const bool enough = [] {
     cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, fp8_tc_kernel<SILU, T>) != cudaSuccess) return false;
-    return at.numRegs * (EPI0 + EPI_WARPS) >= EPI0 * LOW_REGS + EPI_WARPS * HIGH_REGS;
+    if (cudaFuncGetAttributes(&at, fp8_tc_kernel<SILU, T, 2>) != cudaSuccess) return false;
+    return at.numRegs * (EPI0 + 8) >= EPI0 * LOW_REGS + 8 * HIGH_REGS;
   }();
   return enough;
 }
 
-template <bool SILU, class T>
-int launch(const Fp8Args& a, cudaStream_t s) {
+template <bool SILU, class T, int PARTS>
+int launch_form(const Fp8Args& a, cudaStream_t s) {
+  using F = Form<PARTS, T>;
   const char* name = "fp8_grouped_gemm";
-  if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T>, dsmem_bytes<T>(), name)) return rc;
-  if (!enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
+  if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T, PARTS>, F::DSMEM, name)) return rc;
+  if (PARTS == 2 && !enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
   CUtensorMap tx, tw, ty{};
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;
-  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, SILU ? HALF : BN))) return rc;
+  if ((rc = make_tmap_3d(&tw, a.w, 1, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.E, KB, SILU ? F::HALF : F::BN))) return rc;
   Params p{};
   p.offsets = a.offsets;
   p.x_scales = a.x_scales;
@@ -358,7 +364,7 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   p.kb = fp8::blocks(a.K);
   p.nb = fp8::blocks(a.N);
   p.cols = SILU ? a.N / 2 : a.N;
-  p.NT = SILU ? (p.cols + HALF - 1) / HALF : (p.cols + BN - 1) / BN;
+  p.NT = SILU ? (p.cols + F::HALF - 1) / F::HALF : (p.cols + F::BN - 1) / F::BN;
   p.y = a.y;
   p.vec = grouped::store_width(a.y, p.cols, sizeof(T));
   if (sizeof(T) == 2 && p.vec > 0 && (rc = make_tmap_3d(&ty, a.y, 2, (uint64_t)p.cols, (uint64_t)a.S, 1, 64, 32))) return rc;
@@ -367,9 +373,21 @@ int launch(const Fp8Args& a, cudaStream_t s) {
   const long tiles = ((long)(a.S + BM - 1) / BM + a.E) * p.NT;
   const int grid = (int)std::max(1L, std::min(tiles, (long)num_sms()));
   ProfScope ps(name, s);
-  const cudaError_t e = launch_pdl(fp8_tc_kernel<SILU, T>, grid, THREADS, dsmem_bytes<T>(), s, tx, tw, ty, p);
+  const cudaError_t e = launch_pdl(fp8_tc_kernel<SILU, T, PARTS>, grid, F::THREADS, F::DSMEM, s, tx, tw, ty, p);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
   return check_launch(name);
+}
+
+// Tiles of 128 rows of w where all of them find an SM (about: an expert has one tile of rows, or half a tile more than its
+// share): their accumulators come and go faster, and half as much passes through an SM. Measured, us, wide / narrow, K = 2048:
+// 256 rows of 4 experts, [1024, 2048] 10.6 / 8.7, with the gate 11.7 / 9.6, [2816, 2048] 11.4 / 9.8; 1024 rows of 16 experts,
+// [1024, 2048] 13.7 / 11.1; more tiles than SMs: 4096 rows of 16 experts 22.7 / 23.2, 128 rows of 8 experts, [2816, 2048]
+// 14.2 / 16.8, 1024 rows of 64 experts 62 / 69.
+template <bool SILU, class T>
+int launch(const Fp8Args& a, cudaStream_t s) {
+  const int cols = SILU ? a.N / 2 : a.N, width = Form<1, T>::BN / (SILU ? 2 : 1);
+  const long rows = std::max<long>(std::min(a.S, a.E), a.S / BM + a.E / 2);
+  return rows * ((cols + width - 1) / width) <= num_sms() ? launch_form<SILU, T, 1>(a, s) : launch_form<SILU, T, 2>(a, s);
 }
 
 }  // namespace

@@ -287,6 +287,18 @@ def test_product_with_the_gate(dtype, counts, K, N):
     check_product(moe, *operands(counts, K, N, seed=K + N), dtype, True)
 
 
+# more tiles than SMs
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("counts,K,N", [
+    ([20] * 30, 400, 1030), ([129, 0, 257, 3] * 8, 144, 1056), ([300] * 8, 144, 1090), ([10] * 200, 272, 64), ([2000, 2300], 128, 1281)])
+def test_product_of_many_tiles(dtype, silu, counts, K, N):
+    moe = need_gpu()
+    N -= N % 32 if silu else 0          # what the gate takes
+    got = check_product(moe, *operands(counts, K, N, seed=K + N, lead=3, tail=4), dtype, silu)
+    assert not got[:3].any() and not got[-4:].any()
+
+
 # few rows an expert on average, many of one of them
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("silu", [False, True])
@@ -367,7 +379,7 @@ def test_many_experts():
     check_product(moe, *operands([64 if i % 16 == 0 else 32 for i in range(130)], 128, 32), "bf16", True)
 
 
-@pytest.mark.parametrize("counts", [[3, 0, 6], [300, 0, 120]])
+@pytest.mark.parametrize("counts", [[3, 0, 6], [300, 0, 120], [20] * 60])
 def test_a_call_in_a_graph_and_equal_bits(counts):
     moe = need_gpu()
     x, w, off = operands(counts, 512, 320)
@@ -390,10 +402,10 @@ def test_a_call_in_a_graph_and_equal_bits(counts):
 
 
 @pytest.mark.parametrize("silu", [False, True])
-@pytest.mark.parametrize("counts", [[5, 3], [300, 90]])
-def test_a_wait_that_runs_out_is_reported(silu, counts):
+@pytest.mark.parametrize("counts,K", [([5, 3], 4096), ([300, 90], 4096), ([20] * 40, 512)])
+def test_a_wait_that_runs_out_is_reported(silu, counts, K):
     moe = need_gpu()
-    x, w, off = operands(counts, 4096, 512)
+    x, w, off = operands(counts, K, 512)
     args = (*to_gpu(x), *to_gpu(w), torch.from_numpy(off).to(DEV))
     act = "silu_and_mul" if silu else None
     want = moe.moe_fp8_grouped_gemm(*args, activation=act)

@@ -500,8 +500,9 @@ MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, cons
  * d_y and d_weights may be null (it is then not computed; y_sorted is read only
  * for d_weights and may be null without). reverse_indices name distinct slots, as
  * moe_align_by_expert writes them; an entry outside [0, T*k) or an offsets[E]
- * outside it sets MOE_STATUS_BAD_INDEX (the results of the slots concerned are
- * undefined). No atomics on the outputs: equal calls give equal bits.
+ * outside [0, T*k] sets MOE_STATUS_BAD_INDEX (the count is cut to that range, and
+ * a slot that no entry names is like a dropped one). No atomics on the outputs:
+ * equal calls give equal bits.
  * ws / ws_bytes: at least the matching *_workspace_size(T, k) bytes (0 for small
  * calls: then ws may be null); calls that may run at the same time need separate
  * workspaces.

@@ -11,9 +11,9 @@
 // Bound by memory.
 //
 // The inverse comes from a first kernel (a word per slot in the workspace), which writes the slots that have a row and
-// leaves the others as they were: a reader takes an entry p only if reverse[p] is the slot (asked only if some slot was
-// dropped) and p is a routed row, so that whatever else the buffer holds, no index leaves the arrays. With few slots
-// each CTA of the one launch looks through reverse_indices itself instead.
+// leaves the others as they were: a reader takes an entry p only if p is a routed row and reverse[p] is the slot, so
+// that whatever else the buffer holds, no index leaves the arrays and no slot takes another one's row. With few slots each
+// CTA of the one launch looks through reverse_indices itself instead.
 #include <algorithm>
 #include <type_traits>
 
@@ -170,7 +170,7 @@ __device__ __forceinline__ void take_positions(const Args& a, int s0, int count,
   } else {
     for (int i = threadIdx.x; i < count; i += kThreads) {
       int p = __ldcg(a.pos + s0 + i);
-      if (p < 0 || p >= n || (n < S && __ldg(a.reverse + p) != s0 + i)) p = -1;
+      if (p < 0 || p >= n || __ldg(a.reverse + p) != s0 + i) p = -1;
       pos[i] = p;
     }
   }

@@ -481,7 +481,9 @@ MOE_API int moe_ep_receive_index(const int32_t* recv_counts, int G, int E_local,
  *   out[t] = sum_{j<k} topk_weights[t, j] * y_sorted[pos(t*k + j)]
  * where pos inverts reverse_indices (slots the align step dropped add
  * nothing); float32 accumulation in j order, one rounding to dtype (any of the
- * three). Rows of any width. ws / ws_bytes: moe_ep_combine_workspace_size(T, k).
+ * three). Rows of any width. An offsets[E] outside [0, T*k] is cut to it, and an
+ * entry of reverse_indices outside [0, T*k) names no slot. ws / ws_bytes:
+ * moe_ep_combine_workspace_size(T, k).
  */
 MOE_API size_t moe_ep_combine_workspace_size(int T, int k);
 MOE_API int moe_ep_combine(const void* y_sorted, const float* topk_weights, const int32_t* reverse_indices,

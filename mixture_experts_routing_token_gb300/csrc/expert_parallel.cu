@@ -91,12 +91,16 @@ __global__ void __launch_bounds__(256) ep_fill_perm_kernel(const int32_t* __rest
   for (int i = threadIdx.x; i < n; i += blockDim.x) perm[d0 + i] = s0 + i;
 }
 
-// pos[reverse[p]] = p for the routed rows p < offsets[E] (pos was set to -1).
+// pos[reverse[p]] = p for the routed rows p < offsets[E] (pos was set to -1). Both come from the caller: the count is
+// cut to [0, S], and an entry that is no slot is left out, so that whatever the words hold, no index leaves the arrays.
 __global__ void __launch_bounds__(256) ep_invert_kernel(const int32_t* __restrict__ reverse,
-                                                        const int32_t* __restrict__ offsets, int E,
+                                                        const int32_t* __restrict__ offsets, int E, int S,
                                                         int32_t* __restrict__ pos) {
-  const int n = __ldg(offsets + E);
-  for (int p = blockIdx.x * blockDim.x + threadIdx.x; p < n; p += gridDim.x * blockDim.x) pos[__ldg(reverse + p)] = p;
+  const int n = min(max(__ldg(offsets + E), 0), S);
+  for (long p = (long)blockIdx.x * blockDim.x + threadIdx.x; p < n; p += (long)gridDim.x * blockDim.x) {
+    const int s = __ldg(reverse + p);
+    if (s >= 0 && s < S) pos[s] = (int)p;
+  }
 }
 
 template <class T>
@@ -189,7 +193,7 @@ int launch_ep_combine(const void* y, const float* w, const int32_t* reverse, con
   cudaError_t e = cudaMemsetAsync(pos, 0xff, (size_t)S * sizeof(int32_t), s);   // -1: slot not routed
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "ep_combine: %s", cudaGetErrorString(e));
   const int g1 = (int)std::max(1L, std::min((long)num_sms() * 4, (S + 255) / 256));
-  ep_invert_kernel<<<g1, 256, 0, s>>>(reverse, offsets, E, pos);
+  ep_invert_kernel<<<g1, 256, 0, s>>>(reverse, offsets, E, (int)S, pos);
   if (int rc = check_launch("ep_combine")) return rc;
   const int HV = H * esz / 16;
   const long units = (long)T * HV;

@@ -457,6 +457,8 @@ MOE_API int moe_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, 
  * left as they are). hidden [T, H] dtype; sorted_token_ids [T*k] and offsets
  * [E+1] from moe_align_by_expert; x_sorted [T*k, H] dtype (any of the three).
  * Rows of any width; those that are a multiple of 16 bytes are the faster ones.
+ * An offsets[E] outside [0, T*k] is cut to it, and a token id outside [0, T) gives
+ * a row of zeros.
  */
 MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids, const int32_t* offsets,
                             int dtype, int T, int H, int E, int k, void* x_sorted, void* stream);

@@ -809,7 +809,7 @@ MOE_API int moe_gather_rows(const void* hidden, const int32_t* sorted_token_ids,
   if (S == 0) return MOE_OK;
   if ((long)H * (long)dsize(dtype) % 16 != 0 || (long)H * (long)dsize(dtype) >= 1L << 31)
     return launch_gather_any_rows(hidden, sorted_token_ids, offsets, (int)dsize(dtype), T, H, E, (int)S, x_sorted, (cudaStream_t)stream);
-  return launch_gather_rows(hidden, sorted_token_ids, offsets, E, H * (int)dsize(dtype), x_sorted, nullptr,
+  return launch_gather_rows(hidden, sorted_token_ids, offsets, E, T, (int)S, H * (int)dsize(dtype), x_sorted, nullptr,
                             (cudaStream_t)stream);
 }
 

@@ -143,8 +143,9 @@ int make_tmap_3d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols
                  uint32_t box_cols, uint32_t box_rows);
 // [atoms] pieces of 512 bytes (scales of 128 rows x 4); box = box_atoms of them, no swizzle.
 int make_tmap_atoms(CUtensorMap* m, const void* base, uint64_t atoms, uint32_t box_atoms);
-// x_sorted[p] = hidden[sorted_ids[p]] for p < offsets[E] (rows of row_bytes, a multiple of 16).
-int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int row_bytes,
+// x_sorted[p] = hidden[sorted_ids[p]] for p < offsets[E] (rows of row_bytes, a multiple of 16; hidden has T of them,
+// x_sorted S; no such token: zeros).
+int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int T, int S, int row_bytes,
                        void* xs, int32_t* status, cudaStream_t s);
 // Expert-parallel index work (expert_parallel.cu).
 size_t ep_receive_workspace_bytes(int G, int El);

@@ -27,18 +27,19 @@ namespace moe {
 namespace {
 
 // Copies the expert-sorted token rows of `hidden` into x_sorted, the FC1 A operand
-// (16-byte vectors; rows p < offsets[E]).
+// (16-byte vectors; rows p < offsets[E]). The words come from the caller: the count is cut to [0, S], and a token id
+// outside [0, T) gives a row of zeros, so that whatever they hold, no index leaves the arrays.
 __global__ void gather_rows_kernel(const uint4* __restrict__ hidden, const int32_t* __restrict__ ids,
-                                   const int32_t* __restrict__ offsets, int E, int H16, int sh,
+                                   const int32_t* __restrict__ offsets, int E, int T, int S, int H16, int sh,
                                    uint4* __restrict__ xs) {
   pdl_wait();
   pdl_trigger();
-  const int n = __ldg(offsets + E);
+  const int n = min(max(__ldg(offsets + E), 0), S);
   for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < (long)n * H16;
        i += (long)gridDim.x * blockDim.x) {
     const long p = div_idx(i, H16, sh);
-    const int c = (int)(i - p * H16);
-    xs[i] = __ldg(hidden + (long)__ldg(ids + p) * H16 + c);
+    const int c = (int)(i - p * H16), t = __ldg(ids + p);
+    xs[i] = t >= 0 && t < T ? __ldg(hidden + (long)t * H16 + c) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -68,7 +69,7 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 
 __global__ void __launch_bounds__(kBulkWarps * 32) gather_rows_bulk_kernel(
     const uint8_t* __restrict__ hidden, const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets,
-    int E, int row_bytes, int R, uint8_t* __restrict__ xs, int32_t* status) {
+    int E, int T, int S, int row_bytes, int R, uint8_t* __restrict__ xs, int32_t* status) {
   extern __shared__ __align__(128) uint8_t slots[];   // [kBulkWarps][R][row_bytes]
   __shared__ __align__(8) uint64_t bar[kBulkWarps][kBulkMaxR];
   __shared__ int abort_flag;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32) gather_rows_bulk_kernel(
   pdl_trigger();
   if (lane != 0) return;
   volatile int* abort_p = &abort_flag;
-  const int n = __ldg(offsets + E);
+  const int n = min(max(__ldg(offsets + E), 0), S);
   const int nw = gridDim.x * kBulkWarps;
   const uint32_t my = ptx::smem_u32(slots) + (uint32_t)(warp * R * row_bytes);
   uint32_t ph = 0;
@@ -90,8 +91,16 @@ __global__ void __launch_bounds__(kBulkWarps * 32) gather_rows_bulk_kernel(
     const int nr = (int)min((long)R, n - p0);
     for (int r = 0; r < nr; ++r) {
       const uint32_t b = ptx::smem_u32(&bar[warp][r]);
-      ptx::mbar_arrive_expect_tx(b, (uint32_t)row_bytes);
-      bulk_load(my + (uint32_t)(r * row_bytes), hidden + (long)__ldg(ids + p0 + r) * row_bytes, (uint32_t)row_bytes, b);
+      const int t = __ldg(ids + p0 + r);
+      if (t >= 0 && t < T) {
+        ptx::mbar_arrive_expect_tx(b, (uint32_t)row_bytes);
+        bulk_load(my + (uint32_t)(r * row_bytes), hidden + (long)t * row_bytes, (uint32_t)row_bytes, b);
+      } else {                        // no such token: zeros, and a phase without a copy
+        uint4* slot = reinterpret_cast<uint4*>(slots + (size_t)(warp * R + r) * row_bytes);
+        for (int i = 0; i < row_bytes / 16; ++i) slot[i] = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");      // the store below reads them
+        ptx::mbar_arrive_expect_tx(b, 0u);
+      }
     }
     bool ok = true;
     for (int r = 0; r < nr && ok; ++r) ok = ptx::mbar_wait(ptx::smem_u32(&bar[warp][r]), ph, abort_p, kBulkWaitNs);
@@ -210,7 +219,7 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int row_bytes,
+int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int32_t* offsets, int E, int T, int S, int row_bytes,
                        void* xs, int32_t* status, cudaStream_t s) {
   if (row_bytes % 16 != 0) return fail(MOE_ERR_UNSUPPORTED, "gather_rows: rows of %d bytes (need a multiple of 16)", row_bytes);
   ProfScope ps("gather_rows", s);
@@ -219,12 +228,12 @@ int launch_gather_rows(const void* hidden, const int32_t* sorted_ids, const int3
     if (int rc = ensure_smem_limit(gather_rows_bulk_kernel, kBulkSmem, "gather_rows")) return rc;
     const int R = std::min(kBulkMaxR, kBulkRowMax / row_bytes);
     e = launch_pdl(gather_rows_bulk_kernel, num_sms(), kBulkWarps * 32, (size_t)kBulkWarps * R * row_bytes, s,
-                   static_cast<const uint8_t*>(hidden), sorted_ids, offsets, E, row_bytes, R,
+                   static_cast<const uint8_t*>(hidden), sorted_ids, offsets, E, T, S, row_bytes, R,
                    static_cast<uint8_t*>(xs), status);
   } else {
     const int r16 = row_bytes / 16;
     e = launch_pdl(gather_rows_kernel, num_sms() * 4, 256, 0, s, static_cast<const uint4*>(hidden), sorted_ids,
-                   offsets, E, r16, pow2_shift(r16), static_cast<uint4*>(xs));
+                   offsets, E, T, S, r16, pow2_shift(r16), static_cast<uint4*>(xs));
   }
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "gather_rows: %s", cudaGetErrorString(e));
   return check_launch("gather_rows");
@@ -354,7 +363,7 @@ int launch_ffn_tc(const FfnArgs& a, cudaStream_t s) {
                    static_cast<uint8_t*>(a.xs), a.status);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "gather_rows: %s", cudaGetErrorString(e));
     if ((rc = check_launch("gather_rows"))) return rc;
-  } else if ((rc = launch_gather_rows(a.hidden, a.sorted_ids, a.offsets, a.E, row_bytes, a.xs, a.status, s))) {
+  } else if ((rc = launch_gather_rows(a.hidden, a.sorted_ids, a.offsets, a.E, a.T, (int)S, row_bytes, a.xs, a.status, s))) {
     return rc;
   }
   if ((rc = make_tmap(&tA1, a.xs, (uint64_t)S, (uint64_t)a.H, 128))) return rc;

@@ -372,9 +372,10 @@ __global__ void __launch_bounds__(kThreads, !WHOLE ? kCtas : sizeof(T) == 2 ? 3 
   }
 }
 
-// out[p] = src[ids[p]] for the routed rows, rows of any width.
+// out[p] = src[ids[p]] for the routed rows, rows of any width (zeros where there is no such row). With registers for four
+// CTAs an SM: 131072 of 16384 bf16 rows of 2047, us, as many registers as it likes / this: 157 / 142.
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
     gather_any_rows_kernel(const T* __restrict__ src, const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, int E,
                            int rows, int S, int H, T* __restrict__ out) {
   constexpr int V = Piece<T>::V, U = 4;
@@ -383,9 +384,12 @@ __global__ void __launch_bounds__(kThreads)
   const int n = min(max(__ldg(offsets + E), 0), S), lane = threadIdx.x & 31;
   for (long p = (long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; p < n; p += (long)gridDim.x * (kThreads / 32)) {
     const int t = __ldg(ids + p);
-    if (t < 0 || t >= rows) continue;
-    const T* from = src + (long)t * H;
     T* to = out + p * H;
+    if (t < 0 || t >= rows) {
+      for (long i = lane; i < H; i += 32) to[i] = from_float<T>(0.0f);
+      continue;
+    }
+    const T* from = src + (long)t * H;
     for (long i = lane * V - values_before(to); i < H; i += U * 32 * V) {
       Window<T> w[U];
 #pragma unroll

@@ -47,3 +47,28 @@ def test_combine_leaves_out_what_is_no_slot(dtype, T, k, H):
         o = off.copy()
         o[-1] = last
         assert torch.equal(moe.moe_ep_combine(y.to(DEV), w.to(DEV), i32(reverse), i32(o)), want)
+
+
+# bulk copies, 16-byte vectors (rows over 16 KB) and windows, by the rows' bytes
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(6, 2, 64), (6, 2, 33), (700, 3, 4096), (700, 3, 1001), (40, 2, 8192), (9, 2, 16400), (9, 2, 16401)])
+def test_gather_gives_zeros_for_what_is_no_token(dtype, T, k, H):
+    moe = need_gpu()
+    dt, S = TYPES[dtype], T * k
+    hidden = torch.randn(T, H, generator=torch.Generator().manual_seed(H)).to(dt)
+    ids = (np.random.default_rng(T).permutation(S) // k).astype(np.int32)
+    n = S - 2                                # the rows behind are left as they are
+    off = np.array([0, 1, n // 2, n], np.int32)
+    for p, v in ((0, -1), (1, T), (2, LOW), (n // 2, HIGH), (n // 2 + 1, T + 7), (n - 1, -5)):
+        ids[p] = v
+    there = torch.from_numpy((ids >= 0) & (ids < T))
+    want = torch.where(there[:, None], hidden[torch.from_numpy(ids).long().clamp(0, T - 1)], torch.zeros(1, dtype=dt))
+    out = torch.full((S, H), 7.0, dtype=dt, device=DEV)
+    moe.moe_gather_rows(hidden.to(DEV), i32(ids), i32(off), k, out=out)
+    assert torch.equal(out[:n].cpu(), want[:n]) and (out[n:] == 7).all()
+    for last, rows in ((S + 1, S), (HIGH, S), (-1, 0), (LOW, 0)):
+        o = off.copy()
+        o[-1] = last
+        out.fill_(7)
+        moe.moe_gather_rows(hidden.to(DEV), i32(ids), i32(o), k, out=out)
+        assert torch.equal(out[:rows].cpu(), want[:rows]) and (out[rows:] == 7).all()

@@ -694,11 +694,15 @@ def moe_gather_rows(hidden, sorted_token_ids, offsets, k, out=None, stream=None)
     _dev(hidden, "hidden")
     dt = _code(hidden.dtype)
     T, H = hidden.shape
-    E = offsets.numel() - 1
     d = hidden.device
+    ids = _take(sorted_token_ids, "sorted_token_ids", _I32, d.index)
+    offs = _take(offsets, "offsets", _I32, d.index)
+    E = offsets.numel() - 1
+    _fits(T, H, T * k)
+    if sorted_token_ids.numel() < T * k:
+        raise ValueError(f"sorted_token_ids must hold T * k = {T * k} ids (got {sorted_token_ids.numel()})")
     out = _out(out, (T * k, H), hidden.dtype, d, "out", stream)
-    _check("moe_gather_rows", lib().moe_gather_rows(
-        _ptr(hidden), _ptr(sorted_token_ids), _ptr(offsets), dt, T, H, E, k, _ptr(out), _stream(stream, d)))
+    _check("moe_gather_rows", lib().moe_gather_rows(_ptr(hidden), ids, offs, dt, T, H, E, k, _ptr(out), _stream(stream, d)))
     return out
 
 
@@ -725,16 +729,23 @@ def moe_ep_combine(y_sorted, topk_weights, reverse_indices, offsets, out=None, w
     """Sender side after the return exchange: out[t] = sum_j w[t,j] * y_sorted[pos(t, j)] -> [T, H]."""
     _dev(y_sorted, "y_sorted")
     dt = _code(y_sorted.dtype)
+    d = y_sorted.device
+    weights = _take(topk_weights, "topk_weights", _F32, d.index)
+    reverse = _take(reverse_indices, "reverse_indices", _I32, d.index)
+    offs = _take(offsets, "offsets", _I32, d.index)
     T, k = topk_weights.shape
     H = y_sorted.shape[1]
     E = offsets.numel() - 1
-    d = y_sorted.device
+    _fits(T * k, H)
+    if y_sorted.shape[0] < T * k or reverse_indices.numel() < T * k:
+        raise ValueError(f"y_sorted and reverse_indices must hold T * k = {T * k} rows "
+                         f"(got {y_sorted.shape[0]} and {reverse_indices.numel()})")
     out = _out(out, (T, H), y_sorted.dtype, d, "out", stream)
     need = int(lib().moe_ep_combine_workspace_size(T, k))
     if workspace is None:
         workspace = _new(max(need, 1), torch.uint8, d.index, stream)
     _check("moe_ep_combine", lib().moe_ep_combine(
-        _ptr(y_sorted), _ptr(topk_weights), _ptr(reverse_indices), _ptr(offsets), dt, T, k, H, E, _ptr(out),
+        _ptr(y_sorted), weights, reverse, offs, dt, T, k, H, E, _ptr(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, d)))
     return out
 

@@ -197,12 +197,13 @@ struct NormArgs {
 };
 
 // h = x + residual, rounded to T as the stream keeps it; n = h / sqrt(mean of h^2 + eps) * weight in float32.
+// The sum may be written over either of them and the normed rows over x, so both come by ordinary loads.
 template <class T>
 __device__ __forceinline__ void take8(const NormArgs& a, long at, float (&h)[8]) {
-  load8(static_cast<const T*>(a.x) + at, h);
+  load8<true>(static_cast<const T*>(a.x) + at, h);
   if (a.residual != nullptr) {
     float r[8];
-    load8(static_cast<const T*>(a.residual) + at, r);
+    load8<true>(static_cast<const T*>(a.residual) + at, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = to_float(from_float<T>(h[j] + r[j]));
   }

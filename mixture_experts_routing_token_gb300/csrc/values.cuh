@@ -4,13 +4,22 @@
 
 namespace moe {
 
+// 16 bytes of memory that the kernel may write as well (SAME), or that nobody writes while it runs (the read-only path).
+template <bool SAME, class V>
+__device__ __forceinline__ V load16b(const V* p) {
+  if constexpr (SAME) return *p;
+  else return __ldg(p);
+}
+
+template <bool SAME = false>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = load16b<SAME>(reinterpret_cast<const float4*>(p)), b = load16b<SAME>(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+template <bool SAME = false>
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 q = load16b<SAME>(reinterpret_cast<const uint4*>(p));
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -18,8 +27,9 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+template <bool SAME = false>
 __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 q = load16b<SAME>(reinterpret_cast<const uint4*>(p));
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -398,7 +398,7 @@ template <class T, int G, int V>
 int norm_as(const NormArgs& a, cudaStream_t s) {
   const char* name = "rms_norm_fp8";
   ProfScope ps(name, s);
-  return done(launch_pdl(rms_norm_fp8_kernel<T, G, V>, (unsigned)((a.T + 256 / G - 1) / (256 / G)), 256, 0, s, a), name);
+  return done(launch_pdl(rms_norm_fp8_kernel<T, G, V>, (unsigned)(((long)a.T + 256 / G - 1) / (256 / G)), 256, 0, s, a), name);
 }
 
 template <class T>

@@ -431,6 +431,9 @@ int positions(Args& a, cudaStream_t s) {
   return done(launch_pdl(slot_positions_kernel, grid, kThreads, 0, s, a), "slot_positions");
 }
 
+// CTAs of `tokens` each (a power of two); T may be the largest int.
+unsigned ctas(int T, int tokens) { return (unsigned)(((long)T + tokens - 1) / tokens); }
+
 // Threads of a token, a power of two: no more than it has pieces, and no more than give every SM five CTAs.
 int threads_per_token(int pieces, int T) {
   int g = kMinGroup;
@@ -450,7 +453,7 @@ template <class T, bool WHOLE, int K>
 int sum_as(const Args& a, const void* src, void* out, const char* name, cudaStream_t s) {
   const int G = threads_per_token(pieces_of<T, WHOLE>(a.H), a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
+  return done(launch_pdl(sum_rows_kernel<T, WHOLE, K>, ctas(a.T, tokens), kThreads, 0, s, a,
                          static_cast<const T*>(src), static_cast<T*>(out), G),
               name);
 }
@@ -466,7 +469,7 @@ int sum_backward_as(const Args& a, const void* d_out, const void* y, void* d_y, 
   const char* name = "ep_combine_backward";
   const int G = threads_per_token(pieces_of<T, WHOLE>(a.H), a.T), tokens = kThreads / G;
   ProfScope ps(name, s);
-  return done(launch_pdl(sum_rows_backward_kernel<T, WHOLE, K>, (unsigned)((a.T + tokens - 1) / tokens), kThreads, 0, s, a,
+  return done(launch_pdl(sum_rows_backward_kernel<T, WHOLE, K>, ctas(a.T, tokens), kThreads, 0, s, a,
                          static_cast<const T*>(d_out), static_cast<const T*>(y), static_cast<T*>(d_y), d_w, G),
               name);
 }

@@ -8,6 +8,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -36,6 +38,29 @@ template <typename... KArgs>
 int ensure_smem_limit(void (*kernel)(KArgs...), size_t bytes, const char* name) {
   return ensure_smem_limit(reinterpret_cast<const void*>(kernel), bytes, name);
 }
+
+// Registers that a kernel is built with, for launches that hand them from warp to warp. The runtime is asked until it has
+// answered once; a query that fails is that call's error only.
+struct BuiltRegisters {
+  std::atomic<int> per_thread{0};      // 0: not known yet
+  // Whether `warps` warps' registers come to `need` (of 32 threads) or more.
+  int check(const void* kernel, int warps, int need, const char* name) {
+    int n = per_thread.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaFuncAttributes at;
+      const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: registers of the kernel: %s", name, cudaGetErrorString(e));
+      n = at.numRegs;
+      per_thread.store(n, std::memory_order_relaxed);
+    }
+    if (n * warps < need) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread (%d)", name, n);
+    return MOE_OK;
+  }
+  template <typename... KArgs>
+  int check(void (*kernel)(KArgs...), int warps, int need, const char* name) {
+    return check(reinterpret_cast<const void*>(kernel), warps, need, name);
+  }
+};
 
 // Row of a flat grid-stride index: i / d for d > 0. A shift when d is a power of
 // two (sh = log2(d), from pow2_shift on the host), else an unsigned 32-bit

@@ -333,24 +333,17 @@ __global__ void __launch_bounds__(Form<PARTS, T>::THREADS, 1)
   }
 }
 
-// The epilogue's warps wait for the registers that they ask for, so a block has to start with as many as the split needs
-// in all: with the register limit of its launch bounds, which a kernel that moves registers is compiled for. Asked once.
-template <bool SILU, class T>
-bool enough_registers() {
-  static const bool enough = [] {
-    cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, fp8_tc_kernel<SILU, T, 2>) != cudaSuccess) return false;
-    return at.numRegs * (EPI0 + 8) >= EPI0 * LOW_REGS + 8 * HIGH_REGS;
-  }();
-  return enough;
-}
-
 template <bool SILU, class T, int PARTS>
 int launch_form(const Fp8Args& a, cudaStream_t s) {
   using F = Form<PARTS, T>;
   const char* name = "fp8_grouped_gemm";
   if (int rc = ensure_smem_limit(fp8_tc_kernel<SILU, T, PARTS>, F::DSMEM, name)) return rc;
-  if (PARTS == 2 && !enough_registers<SILU, T>()) return fail(MOE_ERR_CUDA, "%s: built with too few registers a thread", name);
+  // The epilogue's warps wait for the registers that they ask for, so a block has to start with as many as the split needs
+  // in all: with the register limit of its launch bounds, which a kernel that moves registers is compiled for.
+  if (PARTS == 2) {
+    static BuiltRegisters built;
+    if (int rc = built.check(fp8_tc_kernel<SILU, T, PARTS>, EPI0 + 8, EPI0 * LOW_REGS + 8 * HIGH_REGS, name)) return rc;
+  }
   CUtensorMap tx, tw, ty{};
   int rc;
   if ((rc = make_tmap_3d(&tx, a.x, 1, (uint64_t)a.K, (uint64_t)a.S, 1, KB, BM))) return rc;

@@ -393,7 +393,8 @@ MOE_API int moe_fp8_dequantize(const uint8_t* codes, const float* scales, int M,
  *   h = x + residual, rounded to dtype (h = x without one);
  *   n = h * (1 / sqrt(mean over the row of h^2 + eps)) * weight  in float32;
  *   codes, scales: n as moe_fp8_quantize with block_rows 1.
- *   x, residual [T, H], weight [H] of dtype, H % 16 == 0, eps >= 0;
+ *   x, residual [T, H], weight [H] of dtype, H % 16 == 0, eps >= 0; the sum of
+ *   h^2 is float32: a row with values beyond 1.8e19 has an infinite one, and n = 0;
  *   codes [T, H] bytes, scales [T, ceil(H / 128)] float32;
  *   residual_out [T, H] = h: given if and only if residual is; it may be the
  *   residual itself or x;
@@ -418,16 +419,20 @@ MOE_API int moe_fp8_gather_rows(const uint8_t* codes, const float* scales, const
 /*
  * moe_grouped_gemm on such operands (K % 16 == 0):
  *   x_codes [S, K], x_scales [S, ceil(K / 128)]; w_codes [E, N, K],
- *   w_scales [E, ceil(N / 128), ceil(K / 128)] (any float32 scales);
+ *   w_scales [E, ceil(N / 128), ceil(K / 128)] (float32, not only powers of two;
+ *   the product of a row's scale and a matrix' one is formed first and should be
+ *   a normal number: one that overflows makes NaN of a block whose sum is 0, a
+ *   subnormal one is rounded to its few bits);
  *   y[p, n] = sum over blocks b of x_scales[p, b] w_scales[e, n / 128, b]
  *             * (sum over the k in b of x w), sums in float32.
  *   activation MOE_ACT_NONE: y [S, N]; MOE_ACT_SILU_AND_MUL (N / 2 a multiple
  *   of 16, as the next product's K): y [S, N / 2] = silu(columns 0 .. N/2 - 1) *
- *   (columns N/2 .. N - 1) (silu of arguments below -87 is 0). y is of out_dtype
- *   (any of the three), rounded once.
+ *   (columns N/2 .. N - 1). silu(z) has a fast exponential and division whatever
+ *   out_dtype is: with float32 results the product of the two is off by up to
+ *   (6 + 1.2 |z|) 2^-23 of itself, and silu of arguments below -87 is 0. y is of
+ *   out_dtype (any of the three), rounded once.
  * Within a block the tensor cores add with truncation; the blocks' sums are scaled
- * by the product of their two scales (formed first, in float32: it should be a
- * normal number) and added rounded to nearest. offsets, rows without an expert and status as
+ * by the product of their two scales and added rounded to nearest. offsets, rows without an expert and status as
  * moe_grouped_gemm. No workspace.
  */
 MOE_API int moe_fp8_grouped_gemm(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes,

@@ -969,7 +969,7 @@ def moe_fp8_grouped_gemm(x_codes, x_scales, w_codes, w_scales, offsets, activati
     ``x_codes [S, K]`` with ``x_scales [S, ceil(K/128)]``, ``w_codes [E, N, K]`` with
     ``w_scales [E, ceil(N/128), ceil(K/128)]`` as :func:`moe_fp8_quantize` makes them (``block_rows`` 1 and 128), K a
     multiple of 16. ``activation="silu_and_mul"`` returns [S, N/2]: silu of the first half of the columns times the
-    second half (N a multiple of 32)."""
+    second half (N a multiple of 32); its exponential and division are the fast ones for float32 results, too."""
     xp, dtype, d = _first(x_codes, "x_codes")
     if dtype is not _F8:
         _refuse(x_codes, "x_codes", _F8, d)

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(256) rms_norm_fp8_wide_kernel(const NormArgs a
 // ---- 8-bit rows into expert order ---------------------------------------------------------------
 
 // 16 bytes of codes per thread, and the scale of the block that starts there. A CTA takes 1024 neighbouring pieces a turn,
-// whose loads are under way together, and what it writes is one stretch of memory: 131072 rows of 2048, 284 MB, 61 us (4.6
+// whose loads are under way together, and what it writes is one stretch of memory: 131072 rows of 2048, 277 MB, 60 us (4.6
 // TB/s written; filling the same memory takes 75); with pieces a grid apart 90, with a CTA for each turn 74.
 __global__ void __launch_bounds__(256)
     fp8_gather_kernel(const uint4* __restrict__ src, const float* __restrict__ src_scales, int T, int units, int sh, int kb,

@@ -16,10 +16,11 @@
 // tile: us, SM pairs / this, 131072 rows of 64 experts, [2816, 2048] with the gate 731 / 712, [2048, 1408] without
 // 394 / 380; 64 rows an expert 96 / 66.
 //
-// Bound at prompt sizes by the way of an accumulator: four MMAs (512 cycles), their commit, the read and the sums (356
-// cycles), the hand-back, the next issue. Tensor memory holds two, so a block takes about half of that round trip, 1100
-// to 1200 cycles. 131072 rows, 64 experts of [2816, 2048] with the gate: 670 us on a cold GPU (2.26 PFLOP/s), 700 to 715
-// in a long run. At 64 rows an expert it is HBM: 66 us, 5.8 TB/s.
+// 131072 rows, 64 experts of [2816, 2048] with the gate: 670 us on a cold GPU (2.26 PFLOP/s), 700 to 715 in a long run, which
+// is 1,110 cycles a block of an SM. None of what was measured by itself takes as long: the four MMAs 512, the reads and sums
+// 356, the operands' intake 730, half of an accumulator's way round (of which tensor memory holds two: MMAs until the
+// epilogue knows, read and sums, hand-back, next issue) 700 to 770. Where the other 340 go is not known; without most of the
+// sums and the scales' loads the time is a seventh less. At 64 rows an expert it is HBM: 66 us, 5.8 TB/s.
 #include <algorithm>
 
 #include "fp8.cuh"

@@ -25,11 +25,14 @@ namespace {
 constexpr int kThreads = 256;
 // Loads of sorted rows that a thread has under way: of 2, 4 or 8 slots (K), the least that are k or more. Measured, us, both
 // gradients with 8 / 4 / 2 slots at a time, bf16 rows of 2048: k = 8, 8192 tokens 158 / 160 / 162 (500 tokens of 512 values
-// 10.8 / 11.7 / 14.0), k = 4, 16384 tokens 185 / 153 / 161, k = 3, 8192 tokens 89 / 72 / 77.
+// 10.8 / 11.7 / 14.0), k = 4, 16384 tokens 185 / 153 / 161, k = 3, 8192 tokens 89 / 72 / 77 (before every slot's entry was
+// looked up in reverse_indices again, which made 157, 158 and 74 of 155, 155 and 73).
 constexpr int kFlight = 8;
 // Whether the CTAs look for their slots themselves. Measured, us, both gradients of bf16 rows of 512, from Python / in a
 // graph, with the first kernel and its workspace, and without: 4000 slots of 500 tokens 26.5 / 11.7 and 13.5 / 10.7, 8000
-// slots of 1000 tokens 27.5 / 12.4 and 14.3 / 14.8, of 8000 tokens 27.2 / 22.2 and 30.5 / 31.2.
+// slots of 1000 tokens 27.5 / 12.4 and 14.3 / 14.8, of 8000 tokens 27.2 / 22.2 and 30.5 / 31.2. At the rule's upper end,
+// with / without: 8 slots of 1025 / 1024 tokens 26 / 12.3 and 16 / 15.4, 4 of 2049 / 2048 25 / 15.3 and 21 / 20.3, 1 of 2049 /
+// 2048 25 / 11.7 and 13 / 10.3: chosen for calls from Python; in a graph the first kernel is the faster one there.
 bool each_looks(int T, int k) { return (long)T * k <= 2048 || ((long)T * k <= 8192 && T <= 2048); }
 // Rows in windows: two slots at a time, a piece each, in registers for four CTAs an SM. Measured, us, 8192 tokens x 8 of 2047
 // bf16 values, combine backward / gather backward: 151 / 83; with five CTAs 222 / 93, four slots and three CTAs 167 / 90,
